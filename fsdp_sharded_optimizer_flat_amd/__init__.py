@@ -40,6 +40,8 @@ ZERO_LAYOUT_MAGIC = 0x5A45524F
 ZERO_ABI_VERSION = 2
 ZERO_NOALLOC_SCRATCH_BYTES = 16 << 20
 ZERO_CAP_STEP, ZERO_CAP_STEP1, ZERO_CAP_NORM = 0, 1, 2
+ZERO_MAX_VOCAB, ZERO_MAX_TOP, ZERO_MAX_LOSS_ROWS = 1 << 20, 256, 0x7FFFFFFF
+ZERO_DISTILL_RENORM, ZERO_DISTILL_TAIL = 0, 1
 
 i32, i64, f32, f64, vp, sz = C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_void_p, C.c_size_t
 
@@ -163,6 +165,19 @@ _zero_ckpt_load = _sig("zero_ckpt_load", i32, vp, i32, vp, i32, i32, C.POINTER(i
 _zero_set_waves_per_cu = _sig("zero_set_waves_per_cu", i32, i32, i32)
 _zero_get_waves_per_cu = _sig("zero_get_waves_per_cu", i32, i32, i32, C.POINTER(i32))
 _zero_get_waves_per_cu_for = _sig("zero_get_waves_per_cu_for", i32, i32, i32, i32, i32, C.POINTER(i32))
+_zero_loss_workspace_bytes = _sig("zero_loss_workspace_bytes", i32, i64, i64, i32, C.POINTER(sz))
+_zero_logprob = _sig("zero_logprob", i32, vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, i32, vp, vp, vp,
+                     sz, vp)
+_zero_logprob_grad = _sig("zero_logprob_grad", i32, vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, vp,
+                          vp, i64, vp)
+_zero_logprob_fused = _sig("zero_logprob_fused", i32, vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, vp,
+                           vp, i64, vp, sz, vp)
+_zero_distill = _sig("zero_distill", i32, vp, i32, i64, i64, i64, f32, i32, vp, vp, i32, vp, vp, vp, sz,
+                     vp)
+_zero_distill_grad = _sig("zero_distill_grad", i32, vp, i32, i64, i64, i64, f32, i32, vp, vp, i32, vp,
+                          vp, vp, i64, vp)
+_zero_distill_fused = _sig("zero_distill_fused", i32, vp, i32, i64, i64, i64, f32, i32, vp, vp, i32,
+                           vp, vp, vp, i64, vp, sz, vp)
 _zero_strerror = _sig("zero_strerror", C.c_char_p, i32)
 _zero_last_hip_error = _sig("zero_last_hip_error", C.c_char_p)
 _zero_abi_version = _sig("zero_abi_version", i32)
@@ -180,6 +195,8 @@ EXPORTED = ["zero_layout_bytes", "zero_pack", "zero_pack_rows", "zero_reshard",
             "zero_gather_buffer_bytes", "zero_arena_plan", "zero_step_traffic",
             "zero_gradnorm_traffic", "zero_ckpt_save", "zero_ckpt_inspect", "zero_ckpt_load",
             "zero_set_waves_per_cu", "zero_get_waves_per_cu", "zero_get_waves_per_cu_for",
+            "zero_loss_workspace_bytes", "zero_logprob", "zero_logprob_grad", "zero_logprob_fused",
+            "zero_distill", "zero_distill_grad", "zero_distill_fused",
             "zero_strerror", "zero_last_hip_error", "zero_abi_version"]
 
 
@@ -839,6 +856,182 @@ def zero_gradnorm_traffic(layout: Layout, rank: int, n_grads: int, grad_dtype: i
     _check(_zero_gradnorm_traffic(layout.ptr, rank, n_grads, grad_dtype, int(with_g_out),
                                   C.byref(b), C.byref(e)), "zero_gradnorm_traffic")
     return b.value, e.value
+
+
+# -- token losses ---------------------------------------------------------------------------
+
+def zero_loss_workspace_bytes(rows: int, vocab: int, top_k: int = 0) -> int:
+    """Bytes of a workspace (a device tensor) that is enough for every
+    token-loss call on ``rows`` rows of ``vocab`` logits."""
+    b = sz()
+    _check(_zero_loss_workspace_bytes(rows, vocab, top_k, C.byref(b)), "zero_loss_workspace_bytes")
+    return b.value
+
+
+def _on_device(t, dev, what: str):
+    if t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, the logits on {dev}")
+
+
+def _rows_of(t, what: str):
+    """(address, row stride) of a 2-D device tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions (rows, vocab)")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor (got {t.device})")
+    n, v = t.shape
+    if v > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else max(v, 1)
+
+
+def _logits(t):
+    """(address, dtype, rows, vocab, row stride, device) of the logits, which
+    must be on the current device (the calls run on its streams)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("logits must be a torch tensor")
+    ptr, stride = _rows_of(t, "logits")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"logits are on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    dt = ZERO_BF16 if t.dtype == torch.bfloat16 else ZERO_F32 if t.dtype == torch.float32 else None
+    if dt is None:
+        raise TypeError(f"logits must be bfloat16 or float32, got {t.dtype}")
+    return ptr, dt, t.shape[0], t.shape[1], stride, t.device
+
+
+def _row_values(t, n: int, dev, what: str, dtype=None):
+    """Address of a contiguous device tensor of exactly n values (None: NULL)."""
+    if t is None:
+        return None
+    torch = _torch()
+    if t.dtype != (dtype or torch.float32):
+        raise TypeError(f"{what} must be {dtype or torch.float32}, got {t.dtype}")
+    ptr = _dev_ptr(t, what)
+    if t.numel() != n:
+        raise ValueError(f"{what} holds {t.numel()} values; the call needs {n}")
+    _on_device(t, dev, what)
+    return ptr
+
+
+def _d_logits(t, logits):
+    if t.dtype != logits.dtype or t.shape != logits.shape:
+        raise ValueError("d_logits must have the logits' shape and dtype")
+    ptr, stride = _rows_of(t, "d_logits")
+    _on_device(t, logits.device, "d_logits")
+    return ptr, stride
+
+
+def _workspace(t, dev):
+    if t is None:
+        return None, 0
+    ptr = _dev_ptr(t, "workspace")
+    _on_device(t, dev, "workspace")
+    return ptr, t.numel() * t.element_size()
+
+
+def _top(index, value, rows: int, dev, what):
+    """(top_k, index address, value address) of (rows, top_k) tensors."""
+    if index is None and value is None:
+        return 0, None, None
+    if index is None or value is None:
+        raise ValueError(f"{what[0]} and {what[1]} go together")
+    if index.dim() != 2 or index.shape != value.shape or index.shape[0] != rows:
+        raise ValueError(f"{what[0]} and {what[1]} must have shape (rows, top_k)")
+    n = index.numel()
+    return (index.shape[1], _row_values(index, n, dev, what[0], _torch().int32),
+            _row_values(value, n, dev, what[1]))
+
+
+def zero_logprob(logits, tokens=None, *, scale: float = 1.0, logprob=None, entropy=None, stats=None,
+                 top_index=None, top_logprob=None, workspace=None, stream=None):
+    """Enqueue the log probabilities of the given tokens (int64; negative: a
+    padding row), each row's entropy, its statistics for the backward call
+    (rows, 2) and its top alternatives (rows, top_k); outputs left None are
+    not computed.  ``workspace``: at least zero_loss_workspace_bytes."""
+    p, dt, n, v, st, dev = _logits(logits)
+    k, ip, tp = _top(top_index, top_logprob, n, dev, ("top_index", "top_logprob"))
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_logprob(p, dt, n, v, st, scale, _row_values(tokens, n, dev, "tokens", _torch().int64),
+                         _row_values(logprob, n, dev, "logprob"),
+                         _row_values(entropy, n, dev, "entropy"),
+                         _row_values(stats, 2 * n, dev, "stats"), k, ip, tp, wp, wb, _stream(stream)),
+           "zero_logprob")
+
+
+def zero_logprob_grad(logits, tokens, stats, d_logits, *, scale: float = 1.0, d_logprob=None,
+                      d_entropy=None, entropy=None, stream=None):
+    """Enqueue the backward pass: ``d_logits`` (which may be ``logits``) from
+    the upstream gradients ``d_logprob`` and ``d_entropy``, the forward call's
+    ``stats`` and, with ``d_entropy``, its ``entropy``."""
+    p, dt, n, v, st, dev = _logits(logits)
+    gp, gs = _d_logits(d_logits, logits)
+    _check(_zero_logprob_grad(p, dt, n, v, st, scale,
+                              _row_values(tokens, n, dev, "tokens", _torch().int64),
+                              _row_values(stats, 2 * n, dev, "stats"),
+                              _row_values(entropy, n, dev, "entropy"),
+                              _row_values(d_logprob, n, dev, "d_logprob"),
+                              _row_values(d_entropy, n, dev, "d_entropy"), gp, gs, _stream(stream)),
+           "zero_logprob_grad")
+
+
+def zero_logprob_fused(logits, tokens, d_logits, *, scale: float = 1.0, d_logprob=None,
+                       d_entropy=None, logprob=None, entropy=None, workspace=None, stream=None):
+    """Enqueue forward and backward in one call.  The mean language-model loss
+    over n tokens is ``-logprob.sum() / n`` with ``d_logprob = -1 / n``."""
+    p, dt, n, v, st, dev = _logits(logits)
+    gp, gs = _d_logits(d_logits, logits)
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_logprob_fused(p, dt, n, v, st, scale,
+                               _row_values(tokens, n, dev, "tokens", _torch().int64),
+                               _row_values(d_logprob, n, dev, "d_logprob"),
+                               _row_values(d_entropy, n, dev, "d_entropy"),
+                               _row_values(logprob, n, dev, "logprob"),
+                               _row_values(entropy, n, dev, "entropy"), gp, gs, wp, wb,
+                               _stream(stream)), "zero_logprob_fused")
+
+
+_RECORD = ("top_index", "top_value")
+
+
+def zero_distill(logits, top_index, top_value, mode: int, *, scale: float = 1.0, loss=None,
+                 stats=None, workspace=None, stream=None):
+    """Enqueue the distillation loss of each row against the teacher's record
+    (``top_index`` int32, ``top_value`` float32, both (rows, top_k)) and the
+    row statistics (rows, 4) for the backward call."""
+    p, dt, n, v, st, dev = _logits(logits)
+    k, ip, tp = _top(top_index, top_value, n, dev, _RECORD)
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_distill(p, dt, n, v, st, scale, k, ip, tp, mode, _row_values(loss, n, dev, "loss"),
+                         _row_values(stats, 4 * n, dev, "stats"), wp, wb, _stream(stream)),
+           "zero_distill")
+
+
+def zero_distill_grad(logits, top_index, top_value, mode: int, stats, d_loss, d_logits, *,
+                      scale: float = 1.0, stream=None):
+    """Enqueue the backward pass: ``d_logits`` (which may be ``logits``) from
+    the upstream gradient ``d_loss`` and the forward call's ``stats``."""
+    p, dt, n, v, st, dev = _logits(logits)
+    k, ip, tp = _top(top_index, top_value, n, dev, _RECORD)
+    gp, gs = _d_logits(d_logits, logits)
+    _check(_zero_distill_grad(p, dt, n, v, st, scale, k, ip, tp, mode,
+                              _row_values(stats, 4 * n, dev, "stats"),
+                              _row_values(d_loss, n, dev, "d_loss"), gp, gs, _stream(stream)),
+           "zero_distill_grad")
+
+
+def zero_distill_fused(logits, top_index, top_value, mode: int, d_loss, d_logits, *,
+                       scale: float = 1.0, loss=None, workspace=None, stream=None):
+    """Enqueue forward and backward in one call."""
+    p, dt, n, v, st, dev = _logits(logits)
+    k, ip, tp = _top(top_index, top_value, n, dev, _RECORD)
+    gp, gs = _d_logits(d_logits, logits)
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_distill_fused(p, dt, n, v, st, scale, k, ip, tp, mode,
+                               _row_values(d_loss, n, dev, "d_loss"),
+                               _row_values(loss, n, dev, "loss"), gp, gs, wp, wb, _stream(stream)),
+           "zero_distill_fused")
 
 
 # -- sharded checkpoint ---------------------------------------------------------------------

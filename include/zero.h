@@ -542,6 +542,141 @@ zero_status zero_clip_coef_ranks_async(const double *rank_sums_dev, int32_t n_ra
                                        void *stream);
 
 /* ------------------------------------------------------------------------
+ * Token losses -- where the gradients the step reduces begin.  [p1 How it
+ * works]: backward produces each unit's gradients, last unit first; the first
+ * of them is the gradient of a loss over the vocabulary.  Two losses over rows
+ * of logits l (one row per token), each as the forward pass, the backward pass
+ * from the forward's row statistics, and both in one call.
+ *
+ * With x_j = scale * l_j (scale: the inverse temperature), p = softmax(x):
+ *
+ *   log probabilities of given tokens
+ *     logprob = ln p_t             t the row's given token
+ *     entropy = -sum_j p_j ln p_j
+ *     top     = the top_k largest logits, largest first, ties to the lowest index
+ *     d_logits_j = scale * (d_logprob * ([j = t] - p_j)
+ *                           - d_entropy * p_j * (ln p_j + entropy))
+ *     The language-model loss of a row is -logprob: d_logprob = -1 / tokens.
+ *
+ *   distillation from a teacher's top logits (KL divergence of the student's
+ *   distribution p from the teacher's q, known on the tokens it lists)
+ *     ZERO_DISTILL_RENORM  q = softmax of the listed values
+ *     ZERO_DISTILL_TAIL    q_k = exp(value_k) and one bucket for all other
+ *                          tokens, q_rest = 1 - sum_k q_k (taken as 0 below
+ *                          2^-20, the rounding of binary32 log probabilities,
+ *                          and where the record lists the whole vocabulary)
+ *     loss = sum_k q_k (ln q_k - ln p_{i_k}) + q_rest (ln q_rest - ln p_rest)
+ *     d_logits_j = d_loss * scale * (Q p_j - q_j)                   listed
+ *                  d_loss * scale * (Q - q_rest / p_rest) p_j       not listed
+ *     with Q = sum_k q_k + q_rest and p_rest the other tokens' probability.
+ *     Terms with q = 0 add nothing.  A token named by several entries counts
+ *     once in p and with each of its entries in q.
+ *
+ * Logits: `rows` rows of `vocab` elements of `dtype` (ZERO_F32 / ZERO_BF16),
+ * row r at logits + r * row_stride; 1 <= vocab <= ZERO_MAX_VOCAB, row_stride >=
+ * vocab.  A logit of -inf has probability zero.  Sums are held in binary32
+ * (listed tokens and the teacher's q in binary64), in a fixed order: the same
+ * call gives the same bits.  d_logits has the logits' dtype (each element
+ * rounded once) and its own row stride; elements past a row's vocab are left as
+ * they are.  It may be the logits themselves (same pointer and stride): each
+ * row is then read before it is written.  2^-20 <= scale <= 2^20.
+ *
+ * Rows that have no distribution, or no target:
+ *   - a negative token, or a teacher's record of negative indices only (and no
+ *     NaN value), marks a padding row: it is not read, its outputs and its gradient are zero, and
+ *     its top alternatives index -1, log probability -inf;
+ *   - upstream weights of zero give a zero gradient, whatever the row holds;
+ *   - a row whose logits are all -inf: logprob -inf, entropy 0, a loss of
+ *     +inf, no alternatives, gradient zero;
+ *   - a row with a NaN or +inf logit: NaN everywhere (alternatives index -1);
+ *   - a token, or an index of a teacher's record, >= vocab, or a NaN value in
+ *     the record: logprob, loss and the gradient row are NaN.  A NaN gradient has no clip coefficient, so
+ *     zero_step_device_clip skips its step.
+ * Alternatives past the row's finite logits have index -1, log probability
+ * -inf.
+ *
+ * All pointers are device pointers, tokens 8-byte aligned, indices and floats
+ * 4-byte aligned.  Outputs must not overlap each other or an input (d_logits
+ * over logits excepted).  Async on `stream`; nothing is allocated and the calls
+ * can be captured in a graph.  A workspace serves one call at a time: calls
+ * that may overlap (other streams, other graphs) need workspaces of their own.
+ * Errors: EINVAL (NULL, negative sizes, bad enum, vocab < 1, stride < vocab,
+ * scale not positive and finite, overlapping buffers), ERANGE (vocab, rows,
+ * top_k or scale out of range), EALIGN, ENOSPC (workspace too small), EHIP.
+ * rows = 0 does nothing.
+ * ------------------------------------------------------------------------ */
+#define ZERO_MAX_VOCAB (1 << 20)
+#define ZERO_MAX_TOP 256              /* most alternatives, most listed tokens per row */
+#define ZERO_MAX_LOSS_ROWS 0x7fffffff
+#define ZERO_DISTILL_RENORM 0
+#define ZERO_DISTILL_TAIL 1
+
+/* Workspace bytes that are enough for each of the calls below on `rows` rows of
+ * `vocab` logits (top_k alternatives for zero_logprob; 16-byte aligned device
+ * memory).  Where it is 0 the workspace may be NULL. */
+zero_status zero_loss_workspace_bytes(int64_t rows, int64_t vocab, int32_t top_k, size_t *bytes);
+
+/* Forward: any of logprob [rows], entropy [rows], stats [rows][2] and, with
+ * top_k > 0, top_index and top_logprob [rows][top_k]; NULL where not wanted
+ * (at least one must be).  tokens [rows] may be NULL where logprob is.  stats
+ * (for the backward call): the row's largest logit and ln sum_j exp(scale *
+ * (l_j - largest)). */
+zero_status zero_logprob(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t row_stride, float scale, const int64_t *tokens,
+                         float *logprob, float *entropy, float *stats,
+                         int32_t top_k, int32_t *top_index, float *top_logprob,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward: d_logits from the upstream gradients d_logprob and d_entropy
+ * [rows] (either may be NULL: zero) and the forward call's stats and, with
+ * d_entropy, entropy.  tokens may be NULL where d_logprob is. */
+zero_status zero_logprob_grad(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                              int64_t row_stride, float scale, const int64_t *tokens,
+                              const float *stats, const float *entropy,
+                              const float *d_logprob, const float *d_entropy,
+                              void *d_logits, int64_t d_row_stride, void *stream);
+
+/* Forward and backward in one call, for upstream gradients that are known
+ * before it (a loss averaged over the batch): logprob and entropy may be
+ * NULL. */
+zero_status zero_logprob_fused(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                               int64_t row_stride, float scale, const int64_t *tokens,
+                               const float *d_logprob, const float *d_entropy,
+                               float *logprob, float *entropy,
+                               void *d_logits, int64_t d_row_stride,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Forward: the teacher's record is top_index (token ids; negative: no entry)
+ * and top_value [rows][top_k], 1 <= top_k <= ZERO_MAX_TOP.  For
+ * ZERO_DISTILL_TAIL the values are the teacher's log probabilities at the
+ * student's temperature; zero_logprob writes such records.  loss [rows] and
+ * stats [rows][4], either may be NULL.  stats (for the backward call): the
+ * row's largest logit and ln sum_j exp(scale * (l_j - largest)), over all
+ * tokens, then over those not listed (-inf, -inf where there are none). */
+zero_status zero_distill(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t row_stride, float scale, int32_t top_k,
+                         const int32_t *top_index, const float *top_value, int32_t mode,
+                         float *loss, float *stats,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward: d_logits from the upstream gradient d_loss [rows] and the forward
+ * call's stats. */
+zero_status zero_distill_grad(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                              int64_t row_stride, float scale, int32_t top_k,
+                              const int32_t *top_index, const float *top_value, int32_t mode,
+                              const float *stats, const float *d_loss,
+                              void *d_logits, int64_t d_row_stride, void *stream);
+
+/* Forward and backward in one call (d_loss known before it); loss may be
+ * NULL. */
+zero_status zero_distill_fused(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                               int64_t row_stride, float scale, int32_t top_k,
+                               const int32_t *top_index, const float *top_value, int32_t mode,
+                               const float *d_loss, float *loss,
+                               void *d_logits, int64_t d_row_stride,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Sharded checkpoint -- [p1 Implementation notes]: each rank writes its own
  * shard of the checkpoint, and a checkpoint saved at one N is resharded to a
  * different N when it is loaded; [p4 section 5, FSDP1 vs FSDP2]: the state
