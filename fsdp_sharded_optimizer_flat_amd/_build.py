@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libzero.so")
 
 SOURCES = ["layout.cpp", "scalars.cpp", "ledger.cpp", "capi.cpp", "caps.cpp", "offload.cpp", "reshard.cpp",
            "step_kernels.hip", "norm_kernels.hip", "stage_kernels.hip", "pack_kernels.hip",
-           "reshard_kernels.hip", "token_loss.cpp", "token_loss_kernels.hip"]
+           "reshard_kernels.hip", "token_loss.cpp", "logprob_kernels.hip",
+           "distill_kernels.hip"]
 # Host-only C++ built with g++: the offload step's AVX2 code (no FMA, no
 # fast-math, so every operation rounds once, as on the GPU) and the
 # checkpoint files (the SSE4.2 crc32 instruction, which -mavx2 includes).

@@ -1,0 +1,592 @@
+// distill_kernels.hip -- distillation from a teacher's top logits over rows of
+// logits, forward and backward.
+#include "token_loss_device.h"
+
+namespace zero {
+namespace {
+
+using namespace dev;
+
+// What a row's teacher record comes to, as one wave leaves it in LDS.  Entry k
+// is lane k % 64's.  The teacher's probabilities are binary64: 1 - sum q would
+// lose the rest's digits in binary32.
+struct Teacher {
+    double q[ZERO_MAX_TOP];
+    double token_q[ZERO_MAX_TOP];   // the token's probability over all entries that name it
+    double total, rest;             // sum of q and rest; the other tokens' probability
+    double cross;                   // sum of q (ln q - scale (logit - listed_max))
+    alignas(16) int index[ZERO_MAX_TOP];   // the token; -1: no token of the vocabulary
+    int lead[ZERO_MAX_TOP];         // the token where this is the first entry that names it, else -1
+    float value[ZERO_MAX_TOP];
+    float logit[ZERO_MAX_TOP];      // the student's
+    float listed_max, listed_sum;   // of the listed tokens, each once
+    float max, log2z;               // of the row: largest logit, binary logarithm of the sum
+    int any, bad;                   // an entry at all; one outside the vocabulary or with a NaN value
+};
+
+// Orders a wave's LDS writes before its lanes' later reads.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+__device__ __forceinline__ int wave_count(int x)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        x += __shfl_xor(x, o, kWave);
+    return x;
+}
+
+// exp(x) in binary64, to about 1e-11: 2^n times the 16th power of a Taylor sum
+// of exp(z), |z| <= ln2 / 32 (the first term left out is below 2e-13).  Few
+// constants: the library's takes more registers than a wave that holds a row can
+// spare.
+__device__ __forceinline__ double exp64(double x)
+{
+    const double y = x * 1.4426950408889634074;
+    if (!(y > -1000.0))
+        return x != x ? x : 0.0;
+    const double n = __builtin_rint(y), z = (y - n) * (0.69314718055994530942 / 16);
+    double p = 1.0 + z * (1.0 + z * (1.0 / 2 + z * (1.0 / 6 + z * (1.0 / 24 + z * (1.0 / 120)))));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        p = p * p;
+    return __builtin_ldexp(p, (int)fmin(n, 2000.0));
+}
+// ln(x), x > 0: binary32's, then one Newton step (the error is squared).
+__device__ __forceinline__ double log64(double x)
+{
+    const double l = (double)log2f((float)x) * 0.69314718055994530942;
+    return l + (x * exp64(-l) - 1.0);
+}
+
+// Below this the rest's probability is the rounding of the listed ones: binary32
+// log probabilities v put at most |v| 2^-24 into each exp(v), and sum q |v| is
+// an entropy, below 16 nats for any vocabulary here.
+constexpr double kLeastRest = 0x1p-20;
+
+// True (for every lane) where a record is padding: no entry, and no NaN value.
+__device__ __forceinline__ bool is_padding(const int32_t *index, const float *value, int K, int lane)
+{
+    bool some = false;
+    for (int k = lane; k < K; k += kWave) {
+        const float v = value[k];
+        some = some || index[k] >= 0 || v != v;
+    }
+    return !__any(some);
+}
+
+// Reads a row's record and the listed tokens' logits (one whole wave calls it).
+// Loops over a lane's entries are kept rolled and the entries in LDS: the wave
+// may hold a row in its registers meanwhile.
+template <typename T>
+__device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, const float *value,
+                                             int K, int mode, const T *logits, int vocab,
+                                             const Scale &sc, float scale, int lane)
+{
+    const bool renorm = mode == ZERO_DISTILL_RENORM;
+    bool some = false, bad = false;
+    float top = kLowest, lm = -kInf;
+#pragma nounroll
+    for (int k = lane; k < (K + 3) / 4 * 4; k += kWave) {
+        int id = k < K ? index[k] : -1;
+        const float val = k < K ? value[k] : 0.0f;
+        const bool nan = val != val;
+        some = some || id >= 0 || nan;
+        bad = bad || id >= vocab || nan;
+        id = id < 0 || id >= vocab ? -1 : id;
+        const float l = id >= 0 ? grad_at<T>(logits, id) : -kInf;
+        te.index[k] = te.lead[k] = id;
+        te.value[k] = id >= 0 ? val : -kInf;
+        te.logit[k] = l;
+        if (id >= 0)
+            top = __builtin_fmaxf(top, val);
+        lm = __builtin_fmaxf(lm, l);
+    }
+    some = __any(some);
+    bad = __any(bad);
+    lm = wave_max(lm);
+    // q: exp of the given value, or the softmax over the entries
+    top = renorm ? wave_max(top) : 0.0f;
+    double sum = 0.0;
+#pragma nounroll
+    for (int k = lane; k < K; k += kWave) {
+        const double q = exp64((double)te.value[k] - (double)top);
+        te.q[k] = q;
+        sum += q;
+    }
+    sum = wave_sum(sum);
+    double total, rest = 0.0, ln = 0.0;
+    if (renorm) {
+        ln = log64(sum) + (double)top;
+        total = sum != sum ? sum : sum == 0.0 ? 0.0 : 1.0;
+    } else {
+        rest = 1.0 - sum;
+        if (rest < kLeastRest)
+            rest = 0.0;
+        total = sum + rest;
+    }
+    // entries that name the same token: the first of them stands for it.  The
+    // student's share of the listed tokens and the loss's sum over the entries.
+    wave_sync();
+    const double part = renorm ? sum == 0.0 ? 0.0 : 1.0 / sum : 1.0;   // 0: no finite value
+    const float ref = __builtin_fmaxf(lm, kLowest), r = ref * sc.c;
+    int named = 0;
+    float ls = 0.0f;
+    double cross = 0.0;
+#pragma nounroll
+    for (int k = lane; k < K; k += kWave) {
+        const int id = te.index[k];
+        const double q = te.q[k] * part;
+        double token_q = q;
+        int same = 0;
+        for (int o = 0; o < K; o += 4) {
+            const int4 i = *reinterpret_cast<const int4 *>(&te.index[o]);
+            same += (i.x == id) + (i.y == id) + (i.z == id) + (i.w == id);
+        }
+        bool lead = id >= 0;
+        if (lead && same > 1) {
+            token_q = 0.0;
+            for (int o = 0; o < K; ++o)
+                if (te.index[o] == id) {
+                    token_q += te.q[o] * part;
+                    lead = lead && o >= k;
+                }
+            if (!lead)
+                te.lead[k] = -1;
+        }
+        te.token_q[k] = token_q;
+        named += lead;
+        const float l = te.logit[k];
+        if (lead)
+            ls += pow2(rel(l, ref, r, sc));
+        if (q != 0.0)   // NaN too
+            cross += q * ((double)te.value[k] - ln - ((double)l - (double)ref) * (double)scale);
+    }
+    named = wave_count(named);
+    ls = wave_add(ls);
+    cross = wave_sum(cross);
+    if (named == vocab && rest != 0.0) {   // no token is left for the rest
+        total -= rest;
+        rest = 0.0;
+    }
+    if (lane == 0) {
+        te.total = total;
+        te.rest = rest;
+        te.cross = cross;
+        te.listed_max = ref;
+        te.listed_sum = ls;
+        te.any = some;
+        te.bad = bad;
+    }
+}
+
+// The whole row's sum: the tail's (tokens not listed) and the listed tokens'.
+__device__ __forceinline__ Total whole_row(const Total &tail, float listed_max, float listed_sum,
+                                           const Scale &k)
+{
+    Total t{__builtin_fmaxf(tail.empty() ? kLowest : tail.m, listed_sum == 0.0f ? kLowest : listed_max),
+            0.0f, 0.0f};
+    if (!tail.empty())
+        add_total(t, tail, k);
+    if (listed_sum != 0.0f)
+        add_total(t, Total{listed_max, listed_sum, 0.0f}, k);
+    return t;
+}
+
+// The row's loss and statistics from the total over the tokens that are not
+// listed (one lane, where the record is read).
+__device__ __forceinline__ void finish_distill(Teacher &te, const Total &tail, const LossRows &in,
+                                               float *loss, float *stats, int64_t row)
+{
+    const Scale k(in.c);
+    const Total t = whole_row(tail, te.listed_max, te.listed_sum, k);
+    const float log2z = log2f(t.s), ln = ln_sum(t, k);
+    te.max = t.m;
+    te.log2z = log2z;
+    if (loss) {
+        const double rest = te.rest;
+        double v;
+        if (t.empty()) {
+            v = te.total == 0.0 ? 0.0 : te.total * (double)kInf;
+        } else {
+            // ln p of an entry = scale (logit - listed_max) - (scale (max - listed_max) + ln)
+            v = te.cross;
+            if (te.total - rest != 0.0)
+                v += (te.total - rest) * (((double)t.m - (double)te.listed_max) * (double)in.scale + (double)ln);
+            if (rest > 0.0) {
+                const float lp = kLn2 * (log2f(tail.s) + shift_of(tail.m, t.m, k) - log2z);
+                v += rest * ((double)(kLn2 * log2f((float)rest)) - (double)(tail.empty() ? -kInf : lp));
+            }
+        }
+        loss[row] = te.bad ? __builtin_nanf("") : (float)v;
+    }
+    if (stats) {
+        stats[4 * row] = t.empty() ? -kInf : t.m;
+        stats[4 * row + 1] = t.empty() ? -kInf : ln;
+        stats[4 * row + 2] = tail.empty() ? -kInf : tail.m;
+        stats[4 * row + 3] = tail.empty() ? -kInf : ln_sum(tail, k);
+    }
+}
+__device__ __forceinline__ void pad_distill(float *loss, float *stats, int64_t row)
+{
+    if (threadIdx.x == 0) {
+        if (loss)
+            loss[row] = 0.0f;
+        if (stats)
+            stats[4 * row] = stats[4 * row + 1] = stats[4 * row + 2] = stats[4 * row + 3] = 0.0f;
+    }
+}
+
+// A listed token's gradient, entry k's: m the row's largest logit, off what
+// log2 p is below t.
+__device__ __forceinline__ float listed_grad(const Teacher &te, int k, float m, float off, double w,
+                                             const Scale &sc)
+{
+    const float p = pow2(rel(te.logit[k], m, m * sc.c, sc) - off);
+    return (float)(w * (te.total * (double)p - te.token_q[k]));
+}
+
+// Marks the listed tokens of chunks [k0, k1) in `bits`, one bit per element of
+// the chunks (one whole wave).
+__device__ __forceinline__ void mark_listed(unsigned *bits, int words, const int32_t *index, int K,
+                                            int base, int end, int vocab, int lane)
+{
+    for (int i = lane; i < words; i += kWave)
+        bits[i] = 0;
+    wave_sync();
+    for (int k = lane; k < K; k += kWave) {
+        const int id = index[k], at = id + base;
+        if (id >= 0 && id < vocab && at >= 0 && at < end)
+            atomicOr(&bits[at >> 5], 1u << (at & 31));
+    }
+}
+
+// Words of a segment's bitmap: one bit per element of its chunks, whose first
+// and last may stick out of it.
+constexpr int kBitWords = (int)(kLossMaxSegment / 32) + 8;
+
+// One workgroup per segment of a row: the sum over its tokens that the teacher
+// does not list, which a bitmap in LDS leaves out (subtracting the listed ones
+// from the whole sum would lose the rest's digits where little is left).
+template <typename T>
+__global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row0, int segs, int cps)
+{
+    constexpr int U = 4, W = Row<T>::W;
+    __shared__ Total tot[kNW];
+    __shared__ Teacher te;
+    __shared__ unsigned bits[kBitWords];
+    const int64_t row_i = row0 + blockIdx.x / segs;
+    const int seg = blockIdx.x % segs, tid = threadIdx.x, K = a.top_k, lane = tid & (kWave - 1);
+    const int32_t *index = a.top_index + row_i * K;
+    const float *value = a.top_value + row_i * K;
+    const Row<T> row(a.in.logits, row_i * a.in.stride, a.in.vocab);
+    const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
+    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    if (is_padding(index, value, K, lane)) {
+        if (segs == 1)
+            pad_distill(a.loss, a.stats, row_i);
+        return;
+    }
+    const Scale sc(a.in.c);
+    if (tid < kWave) {
+        mark_listed(bits, ((k1 - k0) * W + 31) / 32, index, K, row.phase - k0 * W, (k1 - k0) * W,
+                    a.in.vocab, lane);
+        if (segs == 1)
+            read_teacher(te, index, value, K, a.mode, row.p, a.in.vocab, sc, a.in.scale, lane);
+    }
+    __syncthreads();
+    Sum q;
+    auto take = [&](const Chunk<T> &ch, int k) {
+        float x[W];
+        ch.widen(x);
+        const int at = (k - k0) * W;
+        const unsigned listed = bits[at >> 5] >> (at & 31) & ((1u << W) - 1);
+        if (listed) {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                x[i] = listed >> i & 1 ? -kInf : x[i];
+        }
+        q.add<W, false>(x, sc);
+    };
+    int k = lo + tid;
+    for (; k + kNT * (U - 1) < hi; k += kNT * U) {
+        Chunk<T> ch[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            ch[u].stream(row.chunk(k + kNT * u));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            take(ch[u], k + kNT * u);
+    }
+    for (; k < hi; k += kNT) {
+        Chunk<T> ch;
+        ch.stream(row.chunk(k));
+        take(ch, k);
+    }
+    const int e = tid < 2 * W ? row.edge(tid, k0, k1) : -1;
+    if (e >= 0) {
+        const int at = e + row.phase - k0 * W;
+        const float x[1] = {bits[at >> 5] >> (at & 31) & 1 ? -kInf : row.at(e)};
+        q.add<1, false>(x, sc);
+    }
+    const Total t = block_total<false>(q, sc, tot);
+    if (segs > 1) {
+        if (tid == 0)
+            a.parts[row_i * segs + seg] = LossPart{t.m, t.s, 0.0f, 0.0f};
+    } else if (tid == 0) {
+        finish_distill(te, t, a.in, a.loss, a.stats, row_i);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_t row0, int segs)
+{
+    __shared__ Total tot[kNW];
+    __shared__ Teacher te;
+    const int64_t r = row0 + blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
+    const int32_t *index = a.top_index + r * K;
+    const float *value = a.top_value + r * K;
+    if (is_padding(index, value, K, lane)) {
+        pad_distill(a.loss, a.stats, r);
+        return;
+    }
+    const Scale sc(a.in.c);
+    if (tid < kWave)
+        read_teacher(te, index, value, K, a.mode, static_cast<const T *>(a.in.logits) + r * a.in.stride,
+                     a.in.vocab, sc, a.in.scale, lane);
+    const Total t = join_parts(a.parts + r * segs, segs, sc, tot);
+    if (tid == 0)
+        finish_distill(te, t, a.in, a.loss, a.stats, r);
+}
+
+// d_logits_j = w (Q p_j - q_j) for a listed token and w (Q p_rest - q_rest)
+// p_j / p_rest for the others (w = scale d_loss, Q the teacher's total), where
+// p_j / p_rest is the softmax over the tokens that are not listed.  Every
+// element is written in the second form first, then the listed ones again.
+template <typename T>
+__global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs,
+                                                           int cps)
+{
+    constexpr int W = Row<T>::W;
+    __shared__ Teacher te;
+    const int64_t r = row0 + blockIdx.x / segs;
+    const int seg = blockIdx.x % segs, tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
+    const Row<T> row(a.in.logits, r * a.in.stride, a.in.vocab);
+    T *out = static_cast<T *>(a.d_logits) + r * a.d_stride;
+    const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
+    const float dl = a.d_loss[r];
+    const float m = a.stats[4 * r], ln = a.stats[4 * r + 1];
+    const float tm = a.stats[4 * r + 2], tln = a.stats[4 * r + 3];
+    const double w = (double)dl * (double)a.in.scale;
+    const Scale k(a.in.c);
+    if (tid < kWave)
+        read_teacher(te, a.top_index + r * K, a.top_value + r * K, K, a.mode, row.p, a.in.vocab, k,
+                     a.in.scale, lane);
+    __syncthreads();   // in place: the listed logits are read before any is overwritten
+    const bool zero = !te.any || dl == 0.0f;
+    if (zero || te.bad || m == -kInf) {
+        fill_row(row, out, k0, k1, te.bad && !zero ? __builtin_nanf("") : 0.0f);
+        return;
+    }
+    if (tm == -kInf) {
+        fill_row(row, out, k0, k1, 0.0f);
+    } else {
+        // ln p_rest, then log2 of the tail's softmax = t - off
+        const float c = k.c, ref = tm * c;
+        const float rest_ln = (float)(((double)tm - (double)m) * (double)a.in.scale + ((double)tln - (double)ln));
+        const float off = residue(tm, k) + tln * kLog2E;
+        const float coef = (float)(w * (te.total * (double)pow2(rest_ln * kLog2E) - te.rest)) * pow2(-off);
+        if (__builtin_fabsf(tm) > k.big)
+            map_row(row, out, k0, k1, -1, 0.0f, [&](float x) { return coef * pow2((x - tm) * c); });
+        else
+            map_row(row, out, k0, k1, -1, 0.0f,
+                    [&](float x) { return coef * pow2(__builtin_fmaf(x, c, -ref)); });
+    }
+    __syncthreads();
+    // the listed tokens of this segment
+    const int id = tid < K ? te.lead[tid] : -1, at = id + row.phase;
+    if (id >= 0 && at >= k0 * W && at < k1 * W)
+        store_one(out + id, listed_grad(te, tid, m, residue(m, k) + ln * kLog2E, w, k));
+}
+
+// Forward and backward of whole rows, at most kHeld NT chunks each.  The first
+// wave reads the next row's record while the others write this row's gradients;
+// records and bitmaps have two places each (one for single-wave workgroups).
+template <typename T, int NT, bool SAME>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4)))
+void distill_row_kernel(DistillArgs a, DistillGradArgs b)
+{
+    constexpr int W = Row<T>::W, N = HeldRow<T, NT, SAME>::G * W, kSets = NT == kWave ? 1 : 2;
+    constexpr int kWords = (NT * kHeld * W + 2 * W + 31) / 32;
+    __shared__ Total tot[2][NT / kWave];
+    __shared__ Teacher teacher[kSets];
+    __shared__ unsigned bitmap[kSets][kWords];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
+    const Scale k(a.in.c);
+    auto row_at = [&](int64_t r) { return Row<T>(a.in.logits, r * a.in.stride, a.in.vocab); };
+    auto out_at = [&](int64_t r) { return static_cast<T *>(b.d_logits) + r * b.d_stride; };
+    auto skip_padding = [&](int64_t r) {
+        while (r < a.in.rows && is_padding(a.top_index + r * K, a.top_value + r * K, K, lane)) {
+            const Row<T> row = row_at(r);
+            pad_distill(a.loss, a.stats, r);
+            fill_row<T, NT>(row, out_at(r), 0, row.chunks, 0.0f);
+            r += gridDim.x;
+        }
+        return r;
+    };
+    auto read_record = [&](int64_t r, const Row<T> &row, int set) {
+        const int32_t *index = a.top_index + r * K;
+        const float *value = a.top_value + r * K;
+        mark_listed(bitmap[set], (row.chunks * W + 31) / 32, index, K, row.phase, row.chunks * W,
+                    a.in.vocab, lane);
+        read_teacher(teacher[set], index, value, K, a.mode, row.p, a.in.vocab, k, a.in.scale, lane);
+    };
+    HeldRow<T, NT, SAME> held;
+    int64_t r = skip_padding(blockIdx.x);
+    if (r >= a.in.rows)
+        return;
+    held.load(row_at(r));
+    if (tid < kWave)
+        read_record(r, held.row, 0);
+    __syncthreads();
+    for (int turn = 0;; turn ^= 1) {
+        const int set = kSets == 1 ? 0 : turn;
+        Teacher &te = teacher[set];
+        const unsigned *bits = bitmap[set];
+        Sum q;
+        held.each_group([&](int i, float (&x)[N]) {
+#pragma unroll
+            for (int j = 0; j < N / W; ++j) {
+                const int at = min(held.row.full_lo + tid + NT * (i + j), held.row.chunks - 1) * W;
+                const unsigned listed = bits[at >> 5] >> (at & 31) & ((1u << W) - 1);
+                if (listed) {
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        x[j * W + w] = listed >> w & 1 ? -kInf : x[j * W + w];
+                }
+            }
+            q.template add<N, false>(x, k);
+        });
+        if (held.e >= 0) {
+            const int at = held.e + held.row.phase;
+            const float x[1] = {bits[at >> 5] >> (at & 31) & 1 ? -kInf : held.edge};
+            q.template add<1, false>(x, k);
+        }
+        const Total t = block_total<false, NT / kWave>(q, k, tot[turn]);
+        const int64_t rn = skip_padding(r + gridDim.x);
+        const Row<T> next = rn < a.in.rows ? row_at(rn) : Row<T>();
+        T *out = out_at(r);
+        const float dl = b.d_loss[r];
+        const double w = (double)dl * (double)a.in.scale;
+        if (tid < kWave) {
+            if (tid == 0)
+                finish_distill(te, t, a.in, a.loss, a.stats, r);
+            if (kSets == 2 && rn < a.in.rows)
+                read_record(rn, next, set ^ 1);
+        }
+        const bool nothing = t.empty() && te.listed_sum == 0.0f;
+        const bool fill = dl == 0.0f || te.bad || nothing, big = __builtin_fabsf(t.m) > k.big;
+        // the rest's share of the whole sum, then the coefficient of 2^t
+        const Total whole = whole_row(t, te.listed_max, te.listed_sum, k);
+        const float share = t.s * pow2(shift_of(t.m, whole.m, k)) / whole.s;
+        const float coef = (float)(w * (te.total * (double)share - te.rest)) / t.s;
+        const float m = t.m, ref = m * k.c;
+        if (fill || t.empty())
+            fill_row<T, NT>(held.row, out, 0, held.row.chunks,
+                            fill && te.bad && dl != 0.0f ? __builtin_nanf("") : 0.0f);
+        else if (big)   // rare: from memory, so that the held row's loop is not written twice
+            map_row<T, NT>(held.row, out, 0, held.row.chunks, -1, 0.0f,
+                           [&](float x) { return coef * pow2((x - m) * k.c); });
+        held.map(out, !fill && !t.empty() && !big, next,
+                 [&](float x) { return coef * pow2(__builtin_fmaf(x, k.c, -ref)); });
+        __syncthreads();
+        if (!fill)
+            for (int i = tid; i < K; i += NT)
+                if (te.lead[i] >= 0)
+                    store_one(out + te.lead[i], listed_grad(te, i, te.max, te.log2z, w, k));
+        held.take(next);
+        if (rn >= a.in.rows)
+            return;
+        r = rn;
+        if (kSets == 1) {
+            wave_sync();
+            read_record(r, next, 0);
+            wave_sync();
+        }
+    }
+}
+
+// -- launches ---------------------------------------------------------------------------------
+
+template <typename T>
+int launch_distill_of(const DistillArgs &a, int segs, hipStream_t st)
+{
+    const int cps = chunks_per<T>(a.in.vocab, segs);
+    if (int e = each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
+            hipLaunchKernelGGL((distill_kernel<T>), dim3(n * (unsigned)segs), dim3(kNT), 0, st, a, r,
+                               segs, cps);
+        }))
+        return e;
+    if (segs == 1)
+        return hipSuccess;
+    return each_launch(a.in.rows, 1, [&](int64_t r, unsigned n) {
+        hipLaunchKernelGGL((distill_join_kernel<T>), dim3(n), dim3(kNT), 0, st, a, r, segs);
+    });
+}
+
+template <typename T, int NT>
+int launch_distill_row_nt(const DistillArgs &a, const DistillGradArgs &b, hipStream_t st)
+{
+    const dim3 grid(held_grid(a.in.rows, NT));
+    if (same_phase(a.in, b.d_logits, b.d_stride))
+        hipLaunchKernelGGL((distill_row_kernel<T, NT, true>), grid, dim3(NT), 0, st, a, b);
+    else
+        hipLaunchKernelGGL((distill_row_kernel<T, NT, false>), grid, dim3(NT), 0, st, a, b);
+    return hipGetLastError();
+}
+template <typename T>
+int launch_distill_row(const DistillArgs &a, const DistillGradArgs &b, hipStream_t st)
+{
+    const int threads = held_threads<T>(a.in.vocab);
+    return threads == 64  ? launch_distill_row_nt<T, 64>(a, b, st)
+         : threads == 256 ? launch_distill_row_nt<T, 256>(a, b, st)
+         : threads == 512 ? launch_distill_row_nt<T, 512>(a, b, st)
+                          : launch_distill_row_nt<T, 1024>(a, b, st);
+}
+
+}  // namespace
+
+int launch_distill(const DistillArgs &a, int32_t segs, void *stream)
+{
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    return a.in.dtype == ZERO_BF16 ? launch_distill_of<uint16_t>(a, segs, st)
+                                   : launch_distill_of<float>(a, segs, st);
+}
+
+int launch_distill_grad(const DistillGradArgs &a, void *stream)
+{
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    const bool bf = a.in.dtype == ZERO_BF16;
+    const int segs = bf ? grad_segments<uint16_t>(a.in.vocab) : grad_segments<float>(a.in.vocab);
+    const int cps = bf ? chunks_per<uint16_t>(a.in.vocab, segs) : chunks_per<float>(a.in.vocab, segs);
+    return each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
+        const dim3 grid(n * (unsigned)segs), block(kNT);
+        if (bf)
+            hipLaunchKernelGGL((distill_grad_kernel<uint16_t>), grid, block, 0, st, a, r, segs, cps);
+        else
+            hipLaunchKernelGGL((distill_grad_kernel<float>), grid, block, 0, st, a, r, segs, cps);
+    });
+}
+
+int launch_distill_fused(const DistillArgs &a, const DistillGradArgs &b, void *stream)
+{
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    return a.in.dtype == ZERO_BF16 ? launch_distill_row<uint16_t>(a, b, st)
+                                   : launch_distill_row<float>(a, b, st);
+}
+
+}  // namespace zero

@@ -1,5 +1,5 @@
 // token_loss.h -- what the token-loss entry points (token_loss.cpp) hand to
-// the kernels (token_loss_kernels.hip).  Not part of the public ABI.
+// the kernels (logprob_kernels.hip, distill_kernels.hip).  Not part of the public ABI.
 #pragma once
 
 #include "zero_internal.h"

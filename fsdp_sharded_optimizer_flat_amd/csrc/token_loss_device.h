@@ -1,0 +1,567 @@
+// token_loss_device.h -- what the kernels of the token losses share: rows cut
+// into 16-byte chunks, running sums of exponentials, rows mapped to gradients,
+// rows held in registers.
+//
+// All work is done in binary logarithms: with c = scale * log2(e) a logit l
+// counts as t = c l - R, R = fl(c m) for a reference logit m, and 2^t is one
+// v_exp_f32.  One fused multiply-add forms t with a single rounding relative to
+// the reference, so the error of 2^t grows with l's distance from the
+// reference only.  A lane keeps the sum of 2^t over its elements in one pass:
+// its reference is the largest logit of its first group, raised (the sum
+// rescaled) only when a group exceeds it by more than kHeadroom binary orders
+// -- sums stay far inside binary32's range, and after the first groups almost
+// no group raises it.  R's own rounding cancels between the sums and what is
+// read off them while it is small; for references with |c m| > 2^20 (rows of huge
+// logits, or parts of rows masked with the type's lowest value, where c m could
+// even leave binary32's range) t = (l - m) c is taken instead.
+//
+// Bound: HBM.  A forward pass reads each logit once; per bf16 element that is 2
+// bytes against 8 to 11 vector issue slots (widen 1, max 1/2, fma 1, exp 4,
+// add 1; entropy: clamp 1, fma 1).
+#pragma once
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "token_loss.h"
+
+namespace zero {
+namespace dev {
+
+constexpr int kNT = kLossBlock;
+constexpr int kNW = kNT / kWave;
+constexpr float kInf = __builtin_inff();
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLowest = -3.40282346638528859812e38f;
+constexpr float kHeadroom = 10.0f;      // binary orders a group may exceed a lane's reference
+constexpr float kBig = 0x1p20f;         // |c m| beyond it: t = (l - m) c
+constexpr float kTiny = -1000.0f;       // t of a probability that is zero, for products with it
+
+// -- loading -------------------------------------------------------------------------
+
+// 16 bytes of a row: W elements.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+    static constexpr int W = 8;
+    u32x4 r;
+    __device__ __forceinline__ void load(const uint16_t *p) { r = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ __forceinline__ void stream(const uint16_t *p)
+    {
+        r = ld_stream(reinterpret_cast<const u32x4 *>(p));
+    }
+    __device__ __forceinline__ void widen(float (&x)[W]) const
+    {
+        x[0] = bf_lo(r.x), x[1] = bf_hi(r.x), x[2] = bf_lo(r.y), x[3] = bf_hi(r.y);
+        x[4] = bf_lo(r.z), x[5] = bf_hi(r.z), x[6] = bf_lo(r.w), x[7] = bf_hi(r.w);
+    }
+};
+template <>
+struct Chunk<float> {
+    static constexpr int W = 4;
+    f32x4 r;
+    __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const f32x4 *>(p); }
+    __device__ __forceinline__ void stream(const float *p)
+    {
+        r = ld_stream(reinterpret_cast<const f32x4 *>(p));
+    }
+    __device__ __forceinline__ void widen(float (&x)[W]) const
+    {
+        x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
+    }
+};
+
+// Stores a chunk's gradients, rounded once, at any element alignment (gfx950
+// takes 16-byte stores at every address; a row whose gradient sits at another
+// 16-byte phase than its logits needs them).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <typename T, int W>
+__device__ __forceinline__ u32x4 pack_chunk(const float (&g)[W])
+{
+    if constexpr (sizeof(T) == 2)
+        return u32x4{pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                     pack_bf16x2(g[6], g[7])};
+    else
+        return u32x4{__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                     __float_as_uint(g[3])};
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_chunk(T *p, const float (&g)[W])
+{
+    __builtin_nontemporal_store(pack_chunk<T>(g), reinterpret_cast<u32x4_any *>(p));
+}
+__device__ __forceinline__ void store_one(uint16_t *p, float g) { *p = to_bf16(g); }
+__device__ __forceinline__ void store_one(float *p, float g) { *p = g; }
+
+// A row cut into chunks that start at 16-byte boundaries: chunk k holds
+// elements k W - phase .. + W - 1, whole for full_lo <= k < full_hi; the first
+// and last may stick out of the row and are read element by element.
+template <typename T>
+struct Row {
+    static constexpr int W = Chunk<T>::W;
+    const T *p;
+    int vocab, phase, chunks, full_lo, full_hi;
+    __device__ __forceinline__ Row() : p(nullptr), vocab(0), phase(0), chunks(0), full_lo(0), full_hi(0) {}
+    __device__ __forceinline__ Row(const void *base, int64_t off, int vocab_) : vocab(vocab_)
+    {
+        p = static_cast<const T *>(base) + off;
+        phase = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+        chunks = (vocab + phase + W - 1) / W;
+        full_lo = phase ? 1 : 0;
+        full_hi = max(full_lo, (vocab + phase) / W);
+    }
+    __device__ __forceinline__ const T *chunk(int k) const { return p + ((int64_t)k * W - phase); }
+    __device__ __forceinline__ float at(int e) const { return grad_at<T>(p, e); }
+    // Element of edge slot s (0 .. 2W-1: the head's, then the tail's) among
+    // chunks [k0, k1), or -1.
+    __device__ __forceinline__ int edge(int s, int k0, int k1) const
+    {
+        const int k = s < W ? 0 : full_hi;
+        const int e = k * W - phase + (s & (W - 1));
+        const bool partial = s < W ? full_lo == 1 : full_hi < chunks;
+        return partial && k >= k0 && k < k1 && e >= 0 && e < vocab ? e : -1;
+    }
+};
+
+// -- running sums ------------------------------------------------------------------------
+
+struct Scale {
+    float c, gap, big;   // logits that span kHeadroom binary orders, and |m| beyond which |c m| > kBig
+    __device__ __forceinline__ explicit Scale(float c_) : c(c_), gap(kHeadroom / c_), big(kBig / c_) {}
+};
+
+// t of logit l against reference m (r = fl(c m)).
+__device__ __forceinline__ float rel(float l, float m, float r, const Scale &k)
+{
+    return __builtin_fabsf(m) > k.big ? (l - m) * k.c : __builtin_fmaf(l, k.c, -r);
+}
+// t of reference m against reference n, as the sums were formed.
+__device__ __forceinline__ float shift_of(float m, float n, const Scale &k)
+{
+    return __builtin_fabsf(m) > k.big || __builtin_fabsf(n) > k.big ? (m - n) * k.c : m * k.c - n * k.c;
+}
+// c m - fl(c m): what the sums' reference R is off the exact one by.
+__device__ __forceinline__ float residue(float m, const Scale &k)
+{
+    return __builtin_fabsf(m) > k.big ? 0.0f : __builtin_fmaf(m, k.c, -(m * k.c));
+}
+__device__ __forceinline__ float pow2(float t) { return __builtin_amdgcn_exp2f(t); }
+
+struct Sum {
+    float top;       // the largest logit seen
+    float m, r;      // the reference and fl(c m)
+    float thr;       // groups whose largest logit is above it raise the reference
+    float s, a;      // sums of 2^t and of t 2^t
+    bool big;        // of the wave: some lane's |c m| is beyond kBig
+    __device__ __forceinline__ Sum() : top(-kInf), m(0), r(0), thr(-kInf), s(0), a(0), big(false) {}
+
+    __device__ __forceinline__ void rebase(float n, const Scale &k)
+    {
+        if (s != 0.0f) {   // else nothing is added yet, and n may lie below m
+            const float d = shift_of(m, n, k), f = pow2(d);
+            a = f * (a + __builtin_fmaxf(d, kTiny) * s);
+            s = s * f;
+        }
+        m = n;
+        r = n * k.c;
+    }
+
+    // Adds N elements (every lane of the wave that is to add any calls it).  A
+    // NaN among them makes the sum NaN (max ignores it).
+    template <int N, bool ENT>
+    __device__ __forceinline__ void add(const float (&x)[N], const Scale &k)
+    {
+        float g = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i)
+            g = __builtin_fmaxf(g, x[i]);
+        add_with_max<N, ENT>(x, g, k);
+    }
+    template <int N, bool ENT>
+    __device__ __forceinline__ void add_with_max(const float (&x)[N], float g, const Scale &k)
+    {
+        top = __builtin_fmaxf(top, g);
+        if (__any(g > thr)) {
+            if (g > thr) {
+                rebase(g, k);
+                thr = g + k.gap;
+            }
+            big = __any(__builtin_fabsf(m) > k.big);
+        }
+        if (big)
+            add_terms<N, ENT, true>(x, k);
+        else
+            add_terms<N, ENT, false>(x, k);
+    }
+    template <int N, bool ENT, bool BIG>
+    __device__ __forceinline__ void add_terms(const float (&x)[N], const Scale &k)
+    {
+        // a group's sums apart from the lane's: shorter chains round less
+        float sg = 0, ag = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float t = BIG ? rel(x[i], m, r, k) : __builtin_fmaf(x[i], k.c, -r);
+            const float e = pow2(t);
+            sg += e;
+            if constexpr (ENT)
+                ag = __builtin_fmaf(e, __builtin_fmaxf(t, kTiny), ag);
+        }
+        s += sg;
+        if constexpr (ENT)
+            a += ag;
+    }
+};
+
+// The sum of a wave's or workgroup's lanes against the largest logit among
+// them (kLowest at least), in a fixed order.
+struct Total {
+    float m, s, a;
+    __device__ __forceinline__ bool empty() const { return s == 0.0f; }   // every logit -inf
+};
+
+__device__ __forceinline__ float wave_max(float x)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        x = __builtin_fmaxf(x, __shfl_xor(x, o, kWave));
+    return x;
+}
+__device__ __forceinline__ float wave_add(float x)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        x += __shfl_xor(x, o, kWave);
+    return x;
+}
+
+// One of several totals moved to reference m and added.
+__device__ __forceinline__ void add_total(Total &t, const Total &o, const Scale &k)
+{
+    const float d = shift_of(o.m, t.m, k), f = pow2(d);
+    t.a += f * (o.a + __builtin_fmaxf(d, kTiny) * o.s);
+    t.s += f * o.s;
+}
+
+// Every thread gets the workgroup's total.  `sh`: one Total per wave.  One
+// barrier; the caller places another before `sh` is written again.
+template <bool ENT, int NW = kNW>
+__device__ __forceinline__ Total block_total(Sum q, const Scale &k, Total *sh)
+{
+    const float m = __builtin_fmaxf(wave_max(q.top), kLowest);
+    q.rebase(m, k);
+    Total w{m, wave_add(q.s), ENT ? wave_add(q.a) : 0.0f};
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        sh[threadIdx.x / kWave] = w;
+    __syncthreads();
+    // each lane takes one wave's total, butterflies over the NW of them (held in
+    // one register each: a wave that holds a row has few to spare)
+    Total t = sh[threadIdx.x & (NW - 1)];
+    const Total own = t;
+#pragma unroll
+    for (int o = NW / 2; o >= 1; o >>= 1)
+        t.m = __builtin_fmaxf(t.m, __shfl_xor(t.m, o, kWave));
+    t.s = t.a = 0.0f;
+    add_total(t, own, k);
+#pragma unroll
+    for (int o = NW / 2; o >= 1; o >>= 1) {
+        t.s += __shfl_xor(t.s, o, kWave);
+        if constexpr (ENT)
+            t.a += __shfl_xor(t.a, o, kWave);
+    }
+    return t;
+}
+
+// The total of a row's segments, one workgroup per row, in a fixed order.
+__device__ __forceinline__ Total join_parts(const LossPart *p, int segs, const Scale &k, Total *sh)
+{
+    const int tid = threadIdx.x;
+    float m = kLowest;
+    for (int i = tid; i < segs; i += kNT)
+        m = __builtin_fmaxf(m, p[i].m);
+    m = wave_max(m);
+    Total t{m, 0.0f, 0.0f};
+    for (int i = tid; i < segs; i += kNT)
+        add_total(t, Total{p[i].m, p[i].s, p[i].a}, k);
+    t.s = wave_add(t.s);
+    t.a = wave_add(t.a);
+    if ((tid & (kWave - 1)) == 0)
+        sh[tid / kWave] = t;
+    __syncthreads();
+    t = Total{kLowest, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kNW; ++i)
+        t.m = __builtin_fmaxf(t.m, sh[i].m);
+#pragma unroll
+    for (int i = 0; i < kNW; ++i)
+        add_total(t, sh[i], k);
+    return t;
+}
+
+// ln of the sum relative to the exact largest logit, and a token's log
+// probability.
+__device__ __forceinline__ float ln_sum(const Total &t, const Scale &k)
+{
+    return kLn2 * (log2f(t.s) - residue(t.m, k));
+}
+__device__ __forceinline__ float log_prob(float l, const Total &t, float log2s, const Scale &k)
+{
+    if (__builtin_fabsf(l) > 0x1p100f)   // c l may leave binary32's range where ln p does not
+        return (l - t.m) * (k.c * kLn2) - kLn2 * log2s;
+    return kLn2 * (rel(l, t.m, t.m * k.c, k) - log2s);
+}
+
+// -- rows mapped to gradients ----------------------------------------------------------------
+
+// Visits chunks [k0, k1) of a row of logits and writes what f(logit) returns to
+// the same elements of the gradient's row; element `hot` gets `add` more.
+template <typename T, int NT = kNT, typename F>
+__device__ __forceinline__ void map_row(const Row<T> &row, T *out, int k0, int k1, int hot, float add,
+                                        F f)
+{
+    constexpr int W = Row<T>::W;
+    const int tid = threadIdx.x;
+    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    const int hot_k = hot < 0 ? -1 : (hot + row.phase) / W, hot_i = (hot + row.phase) & (W - 1);
+    for (int k = lo + tid; k < hi; k += NT) {
+        Chunk<T> ch;
+        ch.stream(row.chunk(k));
+        float x[W], g[W];
+        ch.widen(x);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            g[i] = f(x[i]);
+        if (k == hot_k) {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                g[i] = i == hot_i ? g[i] + add : g[i];
+        }
+        store_chunk(out + (k * W - row.phase), g);
+    }
+    const int e = tid < 2 * W ? row.edge(tid, k0, k1) : -1;
+    if (e >= 0) {
+        const float g = f(row.at(e));
+        store_one(out + e, e == hot ? g + add : g);
+    }
+}
+
+// The same value in every element, without reading the logits.
+template <typename T, int NT = kNT>
+__device__ __forceinline__ void fill_row(const Row<T> &row, T *out, int k0, int k1, float v)
+{
+    constexpr int W = Row<T>::W;
+    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    float g[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        g[i] = v;
+    for (int k = lo + (int)threadIdx.x; k < hi; k += NT)
+        store_chunk(out + (k * W - row.phase), g);
+    const int e = (int)threadIdx.x < 2 * W ? row.edge(threadIdx.x, k0, k1) : -1;
+    if (e >= 0)
+        store_one(out + e, v);
+}
+
+// -- a row held in registers ---------------------------------------------------------------
+//
+// One workgroup of NT threads holds a row of up to kHeld chunks a thread in its
+// registers: the logits are read from memory once, summed as they arrive, and
+// turned into gradients from the registers.  The workgroup goes through rows
+// gridDim.x apart, and as soon as a chunk's gradients are on their way its
+// registers take the same chunk of the next row, so that memory is read and
+// written at the same time and idles only while a row is summed.
+
+constexpr int kHeld = 16;
+
+// SAME: the gradient's rows sit at the 16-byte phase of the logits' rows.
+template <typename T, int NT, bool SAME>
+struct HeldRow {
+    static constexpr int W = Row<T>::W;
+    static constexpr int G = 8 / W;       // chunks of a group that is summed at once
+    Row<T> row;
+    int n;        // whole chunks
+    Chunk<T> ch[kHeld];
+    float edge;   // this thread's element of the row's partial first or last chunk
+    int e;        // and its index, or -1
+
+    // p, which is the same in every lane, in scalar registers.
+    static __device__ __forceinline__ T *scalar(const T *p)
+    {
+        const uint64_t v = reinterpret_cast<uint64_t>(p);
+        const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 |
+                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+        return reinterpret_cast<T *>(u);
+    }
+    // `chunks` chunks from p on as a buffer: what lies past them is neither read
+    // nor written.
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const T *p, int chunks)
+    {
+        return __builtin_amdgcn_make_buffer_rsrc(scalar(p), 0,
+                                                 __builtin_amdgcn_readfirstlane(chunks) * 16,
+                                                 kRawBufferWord3);
+    }
+    __device__ __forceinline__ void load_chunk(__amdgpu_buffer_rsrc_t rs, int i)
+    {
+        ch[i].r = __builtin_bit_cast(decltype(ch[i].r),
+                                     __builtin_amdgcn_raw_buffer_load_b128(
+                                         rs, (int)threadIdx.x * 16, NT * 16 * i, kLoadStreamPolicy));
+    }
+    __device__ __forceinline__ void take(const Row<T> &next)
+    {
+        row = next;
+        n = next.full_hi - next.full_lo;
+        e = (int)threadIdx.x < 2 * W ? next.edge(threadIdx.x, 0, next.chunks) : -1;
+        edge = e >= 0 ? next.at(e) : -kInf;
+    }
+    // Reads a whole row.  Chunks past its end are not read.
+    __device__ __forceinline__ void load(const Row<T> &next)
+    {
+        const __amdgpu_buffer_rsrc_t rs = window(next.chunk(next.full_lo), next.full_hi - next.full_lo);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            load_chunk(rs, i);
+        take(next);
+    }
+    // Visits the groups of G chunks that hold anything: f(first chunk, values).
+    // Values past the row's whole chunks are -inf.
+    template <typename F>
+    __device__ __forceinline__ void each_group(F f)
+    {
+        constexpr unsigned none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
+#pragma unroll
+        for (int i = 0; i < kHeld; i += G) {
+            if (NT * i < n) {
+                float x[W * G];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    if (NT * (i + j + 1) > n) {   // at most one chunk of the row: kept a branch
+                        asm volatile("");
+                        if (NT * (i + j) + (int)threadIdx.x >= n)
+                            ch[i + j].r = __builtin_bit_cast(decltype(ch[0].r), u32x4{none, none, none, none});
+                    }
+                    float y[W];
+                    ch[i + j].widen(y);
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        x[j * W + w] = y[w];
+                }
+                f(i, x);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // Writes f(logit) for every element the thread holds (nothing unless
+    // `write`) and reads `next` (which may be empty) into its place.  `out`: the
+    // gradient's row.
+    template <typename F>
+    __device__ __forceinline__ void map(T *out, bool write, const Row<T> &next, F f)
+    {
+        const __amdgpu_buffer_rsrc_t from = window(next.chunk(next.full_lo), next.full_hi - next.full_lo);
+        T *first = scalar(out + (row.full_lo * W - row.phase));
+        const int m = write ? n : 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            // opaque, or the widened logits of the sums would be kept from there
+            asm volatile("" : "+v"(ch[i].r));
+            if constexpr (SAME) {
+                // The chunk's own window, not an offset in a scalar register:
+                // MI355X has stored what the next instruction wrote to the data
+                // registers of a 16-byte buffer store with such an offset (the
+                // compiler leaves no wait between the two then).
+                if (NT * i < m)
+                    __builtin_amdgcn_raw_buffer_store_b128(mapped(ch[i], f),
+                                                           window(first + NT * W * i, m - NT * i),
+                                                           (int)threadIdx.x * 16, 0, kSpanStorePolicy);
+            } else {
+                if ((int)threadIdx.x < m - NT * i)
+                    __builtin_nontemporal_store(
+                        mapped(ch[i], f),
+                        reinterpret_cast<u32x4_any *>(first + NT * W * i + threadIdx.x * (unsigned)W));
+            }
+            load_chunk(from, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (e >= 0 && write)
+            store_one(out + e, f(edge));
+    }
+    // The thread that holds element x of the row (0 <= x < vocab).
+    __device__ __forceinline__ int owner(int x) const
+    {
+        const int at = x + row.phase, k = at / W;
+        return k < row.full_lo ? at : k < row.full_hi ? (k - row.full_lo) % NT : W + (at & (W - 1));
+    }
+    template <typename F>
+    static __device__ __forceinline__ u32x4 mapped(const Chunk<T> &c, F f)
+    {
+        float x[W], g[W];
+        c.widen(x);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            g[j] = f(x[j]);
+        return pack_chunk<T>(g);
+    }
+};
+
+// -- launches ---------------------------------------------------------------------------------
+
+// Calls f(first row, rows) so that no launch has more than 2^31 threads.
+template <typename F>
+inline int each_launch(int64_t rows, int per_row, F f, int threads = kNT)
+{
+    const int64_t most = std::max<int64_t>(1, (int64_t(1) << 31) / threads / per_row);
+    for (int64_t r = 0; r < rows; r += most) {
+        f(r, (unsigned)std::min(most, rows - r));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+// Chunks per workgroup when a row of `vocab` elements at any 16-byte phase is
+// cut for `segs` workgroups.
+template <typename T>
+int chunks_per(int vocab, int segs)
+{
+    constexpr int W = 16 / (int)sizeof(T);
+    const int most = (vocab + 2 * (W - 1)) / W;
+    return (most + segs - 1) / segs;
+}
+
+// Threads of the workgroup that holds a row in registers; 0: the row is too
+// long for 1024.
+template <typename T>
+int held_threads(int vocab)
+{
+    const int most = chunks_per<T>(vocab, 1);
+    return most <= 64 * kHeld ? 64 : most <= 256 * kHeld ? 256 : most <= 512 * kHeld ? 512
+         : most <= 1024 * kHeld ? 1024 : 0;
+}
+
+// Workgroups of a launch that goes through rows: as many as are resident at once
+// (128 registers a thread: 16 waves on a compute unit).
+inline unsigned held_grid(int64_t rows, int threads)
+{
+    const int64_t most = (int64_t)device_cu_count() * (1024 / threads);
+    return (unsigned)std::max<int64_t>(1, std::min(rows, most));
+}
+
+// Every row of the gradient starts at its logits' 16-byte phase.
+inline bool same_phase(const LossRows &in, const void *d_logits, int64_t d_stride)
+{
+    const uint64_t es = in.dtype == ZERO_BF16 ? 2 : 4;
+    const uint64_t base = (uint64_t)(uintptr_t)in.logits ^ (uint64_t)(uintptr_t)d_logits;
+    return base % 16 == 0 && (uint64_t)(in.stride - d_stride) * es % 16 == 0;
+}
+
+// Workgroups per row of a gradient pass: 8 chunks per thread.
+template <typename T>
+int grad_segments(int vocab)
+{
+    constexpr int W = 16 / (int)sizeof(T);
+    return (vocab + 8 * kNT * W - 1) / (8 * kNT * W);
+}
+
+}  // namespace dev
+}  // namespace zero
