@@ -24,6 +24,13 @@ struct Teacher {
     int any, bad;                   // an entry at all; one outside the vocabulary or with a NaN value
 };
 
+// The backward pass's share of it.
+struct Listed {
+    double q[ZERO_MAX_TOP];
+    int index[ZERO_MAX_TOP];
+    float logit[ZERO_MAX_TOP];
+};
+
 // Orders a wave's LDS writes before its lanes' later reads.
 __device__ __forceinline__ void wave_sync()
 {
@@ -78,6 +85,30 @@ __device__ __forceinline__ bool is_padding(const int32_t *index, const float *va
     return !__any(some);
 }
 
+// The teacher's total and the other tokens' probability from the sum over its
+// entries (relative to their largest value where it is normalised).
+__device__ __forceinline__ void teacher_total(double sum, bool renorm, double &total, double &rest)
+{
+    rest = renorm ? 0.0 : 1.0 - sum;
+    if (rest < kLeastRest)
+        rest = 0.0;
+    total = !renorm ? sum + rest : sum != sum ? sum : sum == 0.0 ? 0.0 : 1.0;
+}
+
+// Distinct tokens of the vocabulary that a record names (one whole wave).
+__device__ __forceinline__ int tokens_named(const int32_t *index, int K, int vocab, int lane)
+{
+    int named = 0;
+    for (int k = lane; k < K; k += kWave) {
+        const int id = index[k];
+        bool lead = id >= 0 && id < vocab;
+        for (int o = 0; o < k && lead; ++o)
+            lead = index[o] != id;
+        named += lead;
+    }
+    return wave_count(named);
+}
+
 // Reads a row's record and the listed tokens' logits (one whole wave calls it).
 // Loops over a lane's entries are kept rolled and the entries in LDS: the wave
 // may hold a row in its registers meanwhile.
@@ -118,16 +149,9 @@ __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, 
         sum += q;
     }
     sum = wave_sum(sum);
-    double total, rest = 0.0, ln = 0.0;
-    if (renorm) {
-        ln = log64(sum) + (double)top;
-        total = sum != sum ? sum : sum == 0.0 ? 0.0 : 1.0;
-    } else {
-        rest = 1.0 - sum;
-        if (rest < kLeastRest)
-            rest = 0.0;
-        total = sum + rest;
-    }
+    double total, rest;
+    teacher_total(sum, renorm, total, rest);
+    const double ln = renorm ? log64(sum) + (double)top : 0.0;
     // entries that name the same token: the first of them stands for it.  The
     // student's share of the listed tokens and the loss's sum over the entries.
     wave_sync();
@@ -282,7 +306,8 @@ __global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row
     const int seg = blockIdx.x % segs, tid = threadIdx.x, K = a.top_k, lane = tid & (kWave - 1);
     const int32_t *index = a.top_index + row_i * K;
     const float *value = a.top_value + row_i * K;
-    const Row<T> row(a.in.logits, row_i * a.in.stride, a.in.vocab);
+    const T *p = static_cast<const T *>(a.in.logits) + row_i * a.in.stride;
+    const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
     if (is_padding(index, value, K, lane)) {
@@ -367,50 +392,107 @@ __global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_
 // p_j / p_rest for the others (w = scale d_loss, Q the teacher's total), where
 // p_j / p_rest is the softmax over the tokens that are not listed.  Every
 // element is written in the second form first, then the listed ones again.
-template <typename T>
-__global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs,
-                                                           int cps)
+//
+// One workgroup per kNT U chunks of a row, U to a thread, so that neighbouring
+// workgroups sweep the memory in order.  Each wave adds up the record's
+// probabilities for itself; a workgroup that holds no listed token (U = 2 and a
+// vocabulary of 128256: 13 % of them at 64 listed) needs nothing more of the
+// record and no barrier.
+template <typename T, int U>
+__global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs)
 {
     constexpr int W = Row<T>::W;
-    __shared__ Teacher te;
+    __shared__ Listed li;
     const int64_t r = row0 + blockIdx.x / segs;
-    const int seg = blockIdx.x % segs, tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
-    const Row<T> row(a.in.logits, r * a.in.stride, a.in.vocab);
+    const int k0 = (int)(blockIdx.x % segs) * (kNT * U);
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
     T *out = static_cast<T *>(a.d_logits) + r * a.d_stride;
-    const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
+    const Row<T> row(static_cast<const T *>(a.in.logits) + r * a.in.stride, a.in.vocab);
+    const int32_t *index = a.top_index + r * K;
+    const float *value = a.top_value + r * K;
+    const RowPart<T, kNT, U> seg(row, k0);   // on its way while the record is read
     const float dl = a.d_loss[r];
     const float m = a.stats[4 * r], ln = a.stats[4 * r + 1];
     const float tm = a.stats[4 * r + 2], tln = a.stats[4 * r + 3];
-    const double w = (double)dl * (double)a.in.scale;
-    const Scale k(a.in.c);
-    if (tid < kWave)
-        read_teacher(te, a.top_index + r * K, a.top_value + r * K, K, a.mode, row.p, a.in.vocab, k,
-                     a.in.scale, lane);
-    __syncthreads();   // in place: the listed logits are read before any is overwritten
-    const bool zero = !te.any || dl == 0.0f;
-    if (zero || te.bad || m == -kInf) {
-        fill_row(row, out, k0, k1, te.bad && !zero ? __builtin_nanf("") : 0.0f);
+    const bool renorm = a.mode == ZERO_DISTILL_RENORM;
+    const int first = k0 * W - row.phase, last = first + kNT * U * W;   // the workgroup's elements
+    bool some = false, bad = false, here = false;
+    float top = kLowest;
+    for (int k = lane; k < K; k += kWave) {
+        const int id = index[k];
+        const float v = value[k];
+        some = some || id >= 0 || v != v;
+        bad = bad || id >= a.in.vocab || v != v;
+        here = here || (id >= 0 && id < a.in.vocab && id >= first && id < last);
+        if (id >= 0 && id < a.in.vocab)
+            top = __builtin_fmaxf(top, v);
+    }
+    some = __any(some);
+    bad = __any(bad);
+    here = __any(here);
+    const bool zero = !some || dl == 0.0f;
+    if (zero || bad || m == -kInf) {
+        fill_row(row, out, k0, k0 + kNT * U, bad && !zero ? __builtin_nanf("") : 0.0f);
         return;
     }
-    if (tm == -kInf) {
-        fill_row(row, out, k0, k1, 0.0f);
-    } else {
-        // ln p_rest, then log2 of the tail's softmax = t - off
-        const float c = k.c, ref = tm * c;
-        const float rest_ln = (float)(((double)tm - (double)m) * (double)a.in.scale + ((double)tln - (double)ln));
-        const float off = residue(tm, k) + tln * kLog2E;
-        const float coef = (float)(w * (te.total * (double)pow2(rest_ln * kLog2E) - te.rest)) * pow2(-off);
-        if (__builtin_fabsf(tm) > k.big)
-            map_row(row, out, k0, k1, -1, 0.0f, [&](float x) { return coef * pow2((x - tm) * c); });
-        else
-            map_row(row, out, k0, k1, -1, 0.0f,
-                    [&](float x) { return coef * pow2(__builtin_fmaf(x, c, -ref)); });
+    top = renorm ? wave_max(top) : 0.0f;
+    double sum = 0.0;
+    for (int k = lane; k < K; k += kWave) {
+        const int id = index[k];   // below vocab: the row is not bad
+        const double q = id >= 0 ? exp64((double)value[k] - (double)top) : 0.0;
+        sum += q;
+        if (here && tid < kWave) {   // the first wave leaves the record for the listed tokens
+            li.index[k] = id;
+            li.q[k] = q;
+            // an entry of padding is no element, also where the row's first chunk
+            // starts before the row (first < 0)
+            li.logit[k] = id >= 0 && id >= first && id < last ? row.at(id) : 0.0f;
+        }
     }
+    sum = wave_sum(sum);
+    double total, rest;
+    teacher_total(sum, renorm, total, rest);
+    // where the record may name the whole vocabulary, no token may be left for the
+    // rest (the statistics say whether one has a probability, not whether it is there)
+    if (K >= a.in.vocab && rest != 0.0 && tokens_named(index, K, a.in.vocab, lane) == a.in.vocab) {
+        total -= rest;
+        rest = 0.0;
+    }
+    const double w = (double)dl * (double)a.in.scale;
+    const Scale k(a.in.c);
+    // ln p_rest, then log2 of the tail's softmax = t - off
+    const float ref = tm * k.c, off = residue(tm, k) + tln * kLog2E;
+    const float rest_ln = (float)(((double)tm - (double)m) * (double)a.in.scale + ((double)tln - (double)ln));
+    const float coef = (float)(w * (total * (double)pow2(rest_ln * kLog2E) - rest)) * pow2(-off);
+    if (here)   // in place: the listed logits are read before any is overwritten
+        __syncthreads();
+    if (tm == -kInf)
+        fill_row(row, out, k0, k0 + kNT * U, 0.0f);
+    else if (__builtin_fabsf(tm) > k.big)
+        seg.map(row, out, [&](float x) { return coef * pow2((x - tm) * k.c); });
+    else
+        seg.map(row, out, [&](float x) { return coef * pow2(__builtin_fmaf(x, k.c, -ref)); });
+    if (!here)
+        return;
     __syncthreads();
-    // the listed tokens of this segment
-    const int id = tid < K ? te.lead[tid] : -1, at = id + row.phase;
-    if (id >= 0 && at >= k0 * W && at < k1 * W)
-        store_one(out + id, listed_grad(te, tid, m, residue(m, k) + ln * kLog2E, w, k));
+    // the listed tokens of this workgroup, each by its first entry
+    const double part = renorm ? sum == 0.0 ? 0.0 : 1.0 / sum : 1.0;
+    const float whole_off = residue(m, k) + ln * kLog2E;
+    for (int i = tid; i < K; i += kNT) {
+        const int id = li.index[i];
+        if (id < first || id >= last || id < 0 || id >= a.in.vocab)
+            continue;
+        double q = 0.0;
+        bool lead = true;
+        for (int o = 0; o < K; ++o)
+            if (li.index[o] == id) {
+                q += li.q[o];
+                lead = lead && o >= i;
+            }
+        const float p = pow2(rel(li.logit[i], m, m * k.c, k) - whole_off);
+        if (lead)
+            store_one(out + id, (float)(w * (total * (double)p - q * part)));
+    }
 }
 
 // Forward and backward of whole rows, at most kHeld NT chunks each.  The first
@@ -427,8 +509,10 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
     __shared__ unsigned bitmap[kSets][kWords];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
     const Scale k(a.in.c);
-    auto row_at = [&](int64_t r) { return Row<T>(a.in.logits, r * a.in.stride, a.in.vocab); };
     auto out_at = [&](int64_t r) { return static_cast<T *>(b.d_logits) + r * b.d_stride; };
+    auto row_at = [&](int64_t r) {
+        return Row<T>(static_cast<const T *>(a.in.logits) + r * a.in.stride, a.in.vocab);
+    };
     auto skip_padding = [&](int64_t r) {
         while (r < a.in.rows && is_padding(a.top_index + r * K, a.top_value + r * K, K, lane)) {
             const Row<T> row = row_at(r);
@@ -449,7 +533,8 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
         return;
-    held.load(row_at(r));
+    held.read(row_at(r));
+    held.take(row_at(r));
     if (tid < kWave)
         read_record(r, held.row, 0);
     __syncthreads();
@@ -499,8 +584,9 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
             fill_row<T, NT>(held.row, out, 0, held.row.chunks,
                             fill && te.bad && dl != 0.0f ? __builtin_nanf("") : 0.0f);
         else if (big)   // rare: from memory, so that the held row's loop is not written twice
-            map_row<T, NT>(held.row, out, 0, held.row.chunks, -1, 0.0f,
-                           [&](float x) { return coef * pow2((x - m) * k.c); });
+            for (int k0 = 0; k0 < held.row.chunks; k0 += NT)
+                RowPart<T, NT, 1>(held.row, k0).map(held.row, out,
+                                                    [&](float x) { return coef * pow2((x - m) * k.c); });
         held.map(out, !fill && !t.empty() && !big, next,
                  [&](float x) { return coef * pow2(__builtin_fmaf(x, k.c, -ref)); });
         __syncthreads();
@@ -570,15 +656,16 @@ int launch_distill(const DistillArgs &a, int32_t segs, void *stream)
 int launch_distill_grad(const DistillGradArgs &a, void *stream)
 {
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    constexpr int U = 4;
     const bool bf = a.in.dtype == ZERO_BF16;
-    const int segs = bf ? grad_segments<uint16_t>(a.in.vocab) : grad_segments<float>(a.in.vocab);
-    const int cps = bf ? chunks_per<uint16_t>(a.in.vocab, segs) : chunks_per<float>(a.in.vocab, segs);
+    const int chunks = bf ? chunks_per<uint16_t>(a.in.vocab, 1) : chunks_per<float>(a.in.vocab, 1);
+    const int segs = (chunks + kNT * U - 1) / (kNT * U);
     return each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
         const dim3 grid(n * (unsigned)segs), block(kNT);
         if (bf)
-            hipLaunchKernelGGL((distill_grad_kernel<uint16_t>), grid, block, 0, st, a, r, segs, cps);
+            hipLaunchKernelGGL((distill_grad_kernel<uint16_t, U>), grid, block, 0, st, a, r, segs);
         else
-            hipLaunchKernelGGL((distill_grad_kernel<float>), grid, block, 0, st, a, r, segs, cps);
+            hipLaunchKernelGGL((distill_grad_kernel<float, U>), grid, block, 0, st, a, r, segs);
     });
 }
 

@@ -330,7 +330,8 @@ __global__ __launch_bounds__(kNT) void logprob_kernel(LogprobArgs a, int64_t row
             pad_logprob(a, row_i);
         return;
     }
-    const Row<T> row(a.in.logits, row_i * a.in.stride, a.in.vocab);
+    const T *p = static_cast<const T *>(a.in.logits) + row_i * a.in.stride;
+    const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
     const Scale sc(a.in.c);
@@ -465,41 +466,43 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
 
 // d_logits_j = scale (d_lp ([j = t] - p_j) - d_H p_j (ln p_j + H)).  With p_j =
 // 2^t inv this is [j = t] scale d_lp - p_j (u + v t), u and v the row's.
+// One workgroup per kNT chunks of a row, one to a thread: neighbouring workgroups
+// sweep the memory in order, as a copy does.
 template <typename T, bool ENT>
-__global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, int64_t row0, int segs,
-                                                           int cps)
+__global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, int64_t row0, int segs)
 {
     const int64_t r = row0 + blockIdx.x / segs;
-    const int seg = blockIdx.x % segs;
-    const Row<T> row(a.in.logits, r * a.in.stride, a.in.vocab);
+    const int k0 = (int)(blockIdx.x % segs) * kNT;
     T *out = static_cast<T *>(a.d_logits) + r * a.d_stride;
-    const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
+    const Row<T> row(static_cast<const T *>(a.in.logits) + r * a.in.stride, a.in.vocab);
+    const RowPart<T, kNT, 1> seg(row, k0);   // on its way while the row's values are read
     const int64_t tok = a.tokens ? a.tokens[r] : 0;
     const float dl = a.d_logprob ? a.d_logprob[r] : 0.0f;
     const float dh = ENT ? a.d_entropy[r] : 0.0f;
     const float m = a.stats[2 * r], ln = a.stats[2 * r + 1];
     const bool zero = tok < 0 || (dl == 0.0f && dh == 0.0f), bad = tok >= a.in.vocab;
     if (zero || bad || m == -kInf) {
-        fill_row(row, out, k0, k1, bad && !zero ? __builtin_nanf("") : 0.0f);
+        fill_row(row, out, k0, k0 + kNT, bad && !zero ? __builtin_nanf("") : 0.0f);
         return;
     }
     const Scale k(a.in.c);
-    const float c = k.c, ref = m * c;
     // log2 p = t - off
-    const float off = residue(m, k) + ln * kLog2E;
+    const float ref = m * k.c, off = residue(m, k) + ln * kLog2E;
     const float inv = pow2(-off);
     const float h = ENT ? a.entropy[r] : 0.0f;
-    const float u = a.in.scale * (dl + dh * (h - off * kLn2)) * inv;
-    const float v = a.in.scale * dh * kLn2 * inv;
-    const int hot = a.d_logprob ? (int)tok : -1;
-    const float add = a.in.scale * dl;
-    auto grad = [&](float t) {
-        return pow2(t) * (ENT ? __builtin_fmaf(-v, __builtin_fmaxf(t, kTiny), -u) : -u);
-    };
+    const float u = -a.in.scale * (dl + dh * (h - off * kLn2)) * inv;
+    const float v = -a.in.scale * dh * kLn2 * inv;
+    // the given token's thread; in place: it reads the logit before it writes
+    const bool mine = a.d_logprob && owner_of<T, kNT>(row, (int)tok, k0, kNT) == (int)threadIdx.x;
+    const float l = mine ? row.at((int)tok) : 0.0f;
+    auto grad = [&](float t) { return pow2(t) * (ENT ? __builtin_fmaf(v, __builtin_fmaxf(t, kTiny), u) : u); };
     if (__builtin_fabsf(m) > k.big)
-        map_row(row, out, k0, k1, hot, add, [&](float x) { return grad((x - m) * c); });
+        seg.map(row, out, [&](float x) { return grad((x - m) * k.c); });
     else
-        map_row(row, out, k0, k1, hot, add, [&](float x) { return grad(__builtin_fmaf(x, c, -ref)); });
+        seg.map(row, out, [&](float x) { return grad(__builtin_fmaf(x, k.c, -ref)); });
+    // after the same thread's own store of the element
+    if (mine)
+        store_one(out + tok, grad(rel(l, m, ref, k)) + a.in.scale * dl);
 }
 
 // Forward and backward of whole rows, at most kHeld NT chunks each.
@@ -509,8 +512,10 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
 {
     constexpr int N = HeldRow<T, NT, SAME>::G * Row<T>::W;
     __shared__ Total tot[2][NT / kWave];
-    auto row_at = [&](int64_t r) { return Row<T>(a.in.logits, r * a.in.stride, a.in.vocab); };
     auto out_at = [&](int64_t r) { return static_cast<T *>(b.d_logits) + r * b.d_stride; };
+    auto row_at = [&](int64_t r) {
+        return Row<T>(static_cast<const T *>(a.in.logits) + r * a.in.stride, a.in.vocab);
+    };
     // The next row from r on that is not padding (padding rows are finished on
     // the way), or a.in.rows.
     auto skip_padding = [&](int64_t r) {
@@ -527,7 +532,8 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
         return;
-    held.load(row_at(r));
+    held.read(row_at(r));
+    held.take(row_at(r));
     for (int turn = 0;; turn ^= 1) {
         const float l = token_logit<T>(a, r);   // in place: before it is overwritten
         const int64_t tok = a.tokens ? a.tokens[r] : 0;
@@ -558,14 +564,16 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
         };
         if (fill)
             fill_row<T, NT>(held.row, out, 0, held.row.chunks, bad && !zero ? __builtin_nanf("") : 0.0f);
-        else if (big)   // rare: from memory, so that the held row's loop is not written twice
-            map_row<T, NT>(held.row, out, 0, held.row.chunks, b.d_logprob ? (int)tok : -1,
-                           a.in.scale * dl, [&](float x) { return grad((x - m) * k.c); });
-        const bool write = !fill && !big;
-        const int owner = b.d_logprob && write ? held.owner((int)tok) : -1;
-        held.map(out, write, next, [&](float x) { return grad(__builtin_fmaf(x, k.c, -ref)); });
-        if ((int)threadIdx.x == owner)   // after its own store of the element
-            store_one(out + tok, grad(__builtin_fmaf(l, k.c, -ref)) + a.in.scale * dl);
+        else if (big) {   // rare: from memory, so that the held row's code is not there twice
+            for (int k0 = 0; k0 < held.row.chunks; k0 += NT)
+                RowPart<T, NT, 1>(held.row, k0).map(held.row, out, [&](float x) { return grad((x - m) * k.c); });
+            __syncthreads();
+        }
+        held.map(out, !fill && !big, next, [&](float x) { return grad(__builtin_fmaf(x, k.c, -ref)); });
+        // the given token's, after its thread's own store of the element
+        const int owner = owner_of<T, NT>(held.row, (int)tok, 0, held.row.chunks);
+        if (b.d_logprob && !fill && (int)threadIdx.x == (big ? 0 : owner))
+            store_one(out + tok, grad(rel(l, m, ref, k)) + a.in.scale * dl);
         held.take(next);
         if (rn >= a.in.rows)
             return;
@@ -639,18 +647,17 @@ int launch_logprob_grad(const LogprobGradArgs &a, void *stream)
 {
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     const bool bf = a.in.dtype == ZERO_BF16, ent = a.d_entropy != nullptr;
-    const int segs = bf ? grad_segments<uint16_t>(a.in.vocab) : grad_segments<float>(a.in.vocab);
-    const int cps = bf ? chunks_per<uint16_t>(a.in.vocab, segs) : chunks_per<float>(a.in.vocab, segs);
+    const int segs = ((bf ? chunks_per<uint16_t>(a.in.vocab, 1) : chunks_per<float>(a.in.vocab, 1)) + kNT - 1) / kNT;
     return each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
         const dim3 grid(n * (unsigned)segs), block(kNT);
         if (bf && ent)
-            hipLaunchKernelGGL((logprob_grad_kernel<uint16_t, true>), grid, block, 0, st, a, r, segs, cps);
+            hipLaunchKernelGGL((logprob_grad_kernel<uint16_t, true>), grid, block, 0, st, a, r, segs);
         else if (bf)
-            hipLaunchKernelGGL((logprob_grad_kernel<uint16_t, false>), grid, block, 0, st, a, r, segs, cps);
+            hipLaunchKernelGGL((logprob_grad_kernel<uint16_t, false>), grid, block, 0, st, a, r, segs);
         else if (ent)
-            hipLaunchKernelGGL((logprob_grad_kernel<float, true>), grid, block, 0, st, a, r, segs, cps);
+            hipLaunchKernelGGL((logprob_grad_kernel<float, true>), grid, block, 0, st, a, r, segs);
         else
-            hipLaunchKernelGGL((logprob_grad_kernel<float, false>), grid, block, 0, st, a, r, segs, cps);
+            hipLaunchKernelGGL((logprob_grad_kernel<float, false>), grid, block, 0, st, a, r, segs);
     });
 }
 

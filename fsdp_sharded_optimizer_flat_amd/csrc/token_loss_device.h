@@ -73,10 +73,7 @@ struct Chunk<float> {
     }
 };
 
-// Stores a chunk's gradients, rounded once, at any element alignment (gfx950
-// takes 16-byte stores at every address; a row whose gradient sits at another
-// 16-byte phase than its logits needs them).
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
+// A chunk's gradients, each rounded once.
 template <typename T, int W>
 __device__ __forceinline__ u32x4 pack_chunk(const float (&g)[W])
 {
@@ -87,13 +84,47 @@ __device__ __forceinline__ u32x4 pack_chunk(const float (&g)[W])
         return u32x4{__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
                      __float_as_uint(g[3])};
 }
-template <typename T, int W>
-__device__ __forceinline__ void store_chunk(T *p, const float (&g)[W])
+// Stores 16 bytes at any element's address (gfx950 takes such stores), for
+// gradients whose rows sit at another 16-byte phase than their logits: reading
+// the logits unaligned instead measured slower (777 x 50257 fp32, loss and
+// gradient: 72 us, and 80 to 93 us with unaligned loads).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <typename T>
+__device__ __forceinline__ void store_any(u32x4 v, T *p)
 {
-    __builtin_nontemporal_store(pack_chunk<T>(g), reinterpret_cast<u32x4_any *>(p));
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(p));
 }
 __device__ __forceinline__ void store_one(uint16_t *p, float g) { *p = to_bf16(g); }
 __device__ __forceinline__ void store_one(float *p, float g) { *p = g; }
+
+// p, which is the same in every lane, in scalar registers.
+template <typename T>
+__device__ __forceinline__ T *scalar(const T *p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+    return reinterpret_cast<T *>(u);
+}
+// `chunks` chunks from p on as a buffer: what lies past them is neither read nor
+// written.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const T *p, int chunks)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(scalar(p), 0, __builtin_amdgcn_readfirstlane(chunks) * 16,
+                                             kRawBufferWord3);
+}
+// Stores chunk `tid` of a window of `chunks` chunks from p on, written through
+// to memory.  Each store has a window of its own, no offset in a scalar register:
+// MI355X has stored what the next instruction wrote to the data registers of a
+// 16-byte buffer store with such an offset (the compiler leaves no wait between
+// the two then).
+template <typename T>
+__device__ __forceinline__ void store_chunks(u32x4 v, T *p, int chunks)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(v, window(p, chunks), (int)threadIdx.x * 16, 0,
+                                           kSpanStorePolicy);
+}
 
 // A row cut into chunks that start at 16-byte boundaries: chunk k holds
 // elements k W - phase .. + W - 1, whole for full_lo <= k < full_hi; the first
@@ -104,9 +135,8 @@ struct Row {
     const T *p;
     int vocab, phase, chunks, full_lo, full_hi;
     __device__ __forceinline__ Row() : p(nullptr), vocab(0), phase(0), chunks(0), full_lo(0), full_hi(0) {}
-    __device__ __forceinline__ Row(const void *base, int64_t off, int vocab_) : vocab(vocab_)
+    __device__ __forceinline__ Row(const T *p_, int vocab_) : p(p_), vocab(vocab_)
     {
-        p = static_cast<const T *>(base) + off;
         phase = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
         chunks = (vocab + phase + W - 1) / W;
         full_lo = phase ? 1 : 0;
@@ -314,39 +344,73 @@ __device__ __forceinline__ float log_prob(float l, const Total &t, float log2s, 
 
 // -- rows mapped to gradients ----------------------------------------------------------------
 
-// Visits chunks [k0, k1) of a row of logits and writes what f(logit) returns to
-// the same elements of the gradient's row; element `hot` gets `add` more.
-template <typename T, int NT = kNT, typename F>
-__device__ __forceinline__ void map_row(const Row<T> &row, T *out, int k0, int k1, int hot, float add,
-                                        F f)
+// The gradients of a chunk.
+template <typename T, typename F>
+__device__ __forceinline__ u32x4 map_chunk(const Chunk<T> &c, F f)
 {
-    constexpr int W = Row<T>::W;
-    const int tid = threadIdx.x;
-    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    const int hot_k = hot < 0 ? -1 : (hot + row.phase) / W, hot_i = (hot + row.phase) & (W - 1);
-    for (int k = lo + tid; k < hi; k += NT) {
-        Chunk<T> ch;
-        ch.stream(row.chunk(k));
-        float x[W], g[W];
-        ch.widen(x);
+    constexpr int W = Chunk<T>::W;
+    float x[W], g[W];
+    c.widen(x);
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            g[i] = f(x[i]);
-        if (k == hot_k) {
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                g[i] = i == hot_i ? g[i] + add : g[i];
-        }
-        store_chunk(out + (k * W - row.phase), g);
-    }
-    const int e = tid < 2 * W ? row.edge(tid, k0, k1) : -1;
-    if (e >= 0) {
-        const float g = f(row.at(e));
-        store_one(out + e, e == hot ? g + add : g);
-    }
+    for (int i = 0; i < W; ++i)
+        g[i] = f(x[i]);
+    return pack_chunk<T>(g);
 }
 
-// The same value in every element, without reading the logits.
+// The thread that holds element x of chunks [k0, k0 + n) of a row gone through NT
+// at a time, or -1.
+template <typename T, int NT>
+__device__ __forceinline__ int owner_of(const Row<T> &row, int x, int k0, int n)
+{
+    constexpr int W = Row<T>::W;
+    const int at = x + row.phase, k = at / W;
+    return k < k0 || k >= k0 + n ? -1 : k < row.full_lo ? at
+           : k < row.full_hi     ? (k - max(k0, row.full_lo)) % NT : W + (at & (W - 1));
+}
+
+// Chunks [k0, k0 + NT U) of a row of logits, U to a thread: read when it is made,
+// then mapped to the gradient's row.
+template <typename T, int NT, int U>
+struct RowPart {
+    static constexpr int W = Row<T>::W;
+    int lo, hi, e;
+    Chunk<T> ch[U];
+    float edge;
+    __device__ __forceinline__ RowPart(const Row<T> &row, int k0)
+        : lo(max(k0, row.full_lo)), hi(min(k0 + NT * U, row.full_hi))
+    {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (lo + tid + NT * u < hi)
+                ch[u].stream(row.chunk(lo + tid + NT * u));
+        e = tid < 2 * W ? row.edge(tid, k0, k0 + NT * U) : -1;
+        edge = e >= 0 ? row.at(e) : 0.0f;
+    }
+    // Writes f(logit).
+    template <typename F>
+    __device__ __forceinline__ void map(const Row<T> &row, T *out, F f) const
+    {
+        T *first = out + (lo * W - row.phase);
+        const bool same = (reinterpret_cast<uintptr_t>(first) & 15) == 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int n = hi - lo - NT * u;
+            if (n <= 0)
+                continue;
+            const u32x4 g = map_chunk(ch[u], f);
+            if (same)
+                store_chunks(g, first + NT * W * u, n);
+            else if ((int)threadIdx.x < n)
+                store_any(g, first + NT * W * u + threadIdx.x * W);
+        }
+        if (e >= 0)
+            store_one(out + e, f(edge));
+    }
+};
+
+// The same value in every element of chunks [k0, k1), without reading the
+// logits.
 template <typename T, int NT = kNT>
 __device__ __forceinline__ void fill_row(const Row<T> &row, T *out, int k0, int k1, float v)
 {
@@ -356,8 +420,9 @@ __device__ __forceinline__ void fill_row(const Row<T> &row, T *out, int k0, int 
 #pragma unroll
     for (int i = 0; i < W; ++i)
         g[i] = v;
+    const u32x4 x = pack_chunk<T>(g);
     for (int k = lo + (int)threadIdx.x; k < hi; k += NT)
-        store_chunk(out + (k * W - row.phase), g);
+        store_any(x, out + (k * W - row.phase));
     const int e = (int)threadIdx.x < 2 * W ? row.edge(threadIdx.x, k0, k1) : -1;
     if (e >= 0)
         store_one(out + e, v);
@@ -368,9 +433,8 @@ __device__ __forceinline__ void fill_row(const Row<T> &row, T *out, int k0, int 
 // One workgroup of NT threads holds a row of up to kHeld chunks a thread in its
 // registers: the logits are read from memory once, summed as they arrive, and
 // turned into gradients from the registers.  The workgroup goes through rows
-// gridDim.x apart, and as soon as a chunk's gradients are on their way its
-// registers take the same chunk of the next row, so that memory is read and
-// written at the same time and idles only while a row is summed.
+// gridDim.x apart: once a row's gradients are on their way its registers take the
+// next row, so that the loads wait behind the stores and not behind their end.
 
 constexpr int kHeld = 16;
 
@@ -385,28 +449,6 @@ struct HeldRow {
     float edge;   // this thread's element of the row's partial first or last chunk
     int e;        // and its index, or -1
 
-    // p, which is the same in every lane, in scalar registers.
-    static __device__ __forceinline__ T *scalar(const T *p)
-    {
-        const uint64_t v = reinterpret_cast<uint64_t>(p);
-        const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 |
-                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
-        return reinterpret_cast<T *>(u);
-    }
-    // `chunks` chunks from p on as a buffer: what lies past them is neither read
-    // nor written.
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const T *p, int chunks)
-    {
-        return __builtin_amdgcn_make_buffer_rsrc(scalar(p), 0,
-                                                 __builtin_amdgcn_readfirstlane(chunks) * 16,
-                                                 kRawBufferWord3);
-    }
-    __device__ __forceinline__ void load_chunk(__amdgpu_buffer_rsrc_t rs, int i)
-    {
-        ch[i].r = __builtin_bit_cast(decltype(ch[i].r),
-                                     __builtin_amdgcn_raw_buffer_load_b128(
-                                         rs, (int)threadIdx.x * 16, NT * 16 * i, kLoadStreamPolicy));
-    }
     __device__ __forceinline__ void take(const Row<T> &next)
     {
         row = next;
@@ -414,14 +456,17 @@ struct HeldRow {
         e = (int)threadIdx.x < 2 * W ? next.edge(threadIdx.x, 0, next.chunks) : -1;
         edge = e >= 0 ? next.at(e) : -kInf;
     }
-    // Reads a whole row.  Chunks past its end are not read.
-    __device__ __forceinline__ void load(const Row<T> &next)
+    // Reads a row's whole chunks.  What lies past them is not read.
+    __device__ __forceinline__ void read(const Row<T> &next)
     {
-        const __amdgpu_buffer_rsrc_t rs = window(next.chunk(next.full_lo), next.full_hi - next.full_lo);
+        const int m = next.full_hi - next.full_lo;
+        const T *first = scalar(next.chunk(next.full_lo));
+        const __amdgpu_buffer_rsrc_t rs = window(first, m);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            load_chunk(rs, i);
-        take(next);
+            ch[i].r = __builtin_bit_cast(decltype(ch[i].r),
+                                         __builtin_amdgcn_raw_buffer_load_b128(
+                                             rs, (int)threadIdx.x * 16, NT * 16 * i, kLoadStreamPolicy));
     }
     // Visits the groups of G chunks that hold anything: f(first chunk, values).
     // Values past the row's whole chunks are -inf.
@@ -452,12 +497,11 @@ struct HeldRow {
         }
     }
     // Writes f(logit) for every element the thread holds (nothing unless
-    // `write`) and reads `next` (which may be empty) into its place.  `out`: the
+    // `write`), then reads `next` (which may be empty) into its place.  `out`: the
     // gradient's row.
     template <typename F>
     __device__ __forceinline__ void map(T *out, bool write, const Row<T> &next, F f)
     {
-        const __amdgpu_buffer_rsrc_t from = window(next.chunk(next.full_lo), next.full_hi - next.full_lo);
         T *first = scalar(out + (row.full_lo * W - row.phase));
         const int m = write ? n : 0;
 #pragma unroll
@@ -465,41 +509,17 @@ struct HeldRow {
             // opaque, or the widened logits of the sums would be kept from there
             asm volatile("" : "+v"(ch[i].r));
             if constexpr (SAME) {
-                // The chunk's own window, not an offset in a scalar register:
-                // MI355X has stored what the next instruction wrote to the data
-                // registers of a 16-byte buffer store with such an offset (the
-                // compiler leaves no wait between the two then).
                 if (NT * i < m)
-                    __builtin_amdgcn_raw_buffer_store_b128(mapped(ch[i], f),
-                                                           window(first + NT * W * i, m - NT * i),
-                                                           (int)threadIdx.x * 16, 0, kSpanStorePolicy);
+                    store_chunks(map_chunk(ch[i], f), first + NT * W * i, m - NT * i);
             } else {
                 if ((int)threadIdx.x < m - NT * i)
-                    __builtin_nontemporal_store(
-                        mapped(ch[i], f),
-                        reinterpret_cast<u32x4_any *>(first + NT * W * i + threadIdx.x * (unsigned)W));
+                    store_any(map_chunk(ch[i], f), first + NT * W * i + threadIdx.x * (unsigned)W);
             }
-            load_chunk(from, i);
             __builtin_amdgcn_sched_barrier(0);
         }
+        read(next);
         if (e >= 0 && write)
             store_one(out + e, f(edge));
-    }
-    // The thread that holds element x of the row (0 <= x < vocab).
-    __device__ __forceinline__ int owner(int x) const
-    {
-        const int at = x + row.phase, k = at / W;
-        return k < row.full_lo ? at : k < row.full_hi ? (k - row.full_lo) % NT : W + (at & (W - 1));
-    }
-    template <typename F>
-    static __device__ __forceinline__ u32x4 mapped(const Chunk<T> &c, F f)
-    {
-        float x[W], g[W];
-        c.widen(x);
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            g[j] = f(x[j]);
-        return pack_chunk<T>(g);
     }
 };
 
@@ -544,7 +564,7 @@ int held_threads(int vocab)
 inline unsigned held_grid(int64_t rows, int threads)
 {
     const int64_t most = (int64_t)device_cu_count() * (1024 / threads);
-    return (unsigned)std::max<int64_t>(1, std::min(rows, most));
+    return (unsigned)(rows <= 4 * most ? rows : most);
 }
 
 // Every row of the gradient starts at its logits' 16-byte phase.
@@ -553,14 +573,6 @@ inline bool same_phase(const LossRows &in, const void *d_logits, int64_t d_strid
     const uint64_t es = in.dtype == ZERO_BF16 ? 2 : 4;
     const uint64_t base = (uint64_t)(uintptr_t)in.logits ^ (uint64_t)(uintptr_t)d_logits;
     return base % 16 == 0 && (uint64_t)(in.stride - d_stride) * es % 16 == 0;
-}
-
-// Workgroups per row of a gradient pass: 8 chunks per thread.
-template <typename T>
-int grad_segments(int vocab)
-{
-    constexpr int W = 16 / (int)sizeof(T);
-    return (vocab + 8 * kNT * W - 1) / (8 * kNT * W);
 }
 
 }  // namespace dev
