@@ -529,7 +529,9 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
                     a.in.vocab, lane);
         read_teacher(teacher[set], index, value, K, a.mode, row.p, a.in.vocab, k, a.in.scale, lane);
     };
+    __shared__ u32x4 park[NT * parked(NT) + 1];
     HeldRow<T, NT, SAME> held;
+    held.park = park;
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
         return;

@@ -528,7 +528,9 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
         return r;
     };
     const Scale k(a.in.c);
+    __shared__ u32x4 park[NT * parked(NT) + 1];
     HeldRow<T, NT, SAME> held;
+    held.park = park;
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
         return;

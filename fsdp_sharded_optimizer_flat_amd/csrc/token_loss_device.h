@@ -40,6 +40,9 @@ constexpr float kTiny = -1000.0f;       // t of a probability that is zero, for 
 
 // -- loading -------------------------------------------------------------------------
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
 // 16 bytes of a row: W elements.
 template <typename T>
 struct Chunk;
@@ -54,8 +57,12 @@ struct Chunk<uint16_t> {
     }
     __device__ __forceinline__ void widen(float (&x)[W]) const
     {
-        x[0] = bf_lo(r.x), x[1] = bf_hi(r.x), x[2] = bf_lo(r.y), x[3] = bf_hi(r.y);
-        x[4] = bf_lo(r.z), x[5] = bf_hi(r.z), x[6] = bf_lo(r.w), x[7] = bf_hi(r.w);
+        // as a conversion: the compiler then knows that no value is a signalling
+        // NaN and takes their maximum without quieting each first
+        const f32x8 v = __builtin_convertvector(__builtin_bit_cast(bf16x8, r), f32x8);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            x[i] = v[i];
     }
 };
 template <>
@@ -228,19 +235,27 @@ struct Sum {
     template <int N, bool ENT, bool BIG>
     __device__ __forceinline__ void add_terms(const float (&x)[N], const Scale &k)
     {
-        // a group's sums apart from the lane's: shorter chains round less
-        float sg = 0, ag = 0;
+        // a group's sums apart from the lane's, as trees: they round less, and no
+        // addition waits for the exponential before it
+        float e[N], b[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float t = BIG ? rel(x[i], m, r, k) : __builtin_fmaf(x[i], k.c, -r);
-            const float e = pow2(t);
-            sg += e;
+            e[i] = pow2(t);
             if constexpr (ENT)
-                ag = __builtin_fmaf(e, __builtin_fmaxf(t, kTiny), ag);
+                b[i] = e[i] * __builtin_fmaxf(t, kTiny);
         }
-        s += sg;
+#pragma unroll
+        for (int w = 1; w < N; w *= 2)
+#pragma unroll
+            for (int i = 0; i + w < N; i += 2 * w) {
+                e[i] += e[i + w];
+                if constexpr (ENT)
+                    b[i] += b[i + w];
+            }
+        s += e[0];
         if constexpr (ENT)
-            a += ag;
+            a += b[0];
     }
 };
 
@@ -437,12 +452,18 @@ __device__ __forceinline__ void fill_row(const Row<T> &row, T *out, int k0, int 
 // next row, so that the loads wait behind the stores and not behind their end.
 
 constexpr int kHeld = 16;
+// Of these, the last chunks a thread parks in LDS once they are summed, which
+// leaves registers for what happens between the sums and the gradients (as many
+// as the workgroups resident on a compute unit have LDS for).
+constexpr int parked(int threads) { return threads >= 512 ? 4 : threads == 256 ? 2 : 0; }
 
 // SAME: the gradient's rows sit at the 16-byte phase of the logits' rows.
 template <typename T, int NT, bool SAME>
 struct HeldRow {
     static constexpr int W = Row<T>::W;
     static constexpr int G = 8 / W;       // chunks of a group that is summed at once
+    static constexpr int P = parked(NT), P0 = kHeld - P;
+    u32x4 *park;  // P NT chunks of LDS
     Row<T> row;
     int n;        // whole chunks
     Chunk<T> ch[kHeld];
@@ -478,6 +499,7 @@ struct HeldRow {
         for (int i = 0; i < kHeld; i += G) {
             if (NT * i < n) {
                 float x[W * G];
+                u32x4 raw[G];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
                     if (NT * (i + j + 1) > n) {   // at most one chunk of the row: kept a branch
@@ -485,6 +507,7 @@ struct HeldRow {
                         if (NT * (i + j) + (int)threadIdx.x >= n)
                             ch[i + j].r = __builtin_bit_cast(decltype(ch[0].r), u32x4{none, none, none, none});
                     }
+                    raw[j] = __builtin_bit_cast(u32x4, ch[i + j].r);
                     float y[W];
                     ch[i + j].widen(y);
 #pragma unroll
@@ -492,6 +515,10 @@ struct HeldRow {
                         x[j * W + w] = y[w];
                 }
                 f(i, x);
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    if (i + j >= P0)
+                        park[NT * (i + j - P0) + threadIdx.x] = __builtin_bit_cast(u32x4, raw[j]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -506,14 +533,17 @@ struct HeldRow {
         const int m = write ? n : 0;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            // opaque, or the widened logits of the sums would be kept from there
-            asm volatile("" : "+v"(ch[i].r));
+            Chunk<T> c = ch[i];
+            if (i >= P0)
+                c.r = __builtin_bit_cast(decltype(c.r), park[NT * (i - P0) + threadIdx.x]);
+            else   // opaque, or the widened logits of the sums would be kept from there
+                asm volatile("" : "+v"(c.r));
             if constexpr (SAME) {
                 if (NT * i < m)
-                    store_chunks(map_chunk(ch[i], f), first + NT * W * i, m - NT * i);
+                    store_chunks(map_chunk(c, f), first + NT * W * i, m - NT * i);
             } else {
                 if ((int)threadIdx.x < m - NT * i)
-                    store_any(map_chunk(ch[i], f), first + NT * W * i + threadIdx.x * (unsigned)W);
+                    store_any(map_chunk(c, f), first + NT * W * i + threadIdx.x * (unsigned)W);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
