@@ -15,7 +15,7 @@ struct Teacher {
     double token_q[ZERO_MAX_TOP];   // the token's probability over all entries that name it
     double total, rest;             // sum of q and rest; the other tokens' probability
     double cross;                   // sum of q (ln q - scale (logit - listed_max))
-    alignas(16) int index[ZERO_MAX_TOP];   // the token; -1: no token of the vocabulary
+    int index[ZERO_MAX_TOP];        // the token; -1: no token of the vocabulary
     int lead[ZERO_MAX_TOP];         // the token where this is the first entry that names it, else -1
     float value[ZERO_MAX_TOP];
     float logit[ZERO_MAX_TOP];      // the student's
@@ -29,6 +29,7 @@ struct Listed {
     double q[ZERO_MAX_TOP];
     int index[ZERO_MAX_TOP];
     float logit[ZERO_MAX_TOP];
+    bool twice;
 };
 
 // Orders a wave's LDS writes before its lanes' later reads.
@@ -74,15 +75,15 @@ __device__ __forceinline__ double log64(double x)
 // an entropy, below 16 nats for any vocabulary here.
 constexpr double kLeastRest = 0x1p-20;
 
-// True (for every lane) where a record is padding: no entry, and no NaN value.
-__device__ __forceinline__ bool is_padding(const int32_t *index, const float *value, int K, int lane)
+// True where a record is padding: no entry, and no NaN value.
+__device__ __forceinline__ bool is_padding(const int32_t *index, const float *value, int K)
 {
-    bool some = false;
-    for (int k = lane; k < K; k += kWave) {
-        const float v = value[k];
-        some = some || index[k] >= 0 || v != v;
+    for (int k = 0; k < K; ++k) {
+        const float v = ld_uniform(value + k);
+        if (ld_uniform(index + k) >= 0 || v != v)
+            return false;
     }
-    return !__any(some);
+    return true;
 }
 
 // The teacher's total and the other tokens' probability from the sum over its
@@ -109,21 +110,41 @@ __device__ __forceinline__ int tokens_named(const int32_t *index, int K, int voc
     return wave_count(named);
 }
 
+// Clears a 16-byte aligned bitmap of `words` words (of a multiple of 4) and sets
+// the bits id + base in [0, end) of a record's tokens (one whole wave).  True
+// where one of them was set already: a token is named twice.
+__device__ __forceinline__ bool mark_listed(unsigned *bits, int words, const int32_t *index, int K,
+                                            int base, int end, int vocab, int lane)
+{
+    for (int i = lane; i < (words + 3) / 4; i += kWave)
+        reinterpret_cast<u32x4 *>(bits)[i] = u32x4{0, 0, 0, 0};
+    wave_sync();
+    bool twice = false;
+    for (int k = lane; k < K; k += kWave) {
+        const int id = index[k], at = id + base;
+        if (id >= 0 && id < vocab && at >= 0 && at < end) {
+            const unsigned was = atomicOr(&bits[at >> 5], 1u << (at & 31));
+            twice = twice || (was >> (at & 31) & 1);
+        }
+    }
+    return __any(twice);
+}
+
 // Reads a row's record and the listed tokens' logits (one whole wave calls it).
-// Loops over a lane's entries are kept rolled and the entries in LDS: the wave
+// `twice`: some token is named by several entries.  Loops over a lane's entries are kept rolled and the entries in LDS: the wave
 // may hold a row in its registers meanwhile.
 template <typename T>
 __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, const float *value,
                                              int K, int mode, const T *logits, int vocab,
-                                             const Scale &sc, float scale, int lane)
+                                             const Scale &sc, float scale, bool twice, int lane)
 {
     const bool renorm = mode == ZERO_DISTILL_RENORM;
     bool some = false, bad = false;
     float top = kLowest, lm = -kInf;
 #pragma nounroll
-    for (int k = lane; k < (K + 3) / 4 * 4; k += kWave) {
-        int id = k < K ? index[k] : -1;
-        const float val = k < K ? value[k] : 0.0f;
+    for (int k = lane; k < K; k += kWave) {
+        int id = index[k];
+        const float val = value[k];
         const bool nan = val != val;
         some = some || id >= 0 || nan;
         bad = bad || id >= vocab || nan;
@@ -165,13 +186,8 @@ __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, 
         const int id = te.index[k];
         const double q = te.q[k] * part;
         double token_q = q;
-        int same = 0;
-        for (int o = 0; o < K; o += 4) {
-            const int4 i = *reinterpret_cast<const int4 *>(&te.index[o]);
-            same += (i.x == id) + (i.y == id) + (i.z == id) + (i.w == id);
-        }
         bool lead = id >= 0;
-        if (lead && same > 1) {
+        if (lead && twice) {
             token_q = 0.0;
             for (int o = 0; o < K; ++o)
                 if (te.index[o] == id) {
@@ -273,21 +289,6 @@ __device__ __forceinline__ float listed_grad(const Teacher &te, int k, float m, 
     return (float)(w * (te.total * (double)p - te.token_q[k]));
 }
 
-// Marks the listed tokens of chunks [k0, k1) in `bits`, one bit per element of
-// the chunks (one whole wave).
-__device__ __forceinline__ void mark_listed(unsigned *bits, int words, const int32_t *index, int K,
-                                            int base, int end, int vocab, int lane)
-{
-    for (int i = lane; i < words; i += kWave)
-        bits[i] = 0;
-    wave_sync();
-    for (int k = lane; k < K; k += kWave) {
-        const int id = index[k], at = id + base;
-        if (id >= 0 && id < vocab && at >= 0 && at < end)
-            atomicOr(&bits[at >> 5], 1u << (at & 31));
-    }
-}
-
 // Words of a segment's bitmap: one bit per element of its chunks, whose first
 // and last may stick out of it.
 constexpr int kBitWords = (int)(kLossMaxSegment / 32) + 8;
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row
     constexpr int U = 4, W = Row<T>::W;
     __shared__ Total tot[kNW];
     __shared__ Teacher te;
-    __shared__ unsigned bits[kBitWords];
+    __shared__ alignas(16) unsigned bits[kBitWords];
     const int64_t row_i = row0 + blockIdx.x / segs;
     const int seg = blockIdx.x % segs, tid = threadIdx.x, K = a.top_k, lane = tid & (kWave - 1);
     const int32_t *index = a.top_index + row_i * K;
@@ -310,17 +311,17 @@ __global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row
     const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    if (is_padding(index, value, K, lane)) {
+    if (is_padding(index, value, K)) {
         if (segs == 1)
             pad_distill(a.loss, a.stats, row_i);
         return;
     }
     const Scale sc(a.in.c);
     if (tid < kWave) {
-        mark_listed(bits, ((k1 - k0) * W + 31) / 32, index, K, row.phase - k0 * W, (k1 - k0) * W,
-                    a.in.vocab, lane);
+        const bool twice = mark_listed(bits, ((k1 - k0) * W + 31) / 32, index, K, row.phase - k0 * W,
+                                       (k1 - k0) * W, a.in.vocab, lane);
         if (segs == 1)
-            read_teacher(te, index, value, K, a.mode, row.p, a.in.vocab, sc, a.in.scale, lane);
+            read_teacher(te, index, value, K, a.mode, row.p, a.in.vocab, sc, a.in.scale, twice, lane);
     }
     __syncthreads();
     Sum q;
@@ -375,14 +376,14 @@ __global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_
     const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
     const int32_t *index = a.top_index + r * K;
     const float *value = a.top_value + r * K;
-    if (is_padding(index, value, K, lane)) {
+    if (is_padding(index, value, K)) {
         pad_distill(a.loss, a.stats, r);
         return;
     }
     const Scale sc(a.in.c);
     if (tid < kWave)
         read_teacher(te, index, value, K, a.mode, static_cast<const T *>(a.in.logits) + r * a.in.stride,
-                     a.in.vocab, sc, a.in.scale, lane);
+                     a.in.vocab, sc, a.in.scale, true, lane);   // no bitmap of the row: look for them
     const Total t = join_parts(a.parts + r * segs, segs, sc, tot);
     if (tid == 0)
         finish_distill(te, t, a.in, a.loss, a.stats, r);
@@ -403,6 +404,7 @@ __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, in
 {
     constexpr int W = Row<T>::W;
     __shared__ Listed li;
+    __shared__ alignas(16) unsigned bits[kNT * U * W / 32];
     const int64_t r = row0 + blockIdx.x / segs;
     const int k0 = (int)(blockIdx.x % segs) * (kNT * U);
     const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
@@ -411,9 +413,9 @@ __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, in
     const int32_t *index = a.top_index + r * K;
     const float *value = a.top_value + r * K;
     const RowPart<T, kNT, U> seg(row, k0);   // on its way while the record is read
-    const float dl = a.d_loss[r];
-    const float m = a.stats[4 * r], ln = a.stats[4 * r + 1];
-    const float tm = a.stats[4 * r + 2], tln = a.stats[4 * r + 3];
+    const float dl = ld_uniform(a.d_loss + r);
+    const float m = ld_uniform(a.stats + 4 * r), ln = ld_uniform(a.stats + 4 * r + 1);
+    const float tm = ld_uniform(a.stats + 4 * r + 2), tln = ld_uniform(a.stats + 4 * r + 3);
     const bool renorm = a.mode == ZERO_DISTILL_RENORM;
     const int first = k0 * W - row.phase, last = first + kNT * U * W;   // the workgroup's elements
     bool some = false, bad = false, here = false;
@@ -450,6 +452,8 @@ __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, in
         }
     }
     sum = wave_sum(sum);
+    if (here && tid < kWave)
+        li.twice = mark_listed(bits, kNT * U * W / 32, index, K, -first, last - first, a.in.vocab, lane);
     double total, rest;
     teacher_total(sum, renorm, total, rest);
     // where the record may name the whole vocabulary, no token may be left for the
@@ -476,86 +480,140 @@ __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, in
         return;
     __syncthreads();
     // the listed tokens of this workgroup, each by its first entry
+    const bool look = li.twice;
     const double part = renorm ? sum == 0.0 ? 0.0 : 1.0 / sum : 1.0;
     const float whole_off = residue(m, k) + ln * kLog2E;
     for (int i = tid; i < K; i += kNT) {
         const int id = li.index[i];
         if (id < first || id >= last || id < 0 || id >= a.in.vocab)
             continue;
-        double q = 0.0;
+        double q = li.q[i];
         bool lead = true;
-        for (int o = 0; o < K; ++o)
-            if (li.index[o] == id) {
-                q += li.q[o];
-                lead = lead && o >= i;
-            }
+        if (look) {
+            q = 0.0;
+            for (int o = 0; o < K; ++o)
+                if (li.index[o] == id) {
+                    q += li.q[o];
+                    lead = lead && o >= i;
+                }
+        }
         const float p = pow2(rel(li.logit[i], m, m * k.c, k) - whole_off);
         if (lead)
             store_one(out + id, (float)(w * (total * (double)p - q * part)));
     }
 }
 
-// Forward and backward of whole rows, at most kHeld NT chunks each.  The first
-// wave reads the next row's record while the others write this row's gradients;
-// records and bitmaps have two places each (one for single-wave workgroups).
-template <typename T, int NT, bool SAME>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4)))
+constexpr int kHeld = 17;   // chunks a thread holds
+
+// Forward and backward of whole rows, at most kHeld NS chunks each, by NS threads
+// and one more wave, which reads the next row's record while the others sum the
+// row, and writes the listed tokens' gradients while they sum the next one:
+// what takes its time there are a few dependent reads, which would hold up a
+// wave that also has its share of the row.  Records and bitmaps have two places.
+template <typename T, int NS, bool SAME>
+__global__ __launch_bounds__(NS + kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_row_kernel(DistillArgs a, DistillGradArgs b)
 {
-    constexpr int W = Row<T>::W, N = HeldRow<T, NT, SAME>::G * W, kSets = NT == kWave ? 1 : 2;
-    constexpr int kWords = (NT * kHeld * W + 2 * W + 31) / 32;
-    __shared__ Total tot[2][NT / kWave];
-    __shared__ Teacher teacher[kSets];
-    __shared__ unsigned bitmap[kSets][kWords];
+    typedef HeldRow<T, NS, kHeld, SAME> Held;
+    constexpr int W = Row<T>::W, N = Held::G * W;
+    constexpr int kWords = ((NS * kHeld * W + 2 * W + 31) / 32 + 3) / 4 * 4;
+    __shared__ Total tot[2][NS / kWave];
+    __shared__ Teacher teacher[2];
+    __shared__ alignas(16) unsigned bitmap[2][kWords];   // the row's listed tokens
+    __shared__ alignas(16) unsigned dirty[2][NS];        // a thread's chunks that hold one
+    __shared__ u32x4 park[NS * parked(NS) + 1];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
+    const bool sums = __builtin_amdgcn_readfirstlane(tid / kWave) < NS / kWave;
     const Scale k(a.in.c);
     auto out_at = [&](int64_t r) { return static_cast<T *>(b.d_logits) + r * b.d_stride; };
     auto row_at = [&](int64_t r) {
         return Row<T>(static_cast<const T *>(a.in.logits) + r * a.in.stride, a.in.vocab);
     };
     auto skip_padding = [&](int64_t r) {
-        while (r < a.in.rows && is_padding(a.top_index + r * K, a.top_value + r * K, K, lane)) {
+        while (r < a.in.rows && is_padding(a.top_index + r * K, a.top_value + r * K, K)) {
             const Row<T> row = row_at(r);
             pad_distill(a.loss, a.stats, r);
-            fill_row<T, NT>(row, out_at(r), 0, row.chunks, 0.0f);
+            if (sums)
+                fill_row<T, NS>(row, out_at(r), 0, row.chunks, 0.0f);
             r += gridDim.x;
         }
         return r;
     };
     auto read_record = [&](int64_t r, const Row<T> &row, int set) {
         const int32_t *index = a.top_index + r * K;
-        const float *value = a.top_value + r * K;
-        mark_listed(bitmap[set], (row.chunks * W + 31) / 32, index, K, row.phase, row.chunks * W,
-                    a.in.vocab, lane);
-        read_teacher(teacher[set], index, value, K, a.mode, row.p, a.in.vocab, k, a.in.scale, lane);
+        const bool twice = mark_listed(bitmap[set], (row.chunks * W + 31) / 32, index, K, row.phase,
+                                       row.chunks * W, a.in.vocab, lane);
+        for (int i = lane; i < NS / 4; i += kWave)
+            reinterpret_cast<u32x4 *>(dirty[set])[i] = u32x4{0, 0, 0, 0};
+        wave_sync();
+        for (int i = lane; i < K; i += kWave) {
+            const int id = index[i], c = (id + row.phase) / W;
+            if (id >= 0 && id < a.in.vocab && c >= row.full_lo && c < row.full_hi)
+                atomicOr(&dirty[set][(c - row.full_lo) % NS], 1u << (c - row.full_lo) / NS);
+        }
+        read_teacher(teacher[set], index, a.top_value + r * K, K, a.mode, row.p, a.in.vocab, k,
+                     a.in.scale, twice, lane);
     };
-    __shared__ u32x4 park[NT * parked(NT) + 1];
-    HeldRow<T, NT, SAME> held;
-    held.park = park;
+    // What both halves need of a row once its sum is known (barrier, then this).
+    auto outcome = [&](int64_t r, const Teacher &te, const Total &t, float &dl, bool &fill) {
+        dl = ld_uniform(b.d_loss + r);
+        fill = dl == 0.0f || te.bad || (t.empty() && te.listed_sum == 0.0f);
+    };
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
         return;
+    // Two loops with the same barriers: one before the first row, one when a row
+    // is summed, one when its gradients are written.
+    if (!sums) {
+        read_record(r, row_at(r), 0);
+        __syncthreads();
+        for (int turn = 0;; turn ^= 1) {
+            Teacher &te = teacher[turn];
+            const int64_t rn = skip_padding(r + gridDim.x);
+            if (rn < a.in.rows)
+                read_record(rn, row_at(rn), turn ^ 1);
+            __syncthreads();
+            const Total t = add_waves<false, NS / kWave>(tot[turn], k);
+            float dl;
+            bool fill;
+            outcome(r, te, t, dl, fill);
+            if (lane == 0)
+                finish_distill(te, t, a.in, a.loss, a.stats, r);
+            __syncthreads();
+            if (!fill) {
+                const double w = (double)dl * (double)a.in.scale;
+                T *out = out_at(r);
+                for (int i = lane; i < K; i += kWave)
+                    if (te.lead[i] >= 0)
+                        store_one(out + te.lead[i], listed_grad(te, i, te.max, te.log2z, w, k));
+            }
+            if (rn >= a.in.rows)
+                return;
+            r = rn;
+        }
+    }
+    Held held;
+    held.park = park;
     held.read(row_at(r));
     held.take(row_at(r));
-    if (tid < kWave)
-        read_record(r, held.row, 0);
     __syncthreads();
     for (int turn = 0;; turn ^= 1) {
-        const int set = kSets == 1 ? 0 : turn;
-        Teacher &te = teacher[set];
-        const unsigned *bits = bitmap[set];
+        const Teacher &te = teacher[turn];
+        const unsigned *bits = bitmap[turn];
+        const int64_t rn = skip_padding(r + gridDim.x);
+        const Row<T> next = rn < a.in.rows ? row_at(rn) : Row<T>();
+        const unsigned mine = dirty[turn][tid];
         Sum q;
         held.each_group([&](int i, float (&x)[N]) {
 #pragma unroll
-            for (int j = 0; j < N / W; ++j) {
-                const int at = min(held.row.full_lo + tid + NT * (i + j), held.row.chunks - 1) * W;
-                const unsigned listed = bits[at >> 5] >> (at & 31) & ((1u << W) - 1);
-                if (listed) {
+            for (int j = 0; j < N / W; ++j)
+                if (mine >> (i + j) & 1) {
+                    const int at = (held.row.full_lo + tid + NS * (i + j)) * W;
+                    const unsigned listed = bits[at >> 5] >> (at & 31);
 #pragma unroll
                     for (int w = 0; w < W; ++w)
                         x[j * W + w] = listed >> w & 1 ? -kInf : x[j * W + w];
                 }
-            }
             q.template add<N, false>(x, k);
         });
         if (held.e >= 0) {
@@ -563,48 +621,36 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
             const float x[1] = {bits[at >> 5] >> (at & 31) & 1 ? -kInf : held.edge};
             q.template add<1, false>(x, k);
         }
-        const Total t = block_total<false, NT / kWave>(q, k, tot[turn]);
-        const int64_t rn = skip_padding(r + gridDim.x);
-        const Row<T> next = rn < a.in.rows ? row_at(rn) : Row<T>();
+        const Total own = wave_total<false>(q, k);
+        if (lane == 0)
+            tot[turn][tid / kWave] = own;
+        __syncthreads();
+        const Total t = add_waves<false, NS / kWave>(tot[turn], k);
         T *out = out_at(r);
-        const float dl = b.d_loss[r];
-        const double w = (double)dl * (double)a.in.scale;
-        if (tid < kWave) {
-            if (tid == 0)
-                finish_distill(te, t, a.in, a.loss, a.stats, r);
-            if (kSets == 2 && rn < a.in.rows)
-                read_record(rn, next, set ^ 1);
-        }
-        const bool nothing = t.empty() && te.listed_sum == 0.0f;
-        const bool fill = dl == 0.0f || te.bad || nothing, big = __builtin_fabsf(t.m) > k.big;
+        float dl;
+        bool fill;
+        outcome(r, te, t, dl, fill);
+        const bool big = __builtin_fabsf(t.m) > k.big;
         // the rest's share of the whole sum, then the coefficient of 2^t
+        const double w = (double)dl * (double)a.in.scale;
         const Total whole = whole_row(t, te.listed_max, te.listed_sum, k);
         const float share = t.s * pow2(shift_of(t.m, whole.m, k)) / whole.s;
         const float coef = (float)(w * (te.total * (double)share - te.rest)) / t.s;
         const float m = t.m, ref = m * k.c;
         if (fill || t.empty())
-            fill_row<T, NT>(held.row, out, 0, held.row.chunks,
+            fill_row<T, NS>(held.row, out, 0, held.row.chunks,
                             fill && te.bad && dl != 0.0f ? __builtin_nanf("") : 0.0f);
-        else if (big)   // rare: from memory, so that the held row's loop is not written twice
-            for (int k0 = 0; k0 < held.row.chunks; k0 += NT)
-                RowPart<T, NT, 1>(held.row, k0).map(held.row, out,
+        else if (big)   // rare: from memory, so that the held row's code is not there twice
+            for (int k0 = 0; k0 < held.row.chunks; k0 += NS)
+                RowPart<T, NS, 1>(held.row, k0).map(held.row, out,
                                                     [&](float x) { return coef * pow2((x - m) * k.c); });
         held.map(out, !fill && !t.empty() && !big, next,
                  [&](float x) { return coef * pow2(__builtin_fmaf(x, k.c, -ref)); });
-        __syncthreads();
-        if (!fill)
-            for (int i = tid; i < K; i += NT)
-                if (te.lead[i] >= 0)
-                    store_one(out + te.lead[i], listed_grad(te, i, te.max, te.log2z, w, k));
         held.take(next);
+        __syncthreads();
         if (rn >= a.in.rows)
             return;
         r = rn;
-        if (kSets == 1) {
-            wave_sync();
-            read_record(r, next, 0);
-            wave_sync();
-        }
     }
 }
 
@@ -626,24 +672,33 @@ int launch_distill_of(const DistillArgs &a, int segs, hipStream_t st)
     });
 }
 
-template <typename T, int NT>
-int launch_distill_row_nt(const DistillArgs &a, const DistillGradArgs &b, hipStream_t st)
+// Threads that hold a row in registers; 0: the row is too long for 960.
+template <typename T>
+int held_threads(int vocab)
 {
-    const dim3 grid(held_grid(a.in.rows, NT));
+    const int most = chunks_per<T>(vocab, 1);
+    return most <= 64 * kHeld ? 64 : most <= 192 * kHeld ? 192 : most <= 448 * kHeld ? 448
+         : most <= 960 * kHeld ? 960 : 0;
+}
+
+template <typename T, int NS>
+int launch_distill_row_ns(const DistillArgs &a, const DistillGradArgs &b, hipStream_t st)
+{
+    const dim3 grid(held_grid(a.in.rows, NS + kWave)), block(NS + kWave);
     if (same_phase(a.in, b.d_logits, b.d_stride))
-        hipLaunchKernelGGL((distill_row_kernel<T, NT, true>), grid, dim3(NT), 0, st, a, b);
+        hipLaunchKernelGGL((distill_row_kernel<T, NS, true>), grid, block, 0, st, a, b);
     else
-        hipLaunchKernelGGL((distill_row_kernel<T, NT, false>), grid, dim3(NT), 0, st, a, b);
+        hipLaunchKernelGGL((distill_row_kernel<T, NS, false>), grid, block, 0, st, a, b);
     return hipGetLastError();
 }
 template <typename T>
 int launch_distill_row(const DistillArgs &a, const DistillGradArgs &b, hipStream_t st)
 {
     const int threads = held_threads<T>(a.in.vocab);
-    return threads == 64  ? launch_distill_row_nt<T, 64>(a, b, st)
-         : threads == 256 ? launch_distill_row_nt<T, 256>(a, b, st)
-         : threads == 512 ? launch_distill_row_nt<T, 512>(a, b, st)
-                          : launch_distill_row_nt<T, 1024>(a, b, st);
+    return threads == 64  ? launch_distill_row_ns<T, 64>(a, b, st)
+         : threads == 192 ? launch_distill_row_ns<T, 192>(a, b, st)
+         : threads == 448 ? launch_distill_row_ns<T, 448>(a, b, st)
+                          : launch_distill_row_ns<T, 960>(a, b, st);
 }
 
 }  // namespace
@@ -669,6 +724,11 @@ int launch_distill_grad(const DistillGradArgs &a, void *stream)
         else
             hipLaunchKernelGGL((distill_grad_kernel<float, U>), grid, block, 0, st, a, r, segs);
     });
+}
+
+bool distill_row_held(const LossRows &in)
+{
+    return (in.dtype == ZERO_BF16 ? held_threads<uint16_t>(in.vocab) : held_threads<float>(in.vocab)) > 0;
 }
 
 int launch_distill_fused(const DistillArgs &a, const DistillGradArgs &b, void *stream)

@@ -476,10 +476,10 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
     T *out = static_cast<T *>(a.d_logits) + r * a.d_stride;
     const Row<T> row(static_cast<const T *>(a.in.logits) + r * a.in.stride, a.in.vocab);
     const RowPart<T, kNT, 1> seg(row, k0);   // on its way while the row's values are read
-    const int64_t tok = a.tokens ? a.tokens[r] : 0;
-    const float dl = a.d_logprob ? a.d_logprob[r] : 0.0f;
-    const float dh = ENT ? a.d_entropy[r] : 0.0f;
-    const float m = a.stats[2 * r], ln = a.stats[2 * r + 1];
+    const int64_t tok = a.tokens ? ld_uniform(a.tokens + r) : 0;
+    const float dl = a.d_logprob ? ld_uniform(a.d_logprob + r) : 0.0f;
+    const float dh = ENT ? ld_uniform(a.d_entropy + r) : 0.0f;
+    const float m = ld_uniform(a.stats + 2 * r), ln = ld_uniform(a.stats + 2 * r + 1);
     const bool zero = tok < 0 || (dl == 0.0f && dh == 0.0f), bad = tok >= a.in.vocab;
     if (zero || bad || m == -kInf) {
         fill_row(row, out, k0, k0 + kNT, bad && !zero ? __builtin_nanf("") : 0.0f);
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
     // log2 p = t - off
     const float ref = m * k.c, off = residue(m, k) + ln * kLog2E;
     const float inv = pow2(-off);
-    const float h = ENT ? a.entropy[r] : 0.0f;
+    const float h = ENT ? ld_uniform(a.entropy + r) : 0.0f;
     const float u = -a.in.scale * (dl + dh * (h - off * kLn2)) * inv;
     const float v = -a.in.scale * dh * kLn2 * inv;
     // the given token's thread; in place: it reads the logit before it writes
@@ -505,12 +505,15 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
         store_one(out + tok, grad(rel(l, m, ref, k)) + a.in.scale * dl);
 }
 
+constexpr int kHeld = 16;   // chunks a thread holds
+
 // Forward and backward of whole rows, at most kHeld NT chunks each.
 template <typename T, int NT, bool ENT, bool SAME>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4)))
 void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
 {
-    constexpr int N = HeldRow<T, NT, SAME>::G * Row<T>::W;
+    typedef HeldRow<T, NT, kHeld, SAME> Held;
+    constexpr int N = Held::G * Row<T>::W;
     __shared__ Total tot[2][NT / kWave];
     auto out_at = [&](int64_t r) { return static_cast<T *>(b.d_logits) + r * b.d_stride; };
     auto row_at = [&](int64_t r) {
@@ -519,7 +522,7 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
     // The next row from r on that is not padding (padding rows are finished on
     // the way), or a.in.rows.
     auto skip_padding = [&](int64_t r) {
-        while (r < a.in.rows && a.tokens && a.tokens[r] < 0) {
+        while (r < a.in.rows && a.tokens && ld_uniform(a.tokens + r) < 0) {
             const Row<T> row = row_at(r);
             pad_logprob(a, r);
             fill_row<T, NT>(row, out_at(r), 0, row.chunks, 0.0f);
@@ -529,7 +532,7 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
     };
     const Scale k(a.in.c);
     __shared__ u32x4 park[NT * parked(NT) + 1];
-    HeldRow<T, NT, SAME> held;
+    Held held;
     held.park = park;
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
@@ -537,10 +540,12 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
     held.read(row_at(r));
     held.take(row_at(r));
     for (int turn = 0;; turn ^= 1) {
+        const int64_t rn = skip_padding(r + gridDim.x);
+        const Row<T> next = rn < a.in.rows ? row_at(rn) : Row<T>();
         const float l = token_logit<T>(a, r);   // in place: before it is overwritten
-        const int64_t tok = a.tokens ? a.tokens[r] : 0;
-        const float dl = b.d_logprob ? b.d_logprob[r] : 0.0f;
-        const float dh = b.d_entropy ? b.d_entropy[r] : 0.0f;
+        const int64_t tok = a.tokens ? ld_uniform(a.tokens + r) : 0;
+        const float dl = b.d_logprob ? ld_uniform(b.d_logprob + r) : 0.0f;
+        const float dh = b.d_entropy ? ld_uniform(b.d_entropy + r) : 0.0f;
         Sum q;
         held.each_group([&](int, const float (&x)[N]) { q.template add<N, ENT>(x, k); });
         if (held.e >= 0) {
@@ -551,8 +556,6 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
         // writes the next row's
         const Total t = block_total<ENT, NT / kWave>(q, k, tot[turn]);
         finish_logprob(a, r, l, t);
-        const int64_t rn = skip_padding(r + gridDim.x);
-        const Row<T> next = rn < a.in.rows ? row_at(rn) : Row<T>();
         T *out = out_at(r);
         const bool zero = dl == 0.0f && dh == 0.0f, bad = tok >= a.in.vocab;
         const bool fill = zero || bad || t.empty(), big = __builtin_fabsf(t.m) > k.big;
@@ -611,6 +614,16 @@ int launch_logprob_of(const LogprobArgs &a, int segs, hipStream_t st)
                    : launch_logprob_t<T, false, false>(a, segs, st);
 }
 
+// Threads of the workgroup that holds a row in registers; 0: the row is too
+// long for 1024.
+template <typename T>
+int held_threads(int vocab)
+{
+    const int most = chunks_per<T>(vocab, 1);
+    return most <= 64 * kHeld ? 64 : most <= 256 * kHeld ? 256 : most <= 512 * kHeld ? 512
+         : most <= 1024 * kHeld ? 1024 : 0;
+}
+
 template <typename T, int NT>
 int launch_logprob_row_nt(const LogprobArgs &a, const LogprobGradArgs &b, hipStream_t st)
 {
@@ -663,7 +676,7 @@ int launch_logprob_grad(const LogprobGradArgs &a, void *stream)
     });
 }
 
-bool loss_row_held(const LossRows &in)
+bool logprob_row_held(const LossRows &in)
 {
     return (in.dtype == ZERO_BF16 ? held_threads<uint16_t>(in.vocab) : held_threads<float>(in.vocab)) > 0;
 }

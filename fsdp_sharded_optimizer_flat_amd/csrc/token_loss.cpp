@@ -261,7 +261,7 @@ extern "C" zero_status zero_logprob_fused(const void *logits, int32_t dtype, int
         return ZERO_EINVAL;
     if (d_row_stride > (int64_t(1) << 61) / 4 / (rows > 0 ? rows : 1))
         return ZERO_ERANGE;
-    const bool held = loss_row_held(a.in);
+    const bool held = logprob_row_held(a.in);
     const int32_t segs = loss_segments(rows, vocab, 0);
     const Workspace w = held ? Workspace{} : workspace_layout(rows, segs, 0, true);
     if (zero_status s = check_workspace(workspace, workspace_bytes, w))
@@ -398,7 +398,7 @@ extern "C" zero_status zero_distill_fused(const void *logits, int32_t dtype, int
         return ZERO_EINVAL;
     if (d_row_stride > (int64_t(1) << 61) / 4 / (rows > 0 ? rows : 1))
         return ZERO_ERANGE;
-    const bool held = loss_row_held(a.in);
+    const bool held = distill_row_held(a.in);
     const int32_t segs = loss_segments(rows, vocab, 0);
     const Workspace w = held ? Workspace{} : workspace_layout(rows, segs, 0, true);
     if (zero_status s = check_workspace(workspace, workspace_bytes, w))

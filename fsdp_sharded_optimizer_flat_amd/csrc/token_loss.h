@@ -78,7 +78,8 @@ struct DistillGradArgs {
 int launch_distill_grad(const DistillGradArgs &a, void *stream);
 
 // Forward and backward in one launch, where a workgroup can hold a row.
-bool loss_row_held(const LossRows &in);
+bool logprob_row_held(const LossRows &in);
+bool distill_row_held(const LossRows &in);
 int launch_logprob_fused(const LogprobArgs &a, const LogprobGradArgs &b, void *stream);
 int launch_distill_fused(const DistillArgs &a, const DistillGradArgs &b, void *stream);
 

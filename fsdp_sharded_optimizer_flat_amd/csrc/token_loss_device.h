@@ -104,6 +104,15 @@ __device__ __forceinline__ void store_any(u32x4 v, T *p)
 __device__ __forceinline__ void store_one(uint16_t *p, float g) { *p = to_bf16(g); }
 __device__ __forceinline__ void store_one(float *p, float g) { *p = g; }
 
+// A value at an address that is the same in every lane, read into a scalar
+// register: only for arrays that the call does not write (its checks keep outputs
+// apart from them).  Such a load does not queue behind the vector loads and stores.
+template <typename T>
+__device__ __forceinline__ T ld_uniform(const T *p)
+{
+    return *(const __attribute__((address_space(4))) T *)p;
+}
+
 // p, which is the same in every lane, in scalar registers.
 template <typename T>
 __device__ __forceinline__ T *scalar(const T *p)
@@ -289,33 +298,45 @@ __device__ __forceinline__ void add_total(Total &t, const Total &o, const Scale 
     t.s += f * o.s;
 }
 
-// Every thread gets the workgroup's total.  `sh`: one Total per wave.  One
-// barrier; the caller places another before `sh` is written again.
-template <bool ENT, int NW = kNW>
-__device__ __forceinline__ Total block_total(Sum q, const Scale &k, Total *sh)
+// The total of a wave's lanes, in every lane.
+template <bool ENT>
+__device__ __forceinline__ Total wave_total(Sum q, const Scale &k)
 {
     const float m = __builtin_fmaxf(wave_max(q.top), kLowest);
     q.rebase(m, k);
-    Total w{m, wave_add(q.s), ENT ? wave_add(q.a) : 0.0f};
-    if ((threadIdx.x & (kWave - 1)) == 0)
-        sh[threadIdx.x / kWave] = w;
-    __syncthreads();
-    // each lane takes one wave's total, butterflies over the NW of them (held in
-    // one register each: a wave that holds a row has few to spare)
-    Total t = sh[threadIdx.x & (NW - 1)];
-    const Total own = t;
+    return Total{m, wave_add(q.s), ENT ? wave_add(q.a) : 0.0f};
+}
+// The total of NW waves' totals, in every lane: each lane takes one of them, and
+// butterflies add them (a wave that holds a row has few registers to spare).
+template <bool ENT, int NW>
+__device__ __forceinline__ Total add_waves(const Total *sh, const Scale &k)
+{
+    constexpr int M = NW <= 1 ? 1 : NW <= 2 ? 2 : NW <= 4 ? 4 : NW <= 8 ? 8 : 16;
+    const int i = threadIdx.x & (M - 1);
+    const Total own = i < NW ? sh[i] : Total{kLowest, 0.0f, 0.0f};
+    Total t{own.m, 0.0f, 0.0f};
 #pragma unroll
-    for (int o = NW / 2; o >= 1; o >>= 1)
+    for (int o = M / 2; o >= 1; o >>= 1)
         t.m = __builtin_fmaxf(t.m, __shfl_xor(t.m, o, kWave));
-    t.s = t.a = 0.0f;
     add_total(t, own, k);
 #pragma unroll
-    for (int o = NW / 2; o >= 1; o >>= 1) {
+    for (int o = M / 2; o >= 1; o >>= 1) {
         t.s += __shfl_xor(t.s, o, kWave);
         if constexpr (ENT)
             t.a += __shfl_xor(t.a, o, kWave);
     }
     return t;
+}
+// Every thread gets the workgroup's total.  `sh`: one Total per wave.  One
+// barrier; the caller places another before `sh` is written again.
+template <bool ENT, int NW = kNW>
+__device__ __forceinline__ Total block_total(const Sum &q, const Scale &k, Total *sh)
+{
+    const Total w = wave_total<ENT>(q, k);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        sh[threadIdx.x / kWave] = w;
+    __syncthreads();
+    return add_waves<ENT, NW>(sh, k);
 }
 
 // The total of a row's segments, one workgroup per row, in a fixed order.
@@ -445,28 +466,27 @@ __device__ __forceinline__ void fill_row(const Row<T> &row, T *out, int k0, int 
 
 // -- a row held in registers ---------------------------------------------------------------
 //
-// One workgroup of NT threads holds a row of up to kHeld chunks a thread in its
+// NT threads of a workgroup hold a row of up to H chunks a thread in their
 // registers: the logits are read from memory once, summed as they arrive, and
 // turned into gradients from the registers.  The workgroup goes through rows
 // gridDim.x apart: once a row's gradients are on their way its registers take the
 // next row, so that the loads wait behind the stores and not behind their end.
 
-constexpr int kHeld = 16;
 // Of these, the last chunks a thread parks in LDS once they are summed, which
 // leaves registers for what happens between the sums and the gradients (as many
 // as the workgroups resident on a compute unit have LDS for).
-constexpr int parked(int threads) { return threads >= 512 ? 4 : threads == 256 ? 2 : 0; }
+constexpr int parked(int threads) { return threads >= 448 ? 4 : threads >= 192 ? 2 : 0; }
 
 // SAME: the gradient's rows sit at the 16-byte phase of the logits' rows.
-template <typename T, int NT, bool SAME>
+template <typename T, int NT, int H, bool SAME>
 struct HeldRow {
     static constexpr int W = Row<T>::W;
     static constexpr int G = 8 / W;       // chunks of a group that is summed at once
-    static constexpr int P = parked(NT), P0 = kHeld - P;
+    static constexpr int P = parked(NT), P0 = H - P;
     u32x4 *park;  // P NT chunks of LDS
     Row<T> row;
     int n;        // whole chunks
-    Chunk<T> ch[kHeld];
+    Chunk<T> ch[H];
     float edge;   // this thread's element of the row's partial first or last chunk
     int e;        // and its index, or -1
 
@@ -484,7 +504,7 @@ struct HeldRow {
         const T *first = scalar(next.chunk(next.full_lo));
         const __amdgpu_buffer_rsrc_t rs = window(first, m);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
+        for (int i = 0; i < H; ++i)
             ch[i].r = __builtin_bit_cast(decltype(ch[i].r),
                                          __builtin_amdgcn_raw_buffer_load_b128(
                                              rs, (int)threadIdx.x * 16, NT * 16 * i, kLoadStreamPolicy));
@@ -496,7 +516,7 @@ struct HeldRow {
     {
         constexpr unsigned none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
 #pragma unroll
-        for (int i = 0; i < kHeld; i += G) {
+        for (int i = 0; i < H; i += G) {
             if (NT * i < n) {
                 float x[W * G];
                 u32x4 raw[G];
@@ -532,7 +552,7 @@ struct HeldRow {
         T *first = scalar(out + (row.full_lo * W - row.phase));
         const int m = write ? n : 0;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
+        for (int i = 0; i < H; ++i) {
             Chunk<T> c = ch[i];
             if (i >= P0)
                 c.r = __builtin_bit_cast(decltype(c.r), park[NT * (i - P0) + threadIdx.x]);
@@ -579,18 +599,10 @@ int chunks_per(int vocab, int segs)
     return (most + segs - 1) / segs;
 }
 
-// Threads of the workgroup that holds a row in registers; 0: the row is too
-// long for 1024.
-template <typename T>
-int held_threads(int vocab)
-{
-    const int most = chunks_per<T>(vocab, 1);
-    return most <= 64 * kHeld ? 64 : most <= 256 * kHeld ? 256 : most <= 512 * kHeld ? 512
-         : most <= 1024 * kHeld ? 1024 : 0;
-}
-
 // Workgroups of a launch that goes through rows: as many as are resident at once
-// (128 registers a thread: 16 waves on a compute unit).
+// (128 registers a thread: 16 waves on a compute unit), or one per row where
+// each would get four rows or fewer (1024 x 50304 bf16, loss and gradient: 39 us,
+// and 44 us with two rows to a workgroup; 8192 x 128256: 840 and 772 us).
 inline unsigned held_grid(int64_t rows, int threads)
 {
     const int64_t most = (int64_t)device_cu_count() * (1024 / threads);
