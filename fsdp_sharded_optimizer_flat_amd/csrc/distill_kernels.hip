@@ -522,6 +522,7 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
     __shared__ alignas(16) unsigned bitmap[2][kWords];   // the row's listed tokens
     __shared__ alignas(16) unsigned dirty[2][NS];        // a thread's chunks that hold one
     __shared__ u32x4 park[NS * parked(NS) + 1];
+    __shared__ unsigned written;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), K = a.top_k;
     const bool sums = __builtin_amdgcn_readfirstlane(tid / kWave) < NS / kWave;
     const Scale k(a.in.c);
@@ -562,11 +563,16 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
     int64_t r = skip_padding(blockIdx.x);
     if (r >= a.in.rows)
         return;
-    // Two loops with the same barriers: one before the first row, one when a row
-    // is summed, one when its gradients are written.
+    // Two loops with the same barriers, one before the first row and one when a row
+    // is summed.  The waves that hold a row count in `written` when its gradients
+    // are on their way; only the other wave waits for that, so each of them can go
+    // on to sum the next row by itself.
     if (!sums) {
+        if (lane == 0)
+            written = 0;
         read_record(r, row_at(r), 0);
         __syncthreads();
+        unsigned all = 0;
         for (int turn = 0;; turn ^= 1) {
             Teacher &te = teacher[turn];
             const int64_t rn = skip_padding(r + gridDim.x);
@@ -579,7 +585,9 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
             outcome(r, te, t, dl, fill);
             if (lane == 0)
                 finish_distill(te, t, a.in, a.loss, a.stats, r);
-            __syncthreads();
+            all += NS / kWave;
+            while (__hip_atomic_load(&written, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) != all)
+                __builtin_amdgcn_s_sleep(1);
             if (!fill) {
                 const double w = (double)dl * (double)a.in.scale;
                 T *out = out_at(r);
@@ -646,8 +654,9 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
                                                     [&](float x) { return coef * pow2((x - m) * k.c); });
         held.map(out, !fill && !t.empty() && !big, next,
                  [&](float x) { return coef * pow2(__builtin_fmaf(x, k.c, -ref)); });
+        if (lane == 0)
+            __hip_atomic_fetch_add(&written, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
         held.take(next);
-        __syncthreads();
         if (rn >= a.in.rows)
             return;
         r = rn;
