@@ -296,11 +296,11 @@ constexpr int kBitWords = (int)(kLossMaxSegment / 32) + 8;
 // One workgroup per segment of a row: the sum over its tokens that the teacher
 // does not list, which a bitmap in LDS leaves out (subtracting the listed ones
 // from the whole sum would lose the rest's digits where little is left).
-template <typename T>
-__global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row0, int segs, int cps)
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0, int segs, int cps)
 {
     constexpr int U = 4, W = Row<T>::W;
-    __shared__ Total tot[kNW];
+    __shared__ Total tot[NT / kWave];
     __shared__ Teacher te;
     __shared__ alignas(16) unsigned bits[kBitWords];
     const int64_t row_i = row0 + blockIdx.x / segs;
@@ -338,16 +338,16 @@ __global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row
         q.add<W, false>(x, sc);
     };
     int k = lo + tid;
-    for (; k + kNT * (U - 1) < hi; k += kNT * U) {
+    for (; k + NT * (U - 1) < hi; k += NT * U) {
         Chunk<T> ch[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            ch[u].stream(row.chunk(k + kNT * u));
+            ch[u].stream(row.chunk(k + NT * u));
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            take(ch[u], k + kNT * u);
+            take(ch[u], k + NT * u);
     }
-    for (; k < hi; k += kNT) {
+    for (; k < hi; k += NT) {
         Chunk<T> ch;
         ch.stream(row.chunk(k));
         take(ch, k);
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(kNT) void distill_kernel(DistillArgs a, int64_t row
         const float x[1] = {bits[at >> 5] >> (at & 31) & 1 ? -kInf : row.at(e)};
         q.add<1, false>(x, sc);
     }
-    const Total t = block_total<false>(q, sc, tot);
+    const Total t = block_total<false, NT / kWave>(q, sc, tot);
     if (segs > 1) {
         if (tid == 0)
             a.parts[row_i * segs + seg] = LossPart{t.m, t.s, 0.0f, 0.0f};
@@ -669,8 +669,13 @@ template <typename T>
 int launch_distill_of(const DistillArgs &a, int segs, hipStream_t st)
 {
     const int cps = chunks_per<T>(a.in.vocab, segs);
+    if (segs == 1 && wide_rows(a.in)) {
+        hipLaunchKernelGGL((distill_kernel<T, kWide>), dim3((unsigned)a.in.rows), dim3(kWide), 0, st, a,
+                           (int64_t)0, 1, cps);
+        return hipGetLastError();
+    }
     if (int e = each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
-            hipLaunchKernelGGL((distill_kernel<T>), dim3(n * (unsigned)segs), dim3(kNT), 0, st, a, r,
+            hipLaunchKernelGGL((distill_kernel<T, kNT>), dim3(n * (unsigned)segs), dim3(kNT), 0, st, a, r,
                                segs, cps);
         }))
         return e;

@@ -13,16 +13,34 @@ using namespace dev;
 //
 // The K largest logits, ties to the lowest index, as keys that order them: the
 // logit's bits made monotonic, then the inverted index.  One pass over the row
-// leaves the largest logit of each of at most kGroups groups of a few chunks in
-// LDS.  The K-th largest of those is at most the K-th largest logit, so only
-// groups that reach it are read again (about K of them) and their logits that
-// reach it become candidates, usually little more than K.  Where there are too
-// many (plateaus of equal logits), a radix search over the whole keys, which are
-// all different, finds the K-th exactly.
+// leaves the largest logit of each group of kGroup in LDS (its upper 16 bits); a
+// group is a whole cache line of bf16, so that reading it again costs no more.  Of its groups each wave finds the ceil(K / waves)-th
+// largest maximum by bisection; the least of these is a bound that at least K
+// logits reach.  Only groups that reach it are read again (a little more than K
+// of them) and their logits that reach it become candidates, each ranked by the
+// number of larger ones.  Where there are too many (plateaus of equal logits, few
+// groups), a radix search over the whole keys, which are all different, finds the
+// K-th exactly.
 
 constexpr int kIndexBits = 20;
 static_assert(ZERO_MAX_VOCAB <= 1 << kIndexBits, "the index fits its field");
-constexpr int kGroups = 2048;
+constexpr int kGroup = 64;
+constexpr int kGroups = 2304;   // those of kLossMaxSegment elements, and some to spare
+static_assert(kGroups >= (int)(kLossMaxSegment / kGroup) + 2, "a segment's groups fit");
+
+// The maximum over N neighbouring lanes (8 or 16, aligned), in each of them.
+template <int N>
+__device__ __forceinline__ float group_max(float x)
+{
+    static_assert(N == 8 || N == 16, "within a row of 16 lanes");
+    auto with = [&](int y) { x = __builtin_fmaxf(x, __int_as_float(y)); };
+    with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0xb1, 0xf, 0xf, true));    // lane ^ 1
+    with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x4e, 0xf, 0xf, true));    // lane ^ 2
+    with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x141, 0xf, 0xf, true));   // mirrored in 8
+    if constexpr (N == 16)
+        with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x140, 0xf, 0xf, true));   // in 16
+    return x;
+}
 constexpr int kCands = 1024;
 
 __device__ __forceinline__ unsigned ord32(float x)
@@ -49,34 +67,41 @@ struct Select {
     unsigned count;        // candidates
     unsigned listed;       // groups to read again
     unsigned bin, above;   // a radix pass's result
-    float gmax[kGroups];
+    unsigned floor[16];    // each wave's bound
+    unsigned long long floor64;
+    alignas(16) uint16_t gmax[kGroups];
     uint16_t list[kGroups];
-    uint64_t cand[kCands];
+    alignas(16) uint64_t cand[kCands];
+    // the K largest of many candidates, once the groups are done with
+    __device__ __forceinline__ uint64_t *best() { return reinterpret_cast<uint64_t *>(gmax); }
 };
+static_assert(ZERO_MAX_TOP * sizeof(uint64_t) <= sizeof(Select::gmax), "room for the best");
 
 // One radix pass's choice: the bin of sh.hist (256 bins) that holds the want-th
-// largest entry, and how many lie above it.  Thread b owns bin b.
+// largest entry, and how many lie above it.  Thread b < 256 owns bin b.
 __device__ __forceinline__ void pick_bin(Select &sh, unsigned want)
 {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     __syncthreads();
-    const unsigned own = sh.hist[tid];
-    unsigned above = 0;                     // entries in bins above this one
-    for (int w = wave + 1; w < kNW; ++w)
-        above += sh.hist[w * kWave + lane];
+    if (wave < 4) {
+        const unsigned own = sh.hist[tid];
+        unsigned above = 0;                     // entries in bins above this one
+        for (int w = wave + 1; w < 4; ++w)
+            above += sh.hist[w * kWave + lane];
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        above += __shfl_xor(above, o, kWave);
-    unsigned suf = own;                     // of this wave: inclusive suffix sum
+        for (int o = 32; o >= 1; o >>= 1)
+            above += __shfl_xor(above, o, kWave);
+        unsigned suf = own;                     // of this wave: inclusive suffix sum
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const unsigned v = __shfl_down(suf, o, kWave);
-        suf += lane + o < kWave ? v : 0;
-    }
-    above += suf - own;
-    if (above < want && above + own >= want) {
-        sh.bin = tid;
-        sh.above = above;
+        for (int o = 1; o < kWave; o <<= 1) {
+            const unsigned v = __shfl_down(suf, o, kWave);
+            suf += lane + o < kWave ? v : 0;
+        }
+        above += suf - own;
+        if (above < want && above + own >= want) {
+            sh.bin = tid;
+            sh.above = above;
+        }
     }
     __syncthreads();
 }
@@ -95,15 +120,17 @@ __device__ __forceinline__ void count_bin(Select &sh, unsigned bin)
     }
 }
 
-// The K-th largest of the keys that `each` visits (all different, at least K of
-// them).  each(f) calls f(key) once for every key, over the whole workgroup.
+// The K-th largest of the keys that `each` visits (at least K of them, all
+// different but for zeros).  each(f) calls f(key) once for every key, over the
+// whole workgroup.
 template <typename Each>
 __device__ uint64_t kth_key(Select &sh, int K, Each each)
 {
     uint64_t prefix = 0;
     unsigned want = (unsigned)K;
     for (int sft = 48; sft >= 0; sft -= 8) {   // 32 + 20 bits in seven bytes
-        sh.hist[threadIdx.x] = 0;
+        if (threadIdx.x < 256)
+            sh.hist[threadIdx.x] = 0;
         __syncthreads();
         each([&](uint64_t k) {
             if ((k >> sft) >> 8 == prefix)
@@ -125,12 +152,12 @@ __device__ __forceinline__ void push(Select &sh, uint64_t key)
 }
 
 // Visits the elements of chunks [k0, k1) of a row: f(value, index).
-template <typename T, typename F>
+template <typename T, int NT, typename F>
 __device__ __forceinline__ void each_element(const Row<T> &row, int k0, int k1, F f)
 {
     constexpr int W = Row<T>::W;
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    for (int k = lo + (int)threadIdx.x; k < hi; k += kNT) {
+    for (int k = lo + (int)threadIdx.x; k < hi; k += NT) {
         Chunk<T> ch;
         ch.load(row.chunk(k));
         float x[W];
@@ -144,86 +171,131 @@ __device__ __forceinline__ void each_element(const Row<T> &row, int k0, int k1, 
         f(row.at(e), e);
 }
 
-// Writes the K largest of the workgroup's candidates, best first, through
-// put(rank, key).  Every candidate's rank is the number of larger ones.
-template <typename Put>
+// Writes the K largest of the workgroup's n candidates, best first, through
+// put(rank, key).  A candidate's rank is the number of larger ones; where there
+// are many, a radix search leaves the K largest first.
+template <int NT, typename Put>
 __device__ __forceinline__ void put_ranked(Select &sh, int n, int K, Put put)
 {
-    for (int i = threadIdx.x; i < n; i += kNT) {
-        const uint64_t own = sh.cand[i];
+    const int tid = threadIdx.x;
+    uint64_t *cand = sh.cand;
+    if (n > 256 && n > K) {
+        const uint64_t kth = kth_key(sh, K, [&](auto f) {
+            for (int i = tid; i < n; i += NT)
+                f(sh.cand[i]);
+        });
+        if (tid == 0)
+            sh.count = 0;
+        __syncthreads();
+        cand = sh.best();
+        for (int i = tid; i < n; i += NT)
+            if (sh.cand[i] >= kth)
+                cand[atomicAdd(&sh.count, 1u)] = sh.cand[i];
+        __syncthreads();
+        n = K;
+    } else if ((n & 1) && n < kCands) {
+        if (tid == 0)
+            cand[n] = 0;   // below every key: they are compared in pairs
+        __syncthreads();
+    }
+    for (int i = tid; i < n; i += NT) {
+        const uint64_t own = cand[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j)
-            rank += sh.cand[j] > own;
+        for (int j = 0; j < n; j += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(cand + j);
+            rank += (o.x > own) + (j + 1 < n && o.y > own);
+        }
         if (rank < K)
             put(rank, own);
     }
 }
 
-// The K largest logits of chunks [k0, k1), whose groups' largest logits are in
-// sh.gmax: group g = thread + kNT * (batch / per), a batch being the U chunks
-// lo + thread + kNT * (batch * U + u).
-template <typename T, int U, typename Put>
-__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int groups, int per, int K,
-                           Put put)
+// The K largest logits of chunks [k0, k1).  Group g of their whole chunks is
+// elements kGroup g .. + kGroup - 1; sh.gmax holds the upper 16 bits of its
+// largest logit's order.
+template <typename T, int NT, typename Put>
+__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K, Put put)
 {
-    constexpr int W = Row<T>::W;
-    const int tid = threadIdx.x;
+    constexpr int W = Row<T>::W, NW = NT / kWave, L = kGroup / W, Q = (kGroups + NT - 1) / NT;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    const int groups = (max(hi - lo, 0) + L - 1) / L;
     const int first = max(k0 * W - row.phase, 0), last = min(k1 * W - row.phase, row.vocab);
     const int n = max(last - first, 0);
-    // the K-th largest group maximum, to 16 bits (a lower bound of it)
-    unsigned floor16 = 0;
-    if (groups >= K) {
-        unsigned want = (unsigned)K;
-        for (int pass = 0; pass < 2; ++pass) {
-            sh.hist[tid] = 0;
-            __syncthreads();
-            for (int g = tid; g < groups; g += kNT) {
-                const unsigned o = ord32(sh.gmax[g]);
-                if (pass == 0)
-                    count_bin(sh, o >> 24);
-                else if (o >> 24 == floor16)
-                    count_bin(sh, o >> 16 & 255u);
-            }
-            pick_bin(sh, want);
-            floor16 = floor16 << 8 | sh.bin;
-            want -= sh.above;
-            __syncthreads();
-        }
+    // this thread's groups, and the wave's bound
+    unsigned g[Q];
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+        g[i] = tid + NT * i < groups ? sh.gmax[tid + NT * i] : 0u;
+    // the waves with a group for each lane (the first, if none has)
+    const int waves = max(min(groups / kWave, NW), 1), want = (K + waves - 1) / waves;
+    unsigned bound = 0;
+    for (int bit = 15; bit >= 0; --bit) {
+        const unsigned v = bound | 1u << bit;
+        int have = 0;
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            have += __popcll(__ballot(g[i] >= v));
+        if (have >= want)
+            bound = v;
     }
-    const uint64_t bound = (uint64_t)(floor16 << 16) << kIndexBits;
+    if (lane == 0)
+        sh.floor[tid / kWave] = tid / kWave < waves ? bound : ~0u;
     if (tid == 0) {
         sh.count = 0;
         sh.listed = 0;
     }
     __syncthreads();
-    for (int g = tid; g < groups; g += kNT)
-        if (ord32(sh.gmax[g]) >> 16 >= floor16)
-            sh.list[atomicAdd(&sh.listed, 1u)] = (uint16_t)g;
-    __syncthreads();
-    const int span = per * U;
-    const int todo = (int)sh.listed * span;
-    for (int j = tid; j < todo; j += kNT) {
-        const int g = sh.list[j / span], step = (g / kNT) * span + j % span;
-        const int k = lo + (g % kNT) + kNT * step;
-        if (k < hi) {
-            Chunk<T> ch;
-            ch.load(row.chunk(k));
-            float x[W];
-            ch.widen(x);
+    bound = ~0u;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const uint64_t key = key_of(x[i], k * W - row.phase + i);
-                if (key >= bound)
-                    push(sh, key);
-            }
-        }
+    for (int w = 0; w < NW; ++w)
+        bound = min(bound, sh.floor[w]);
+    const float least = bound <= 0x7fu ? -kInf : ord32_value(bound << 16);
+    // the groups that reach the bound
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+        mine += __popcll(__ballot(tid + NT * i < groups && g[i] >= bound));
+    unsigned at = 0;
+    if (lane == 0 && mine)
+        at = atomicAdd(&sh.listed, (unsigned)mine);
+    at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const bool in = tid + NT * i < groups && g[i] >= bound;
+        const uint64_t m = __ballot(in);
+        if (in)
+            sh.list[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = (uint16_t)(tid + NT * i);
+        at += __popcll(m);
+    }
+    __syncthreads();
+    const int todo = (int)sh.listed * L;
+    auto chunk_of = [&](int j) { return lo + sh.list[j / L] * L + j % L; };
+    auto look = [&](const Chunk<T> &ch, int k) {
+        float x[W];
+        ch.widen(x);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (x[i] >= least)
+                push(sh, key_of(x[i], k * W - row.phase + i));
+    };
+    for (int j = tid; j < todo; j += 2 * NT) {   // two reads on their way at once
+        const int ka = chunk_of(j), kb = j + NT < todo ? chunk_of(j + NT) : hi;
+        Chunk<T> ca, cb;
+        if (ka < hi)
+            ca.load(row.chunk(ka));
+        if (kb < hi)
+            cb.load(row.chunk(kb));
+        if (ka < hi)
+            look(ca, ka);
+        if (kb < hi)
+            look(cb, kb);
     }
     const int e = tid < 2 * W ? row.edge(tid, k0, k1) : -1;
     if (e >= 0) {
-        const uint64_t key = key_of(row.at(e), e);
-        if (key >= bound)
-            push(sh, key);
+        const float x = row.at(e);
+        if (x >= least)
+            push(sh, key_of(x, e));
     }
     __syncthreads();
     int cands = (int)sh.count;
@@ -232,12 +304,12 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int gr
         uint64_t kth = 0;
         if (n > K)
             kth = kth_key(sh, K, [&](auto f) {
-                each_element(row, k0, k1, [&](float x, int i) { f(key_of(x, i)); });
+                each_element<T, NT>(row, k0, k1, [&](float x, int i) { f(key_of(x, i)); });
             });
         if (tid == 0)
             sh.count = 0;
         __syncthreads();
-        each_element(row, k0, k1, [&](float x, int i) {
+        each_element<T, NT>(row, k0, k1, [&](float x, int i) {
             const uint64_t key = key_of(x, i);
             if (key >= kth)
                 push(sh, key);
@@ -245,7 +317,7 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int gr
         __syncthreads();
         cands = min((int)sh.count, kCands);
     }
-    put_ranked(sh, cands, K, put);
+    put_ranked<NT>(sh, cands, K, put);
 }
 
 // -- log probabilities: forward ----------------------------------------------------------
@@ -309,7 +381,7 @@ __device__ __forceinline__ void put_top(const LogprobArgs &a, int64_t row, int r
 }
 __device__ __forceinline__ void put_none(const LogprobArgs &a, int64_t row, int from, const Total &t)
 {
-    for (int i = from + (int)threadIdx.x; i < a.top_k; i += kNT) {
+    for (int i = from + (int)threadIdx.x; i < a.top_k; i += blockDim.x) {
         a.top_index[row * a.top_k + i] = -1;
         a.top_logprob[row * a.top_k + i] = t.s != t.s ? __builtin_nanf("") : -kInf;
     }
@@ -317,11 +389,12 @@ __device__ __forceinline__ void put_none(const LogprobArgs &a, int64_t row, int 
 
 // One workgroup per segment of a row (segs of them): the whole result where
 // segs is 1, else its LossPart and its top keys.
-template <typename T, bool ENT, bool TOP>
-__global__ __launch_bounds__(kNT) void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
+template <typename T, int NT, bool ENT, bool TOP>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT == kNT ? 8 : 4)))
+void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
 {
     constexpr int U = 4, W = Row<T>::W;
-    __shared__ Total tot[kNW];
+    __shared__ Total tot[NT / kWave];
     __shared__ typename std::conditional<TOP, Select, int>::type sh;
     const int64_t row_i = row0 + blockIdx.x / segs;
     const int seg = blockIdx.x % segs, tid = threadIdx.x;
@@ -334,52 +407,36 @@ __global__ __launch_bounds__(kNT) void logprob_kernel(LogprobArgs a, int64_t row
     const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    const float given = segs == 1 && tid == 0 ? token_logit<T>(a, row_i) : 0.0f;
     const Scale sc(a.in.c);
     Sum q;
-    const int batches = hi > lo ? (hi - lo + kNT * U - 1) / (kNT * U) : 0;
-    const int per = (batches + kGroups / kNT - 1) / (kGroups / kNT);   // batches per group
-    int in_group = 0, group = tid;
-    float gm = -kInf;
-    for (int b = 0; b < batches; ++b) {
-        const int k = lo + tid + kNT * U * b;
-        float g = -kInf;
-        if (k + kNT * (U - 1) < hi) {
-            Chunk<T> ch[U];
+    const int n = max(hi - lo, 0);   // whole chunks
+    const __amdgpu_buffer_rsrc_t in = window(row.chunk(lo), n);
+    for (int b = 0; b < n; b += NT * U) {
+        Chunk<T> ch[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                ch[u].stream(row.chunk(k + kNT * u));
+        for (int u = 0; u < U; ++u)   // chunks past the segment are not read
+            ch[u].r = __builtin_bit_cast(decltype(ch[u].r),
+                                         __builtin_amdgcn_raw_buffer_load_b128(
+                                             in, tid * 16, (b + NT * u) * 16, kLoadStreamPolicy));
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float x[W];
-                ch[u].widen(x);
-                float m = x[0];
+        for (int u = 0; u < U; ++u) {
+            const int first = b + NT * u;
+            if (first >= n)
+                break;
+            if (first + NT > n && first + tid >= n)
+                ch[u].clear();
+            float x[W];
+            ch[u].widen(x);
+            float m = x[0];
 #pragma unroll
-                for (int i = 1; i < W; ++i)
-                    m = __builtin_fmaxf(m, x[i]);
-                q.add_with_max<W, ENT>(x, m, sc);
-                g = __builtin_fmaxf(g, m);
-            }
-        } else {
-            for (int kk = k; kk < hi; kk += kNT) {
-                Chunk<T> ch;
-                ch.stream(row.chunk(kk));
-                float x[W];
-                ch.widen(x);
-                float m = x[0];
-#pragma unroll
-                for (int i = 1; i < W; ++i)
-                    m = __builtin_fmaxf(m, x[i]);
-                q.add_with_max<W, ENT>(x, m, sc);
-                g = __builtin_fmaxf(g, m);
-            }
-        }
-        if constexpr (TOP) {
-            gm = __builtin_fmaxf(gm, g);
-            if (++in_group == per || b + 1 == batches) {
-                sh.gmax[group] = gm;
-                gm = -kInf;
-                group += kNT;
-                in_group = 0;
+            for (int i = 1; i < W; ++i)
+                m = __builtin_fmaxf(m, x[i]);
+            q.add_with_max<W, ENT>(x, m, sc);
+            if constexpr (TOP) {
+                m = group_max<kGroup / W>(m);
+                if ((tid & (kGroup / W - 1)) == 0 && first + tid < n)
+                    sh.gmax[(first + tid) / (kGroup / W)] = (uint16_t)(ord32(m) >> 16);
             }
         }
     }
@@ -388,31 +445,30 @@ __global__ __launch_bounds__(kNT) void logprob_kernel(LogprobArgs a, int64_t row
         const float x[1] = {row.at(e)};
         q.add<1, ENT>(x, sc);
     }
-    const Total t = block_total<ENT>(q, sc, tot);
-    if (segs == 1)
-        finish_logprob(a, row_i, token_logit<T>(a, row_i), t);
-    else if (tid == 0)
+    const Total t = block_total<ENT, NT / kWave>(q, sc, tot);
+    if (segs > 1 && tid == 0)
         a.parts[row_i * segs + seg] = LossPart{t.m, t.s, t.a, 0.0f};
     if constexpr (TOP) {
-        const int groups = per ? (batches + per - 1) / per * kNT : 0;
-        const int n = max(min(k1 * W - row.phase, row.vocab) - max(k0 * W - row.phase, 0), 0);
+        const int elems = max(min(k1 * W - row.phase, row.vocab) - max(k0 * W - row.phase, 0), 0);
         __syncthreads();
         if (t.s != t.s) {   // a NaN or +inf logit: no order, no alternatives
             if (segs == 1)
                 put_none(a, row_i, 0, t);
         } else if (segs == 1) {
             const float log2s = log2f(t.s);
-            select_top<T, U>(sh, row, k0, k1, groups, per, a.top_k,
-                             [&](int r, uint64_t key) { put_top(a, row_i, r, key, t, log2s); });
-            put_none(a, row_i, n, t);
+            select_top<T, NT>(sh, row, k0, k1, a.top_k,
+                              [&](int r, uint64_t key) { put_top(a, row_i, r, key, t, log2s); });
+            put_none(a, row_i, elems, t);
         } else {
             uint64_t *out = a.keys + (row_i * segs + seg) * a.top_k;
-            select_top<T, U>(sh, row, k0, k1, groups, per, a.top_k,
-                             [&](int r, uint64_t key) { out[r] = key; });
-            for (int i = n + tid; i < a.top_k; i += kNT)
+            select_top<T, NT>(sh, row, k0, k1, a.top_k,
+                              [&](int r, uint64_t key) { out[r] = key; });
+            for (int i = elems + tid; i < a.top_k; i += NT)
                 out[i] = 0;   // below every logit's key
         }
     }
+    if (segs == 1)
+        finish_logprob(a, row_i, given, t);
 }
 
 template <bool TOP>
@@ -437,29 +493,41 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
         const uint64_t *keys = a.keys + row * segs * a.top_k;
         const int n = segs * a.top_k;
         const float log2s = log2f(t.s);
-        if (tid == 0)
+        if (tid == 0) {
             sh.count = 0;
+            sh.floor64 = ~uint64_t(0);
+        }
         __syncthreads();
-        uint64_t least = 1;   // absent alternatives are zero keys
-        if (n > kCands) {
-            // at least K keys are not zero where the row has K logits; if it has
-            // fewer, the K-th is zero and every key that is not stays
+        // each segment's alternatives are in order: the least of their
+        // ceil(K / segs)-th ones is reached by K
+        const int step = (a.top_k + segs - 1) / segs - 1;
+        for (int i = tid; i < segs; i += kNT)
+            atomicMin(&sh.floor64, (unsigned long long)keys[(int64_t)i * a.top_k + step]);
+        __syncthreads();
+        uint64_t least = sh.floor64;
+        if (least == 0)
+            least = 1;   // absent alternatives are zero keys
+        for (int i = tid; i < n; i += kNT)
+            if (keys[i] >= least)
+                push(sh, keys[i]);
+        __syncthreads();
+        if (sh.count > (unsigned)kCands) {
+            __syncthreads();
             least = kth_key(sh, a.top_k, [&](auto f) {
                 for (int i = tid; i < n; i += kNT)
                     f(keys[i]);
             });
-            if (least == 0)
-                least = 1;
+            if (tid == 0)
+                sh.count = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += kNT)
+                if (keys[i] >= max(least, uint64_t(1)))
+                    push(sh, keys[i]);
+            __syncthreads();
         }
-        for (int i = tid; i < n; i += kNT) {
-            const uint64_t k = keys[i];
-            if (k >= least)
-                push(sh, k);
-        }
-        __syncthreads();
         const int cands = min((int)sh.count, kCands);
-        put_ranked(sh, cands, a.top_k,
-                   [&](int r, uint64_t key) { put_top(a, row, r, key, t, log2s); });
+        put_ranked<kNT>(sh, cands, a.top_k,
+                        [&](int r, uint64_t key) { put_top(a, row, r, key, t, log2s); });
         put_none(a, row, cands, t);
     }
 }
@@ -592,8 +660,13 @@ template <typename T, bool ENT, bool TOP>
 int launch_logprob_t(const LogprobArgs &a, int segs, hipStream_t st)
 {
     const int cps = chunks_per<T>(a.in.vocab, segs);
+    if (segs == 1 && wide_rows(a.in)) {
+        hipLaunchKernelGGL((logprob_kernel<T, kWide, ENT, TOP>), dim3((unsigned)a.in.rows), dim3(kWide), 0,
+                           st, a, (int64_t)0, 1, cps);
+        return hipGetLastError();
+    }
     if (int e = each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
-            hipLaunchKernelGGL((logprob_kernel<T, ENT, TOP>), dim3(n * (unsigned)segs), dim3(kNT), 0,
+            hipLaunchKernelGGL((logprob_kernel<T, kNT, ENT, TOP>), dim3(n * (unsigned)segs), dim3(kNT), 0,
                                st, a, r, segs, cps);
         }))
         return e;

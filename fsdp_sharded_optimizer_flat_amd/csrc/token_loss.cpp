@@ -134,14 +134,17 @@ zero_status done(int e, const char *where) { return e == hipSuccess ? ZERO_OK : 
 int32_t loss_segments(int64_t rows, int64_t vocab, int32_t top_k)
 {
     // One workgroup per row keeps the whole chip busy from about 1024 rows on
-    // (4 workgroups on each of 256 compute units); fewer rows are cut so that
+    // (4 workgroups on each of 256 compute units).  Fewer rows are cut so that
     // there are about that many workgroups, in segments of at least 2048
-    // elements and 32 per wanted alternative, with at most 4096 alternatives
-    // for the joining workgroup.  A function of the sizes alone, so the result
-    // does not depend on the device's state.
+    // elements and 128 per wanted alternative (two groups of the selection), with at most 4096 alternatives
+    // for the joining workgroup -- unless a workgroup of 1024 threads sums a row
+    // sooner than a second launch joins its segments.  A function of the sizes
+    // alone, so the result does not depend on the device's state.
+    if (rows <= kLossWideRows && vocab <= kLossWideVocab)
+        return 1;
     const int64_t need = (vocab + kLossMaxSegment - 1) / kLossMaxSegment;
     int64_t segs = rows > 0 ? (1024 + rows - 1) / rows : 1;
-    const int64_t least = top_k > 64 ? 32 * (int64_t)top_k : 2048;
+    const int64_t least = top_k > 16 ? 128 * (int64_t)top_k : 2048;
     if (segs > vocab / least)
         segs = vocab / least;
     if (top_k > 0 && segs > 4096 / top_k)

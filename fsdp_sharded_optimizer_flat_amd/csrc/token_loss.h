@@ -14,6 +14,10 @@ static_assert(ZERO_MAX_TOP <= kLossBlock, "one listed token per thread");
 // Most elements one workgroup reduces: its bitmap of listed tokens is 16 KiB.
 constexpr int64_t kLossMaxSegment = int64_t(1) << 17;
 
+// Up to this many rows of at most kLossWideVocab elements are not cut: a workgroup
+// of 1024 threads sums each.
+constexpr int64_t kLossWideRows = 256, kLossWideVocab = int64_t(1) << 16;
+
 // The rows of a call: `logits` in rows of `stride` elements, `vocab` used.
 struct LossRows {
     const void *logits;

@@ -50,6 +50,7 @@ template <>
 struct Chunk<uint16_t> {
     static constexpr int W = 8;
     u32x4 r;
+    __device__ __forceinline__ void clear() { r = u32x4{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }   // -inf
     __device__ __forceinline__ void load(const uint16_t *p) { r = *reinterpret_cast<const u32x4 *>(p); }
     __device__ __forceinline__ void stream(const uint16_t *p)
     {
@@ -69,6 +70,7 @@ template <>
 struct Chunk<float> {
     static constexpr int W = 4;
     f32x4 r;
+    __device__ __forceinline__ void clear() { r = f32x4{-kInf, -kInf, -kInf, -kInf}; }
     __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const f32x4 *>(p); }
     __device__ __forceinline__ void stream(const float *p)
     {
@@ -514,7 +516,6 @@ struct HeldRow {
     template <typename F>
     __device__ __forceinline__ void each_group(F f)
     {
-        constexpr unsigned none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
 #pragma unroll
         for (int i = 0; i < H; i += G) {
             if (NT * i < n) {
@@ -525,7 +526,7 @@ struct HeldRow {
                     if (NT * (i + j + 1) > n) {   // at most one chunk of the row: kept a branch
                         asm volatile("");
                         if (NT * (i + j) + (int)threadIdx.x >= n)
-                            ch[i + j].r = __builtin_bit_cast(decltype(ch[0].r), u32x4{none, none, none, none});
+                            ch[i + j].clear();
                     }
                     raw[j] = __builtin_bit_cast(u32x4, ch[i + j].r);
                     float y[W];
@@ -598,6 +599,10 @@ int chunks_per(int vocab, int segs)
     const int most = (vocab + 2 * (W - 1)) / W;
     return (most + segs - 1) / segs;
 }
+
+// Few rows that are not cut are summed by workgroups of kWide threads.
+constexpr int kWide = 1024;
+inline bool wide_rows(const LossRows &in) { return in.rows <= kLossWideRows && in.vocab > 4096; }
 
 // Workgroups of a launch that goes through rows: as many as are resident at once
 // (128 registers a thread: 16 waves on a compute unit), or one per row where

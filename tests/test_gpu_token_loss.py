@@ -262,7 +262,7 @@ def run_logprob(x, tokens, scale, k=0, entropy=True):
 
 # rows, vocab, row stride, elements into the allocation
 SIZES = [(1, 1, 1, 0), (2, 2, 5, 1), (3, 7, 7, 0), (5, 8, 8, 1), (4, 9, 9, 0), (6, 63, 64, 3),
-         (1, 4099, 4099, 0), (7, 1023, 1040, 2), (300, 2049, 2049, 0), (1100, 130, 130, 1),
+         (1, 4099, 4099, 0), (2, 70001, 70001, 1), (7, 1023, 1040, 2), (300, 2049, 2049, 0), (1100, 130, 130, 1),
          (1030, 5003, 5003, 0), (1, 50304, 50304, 0), (3, 50257, 50257, 5), (2, 131073, 131073, 0),
          (1025, 16500, 16512, 0), (1, 1 << 20, 1 << 20, 0), (2, (1 << 20) - 3, (1 << 20) - 3, 1)]
 DTYPES = [torch.bfloat16, torch.float32]
@@ -362,8 +362,8 @@ def test_distill_sizes(rows, vocab, stride, shift, dtype, mode):
 
 # -- rows that can go wrong ---------------------------------------------------------------
 
-# (rows, vocab): one workgroup per row, and rows cut for several
-WIDTHS = [(1100, 3001), (9, 40007)]
+# (rows, vocab): a small and a large workgroup per row, and rows cut for several
+WIDTHS = [(1100, 3001), (9, 40007), (9, 80021)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
@@ -707,7 +707,7 @@ def test_binding_refuses_mismatched_tensors():
         lambda: z.zero_logprob_grad(x, t, f, g, d_logprob=f),
         lambda: z.zero_distill(x, i[:3], v[:3], 0, loss=f),
         lambda: z.zero_distill_grad(x, i, v, 0, st[:, :2], f, g),
-        lambda: z.zero_logprob(make_logits(1, 50304, torch.bfloat16, 1), t[:1], logprob=f[:1],
+        lambda: z.zero_logprob(make_logits(1, 70001, torch.bfloat16, 1), t[:1], logprob=f[:1],
                                workspace=torch.zeros(8, dtype=torch.uint8, device=DEV)),
     ]
     for n, call in enumerate(bad):
