@@ -14,13 +14,13 @@ using namespace dev;
 // The K largest logits, ties to the lowest index, as keys that order them: the
 // logit's bits made monotonic, then the inverted index.  One pass over the row
 // leaves the largest logit of each group of kGroup in LDS (its upper 16 bits); a
-// group is a whole cache line of bf16, so that reading it again costs no more.  Of its groups each wave finds the ceil(K / waves)-th
-// largest maximum by bisection; the least of these is a bound that at least K
-// logits reach.  Only groups that reach it are read again (a little more than K
-// of them) and their logits that reach it become candidates, each ranked by the
-// number of larger ones.  Where there are too many (plateaus of equal logits, few
-// groups), a radix search over the whole keys, which are all different, finds the
-// K-th exactly.
+// group is a whole cache line of bf16, so that reading it again costs no more.  Of
+// its groups each wave finds the ceil(K / waves)-th largest maximum by bisection;
+// the least of these is a bound that at least K logits reach.  Only groups that
+// reach it are read again (a little more than K of them), and their logits that
+// reach it become candidates, each ranked by the number of larger ones.  Where
+// there are too many (plateaus of equal logits, few groups), a radix search over
+// the whole keys, which are all different, finds the K-th exactly.
 
 constexpr int kIndexBits = 20;
 static_assert(ZERO_MAX_VOCAB <= 1 << kIndexBits, "the index fits its field");
@@ -33,12 +33,11 @@ template <int N>
 __device__ __forceinline__ float group_max(float x)
 {
     static_assert(N == 8 || N == 16, "within a row of 16 lanes");
-    auto with = [&](int y) { x = __builtin_fmaxf(x, __int_as_float(y)); };
-    with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0xb1, 0xf, 0xf, true));    // lane ^ 1
-    with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x4e, 0xf, 0xf, true));    // lane ^ 2
-    with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x141, 0xf, 0xf, true));   // mirrored in 8
+    x = __builtin_fmaxf(x, from_lane<kLaneXor1>(x, x));
+    x = __builtin_fmaxf(x, from_lane<kLaneXor2>(x, x));
+    x = __builtin_fmaxf(x, from_lane<kMirror8>(x, x));
     if constexpr (N == 16)
-        with(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x140, 0xf, 0xf, true));   // in 16
+        x = __builtin_fmaxf(x, from_lane<kMirror16>(x, x));
     return x;
 }
 constexpr int kCands = 1024;
@@ -229,13 +228,15 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K,
         g[i] = tid + NT * i < groups ? sh.gmax[tid + NT * i] : 0u;
     // the waves with a group for each lane (the first, if none has)
     const int waves = max(min(groups / kWave, NW), 1), want = (K + waves - 1) / waves;
+    const int rounds = (groups + NT - 1) / NT;   // groups of a thread, at most Q
     unsigned bound = 0;
     for (int bit = 15; bit >= 0; --bit) {
         const unsigned v = bound | 1u << bit;
         int have = 0;
 #pragma unroll
         for (int i = 0; i < Q; ++i)
-            have += __popcll(__ballot(g[i] >= v));
+            if (i < rounds)
+                have += __popcll(__ballot(g[i] >= v));
         if (have >= want)
             bound = v;
     }
@@ -350,7 +351,7 @@ __device__ __forceinline__ void finish_logprob(const LogprobArgs &a, int64_t row
 template <typename T>
 __device__ __forceinline__ float token_logit(const LogprobArgs &a, int64_t row)
 {
-    const int64_t tok = a.tokens ? a.tokens[row] : -1;
+    const int64_t tok = a.tokens ? ld_uniform(a.tokens + row) : -1;
     return tok >= 0 && tok < a.in.vocab
                ? grad_at<T>(static_cast<const T *>(a.in.logits) + row * a.in.stride, tok) : 0.0f;
 }
@@ -398,7 +399,7 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
     __shared__ typename std::conditional<TOP, Select, int>::type sh;
     const int64_t row_i = row0 + blockIdx.x / segs;
     const int seg = blockIdx.x % segs, tid = threadIdx.x;
-    if (a.tokens && a.tokens[row_i] < 0) {
+    if (a.tokens && ld_uniform(a.tokens + row_i) < 0) {
         if (segs == 1)
             pad_logprob(a, row_i);
         return;
@@ -478,13 +479,17 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
     __shared__ typename std::conditional<TOP, Select, int>::type sh;
     const int64_t row = row0 + blockIdx.x;
     const int tid = threadIdx.x;
-    if (a.tokens && a.tokens[row] < 0) {
+    if (a.tokens && ld_uniform(a.tokens + row) < 0) {
         pad_logprob(a, row);
         return;
     }
+    const float given = a.in.dtype == ZERO_BF16 ? token_logit<uint16_t>(a, row) : token_logit<float>(a, row);
+    uint64_t mine = 0;   // the first of this thread's keys: most rows have no more
+    if constexpr (TOP)
+        if (tid < segs * a.top_k)
+            mine = a.keys[row * segs * a.top_k + tid];
     const Total t = join_parts(a.parts + row * segs, segs, Scale(a.in.c), tot);
-    finish_logprob(a, row, a.in.dtype == ZERO_BF16 ? token_logit<uint16_t>(a, row)
-                                                   : token_logit<float>(a, row), t);
+    finish_logprob(a, row, given, t);
     if constexpr (TOP) {
         if (t.s != t.s) {
             put_none(a, row, 0, t);
@@ -507,9 +512,11 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
         uint64_t least = sh.floor64;
         if (least == 0)
             least = 1;   // absent alternatives are zero keys
-        for (int i = tid; i < n; i += kNT)
-            if (keys[i] >= least)
-                push(sh, keys[i]);
+        for (int i = tid; i < n; i += kNT) {
+            const uint64_t key = i == tid ? mine : keys[i];
+            if (key >= least)
+                push(sh, key);
+        }
         __syncthreads();
         if (sh.count > (unsigned)kCands) {
             __syncthreads();

@@ -277,19 +277,35 @@ struct Total {
     __device__ __forceinline__ bool empty() const { return s == 0.0f; }   // every logit -inf
 };
 
+// Over a wave, in every lane, in a fixed order: within rows of 16 lanes by
+// exchanges between neighbours, then row by row to the last lane (data-parallel
+// moves: a shuffle through LDS takes about ten times as long).
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float from_lane(float other, float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(other), __float_as_int(x), CTRL, ROWS,
+                                                      0xf, false));
+}
+constexpr int kLaneXor1 = 0xb1, kLaneXor2 = 0x4e, kMirror8 = 0x141, kMirror16 = 0x140;
+constexpr int kLastOfRow = 0x142, kLastOfHalf = 0x143;   // lane 15 / 31 to the next rows
+template <typename F>
+__device__ __forceinline__ float wave_reduce(float x, float neutral, F f)
+{
+    x = f(x, from_lane<kLaneXor1>(x, x));
+    x = f(x, from_lane<kLaneXor2>(x, x));
+    x = f(x, from_lane<kMirror8>(x, x));
+    x = f(x, from_lane<kMirror16>(x, x));
+    x = f(x, from_lane<kLastOfRow, 0xa>(neutral, x));
+    x = f(x, from_lane<kLastOfHalf, 0xc>(neutral, x));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
 __device__ __forceinline__ float wave_max(float x)
 {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        x = __builtin_fmaxf(x, __shfl_xor(x, o, kWave));
-    return x;
+    return wave_reduce(x, -kInf, [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
 __device__ __forceinline__ float wave_add(float x)
 {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        x += __shfl_xor(x, o, kWave);
-    return x;
+    return wave_reduce(x, 0.0f, [](float a, float b) { return a + b; });
 }
 
 // One of several totals moved to reference m and added.
@@ -308,25 +324,30 @@ __device__ __forceinline__ Total wave_total(Sum q, const Scale &k)
     q.rebase(m, k);
     return Total{m, wave_add(q.s), ENT ? wave_add(q.a) : 0.0f};
 }
-// The total of NW waves' totals, in every lane: each lane takes one of them, and
-// butterflies add them (a wave that holds a row has few registers to spare).
+// The total of NW waves' totals, in every lane: each lane takes one of them (a wave
+// that holds a row has few registers to spare).
 template <bool ENT, int NW>
 __device__ __forceinline__ Total add_waves(const Total *sh, const Scale &k)
 {
+    auto reduce = [](float x, auto f) {   // over 16 lanes, of which NW hold something
+        if constexpr (NW > 1)
+            x = f(x, from_lane<kLaneXor1>(x, x));
+        if constexpr (NW > 2)
+            x = f(x, from_lane<kLaneXor2>(x, x));
+        if constexpr (NW > 4)
+            x = f(x, from_lane<kMirror8>(x, x));
+        if constexpr (NW > 8)
+            x = f(x, from_lane<kMirror16>(x, x));
+        return x;
+    };
     constexpr int M = NW <= 1 ? 1 : NW <= 2 ? 2 : NW <= 4 ? 4 : NW <= 8 ? 8 : 16;
     const int i = threadIdx.x & (M - 1);
     const Total own = i < NW ? sh[i] : Total{kLowest, 0.0f, 0.0f};
-    Total t{own.m, 0.0f, 0.0f};
-#pragma unroll
-    for (int o = M / 2; o >= 1; o >>= 1)
-        t.m = __builtin_fmaxf(t.m, __shfl_xor(t.m, o, kWave));
+    Total t{reduce(own.m, [](float a, float b) { return __builtin_fmaxf(a, b); }), 0.0f, 0.0f};
     add_total(t, own, k);
-#pragma unroll
-    for (int o = M / 2; o >= 1; o >>= 1) {
-        t.s += __shfl_xor(t.s, o, kWave);
-        if constexpr (ENT)
-            t.a += __shfl_xor(t.a, o, kWave);
-    }
+    t.s = reduce(t.s, [](float a, float b) { return a + b; });
+    if constexpr (ENT)
+        t.a = reduce(t.a, [](float a, float b) { return a + b; });
     return t;
 }
 // Every thread gets the workgroup's total.  `sh`: one Total per wave.  One
