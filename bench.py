@@ -129,6 +129,13 @@ def parse():
                          "dW = dY^T X (MFMA) or a copy of resident gradients (HBM)")
     ap.add_argument("--tokens", type=int, default=1024,
                     help="tokens per simulated rank of the --streamed GEMM producer")
+    ap.add_argument("--loss", default="none", choices=["none", "lm", "distill"],
+                    help="with --streamed --workload gpt2l: start each pass with every simulated "
+                         "rank's loss over its tokens' logits and take the head's weight gradient "
+                         "from it: the language-model loss (zero_logprob_fused), or the record of "
+                         "a teacher's top logits and the distillation loss against it "
+                         "(zero_logprob, zero_distill_fused)")
+    ap.add_argument("--top-k", type=int, default=64, help="logits of a teacher's record (--loss distill)")
     ap.add_argument("--reshard", default=None, metavar="NAME",
                     help="time a checkpoint reshard (gpt2l_reshard, llama8b_reshard) instead of "
                          "the step: one destination rank's fp32 shard from flat block units to "
@@ -740,6 +747,14 @@ def streamed_bench(args):
               make the stand-in launch-bound);
       copy -- the unit's buckets copied from resident gradients (HBM-bound).
 
+    With --loss the pass starts as backward does, at the loss: each rank's
+    logits (tokens x vocabulary, bf16) give the loss and d(logits), and the
+    token embedding's weight gradient (the tied head's) is
+    d(logits)^T X; `loss_only` times that part.  lm: zero_logprob_fused, the
+    mean negative log probability; distill: the teacher's top-k logits
+    (zero_logprob) and the renormalised divergence from them
+    (zero_distill_fused), the mean over the rank's tokens.
+
     Three passes over the whole model, each timed between synchronizations
     (median of `steps` repetitions after `warmup`): the producer alone;
     serial -- produce unit k, then step it (zero_step_units), one stream;
@@ -758,6 +773,10 @@ def streamed_bench(args):
     wl = workload_from_args(args)
     if wl.rank >= 0 or wl.grad_index != "global":
         raise SystemExit("--streamed runs the all-ranks workloads (gpt2l, gpt2l_block)")
+    if args.loss != "none" and (args.workload != "gpt2l" or args.producer != "gemm"):
+        raise SystemExit("--loss needs --workload gpt2l (a head) and --producer gemm")
+    if args.loss == "distill" and not 1 <= args.top_k <= z.ZERO_MAX_TOP:
+        raise SystemExit(f"--top-k must be between 1 and {z.ZERO_MAX_TOP}")
     n, h = wl.n_ranks, wl.hyper
     dev = torch.device("cuda:0")
     L = z.zero_pack(n, wl.unit_numel)
@@ -788,6 +807,32 @@ def streamed_bench(args):
         for r in range(n):
             synth.fill_grad_(src[r], wl.grad_dist, wl.grad_scale, synth.seed_of(wl.seed, synth.TAG_GRAD, 1, r))
         flops = 0.0
+    loss_bytes = 0
+    if args.loss != "none":
+        V = workloads.VOCAB_GPT2L
+        logits = (torch.randn(tok, V, device=dev) * 2.0).to(torch.bfloat16)
+        d_logits = torch.empty(n, tok, V, dtype=torch.bfloat16, device=dev)
+        targets = torch.randint(0, V, (n, tok), device=dev)
+        row_loss = torch.empty(n, tok, device=dev)
+        weight = torch.full((tok,), (-1.0 if args.loss == "lm" else 1.0) / tok, device=dev)
+        loss_ws = torch.empty(max(z.zero_loss_workspace_bytes(tok, V, args.top_k), 1),
+                              dtype=torch.uint8, device=dev)
+        loss_bytes = n * tok * V * 2 * 2
+        if args.loss == "distill":
+            teacher = (torch.randn(tok, V, device=dev) * 2.0).to(torch.bfloat16)
+            top_i = torch.empty(tok, args.top_k, dtype=torch.int32, device=dev)
+            top_v = torch.empty(tok, args.top_k, device=dev)
+            loss_bytes = n * tok * V * 2 * 3
+
+    def loss():
+        for r in range(n):
+            if args.loss == "lm":
+                z.zero_logprob_fused(logits, targets[r], d_logits[r], d_logprob=weight,
+                                     logprob=row_loss[r], workspace=loss_ws)
+            elif args.loss == "distill":
+                z.zero_logprob(teacher, top_index=top_i, top_logprob=top_v, workspace=loss_ws)
+                z.zero_distill_fused(logits, top_i, top_v, z.ZERO_DISTILL_RENORM, weight, d_logits[r],
+                                     loss=row_loss[r], workspace=loss_ws)
 
     def produce(u, slot):
         pad = int(T[u, 1])
@@ -799,7 +844,9 @@ def streamed_bench(args):
             at = 0
             for s in shapes[u]:
                 k = workloads.numel_of(s)
-                if len(s) == 2:   # dW [out, in] = dY^T [out, T] @ X [T, in]
+                if args.loss != "none" and u == 0 and at == 0:   # the token embedding, the tied head
+                    torch.matmul(d_logits[r].t(), X[s[1]], out=slots[slot, r, :k].view(s[0], s[1]))
+                elif len(s) == 2:   # dW [out, in] = dY^T [out, T] @ X [T, in]
                     torch.matmul(dYT[:s[0]], X[s[1]], out=slots[slot, r, at:at + k].view(s[0], s[1]))
                 at += k
 
@@ -817,11 +864,13 @@ def streamed_bench(args):
     order = list(range(U - 1, -1, -1))
 
     def producer_only():
+        loss()
         for i, u in enumerate(order):
             produce(u, i % 2)
 
     def serial():
         s = sc()
+        loss()
         for i, u in enumerate(order):
             produce(u, i % 2)
             step_unit(u, i % 2, main, s)
@@ -829,6 +878,7 @@ def streamed_bench(args):
     def overlapped():
         s = sc()
         stepped = [None] * U
+        loss()
         for i, u in enumerate(order):
             if i >= 2:
                 main.wait_event(stepped[i - 2])
@@ -880,6 +930,8 @@ def streamed_bench(args):
                      ("serial", serial), ("overlapped", overlapped), ("serial_again", serial),
                      ("overlapped_again", overlapped), ("overlapped_uncapped", overlapped_uncapped)):
         res[name] = timed(fn)
+    if args.loss != "none":
+        res["loss_only"] = timed(loss)
     del slots
     if args.producer == "copy":
         del src
@@ -913,6 +965,11 @@ def streamed_bench(args):
         "producer_tflops": flops / (res["producer_only"][0] / 1e3) / 1e12 if flops else None,
         "timing": "wall clock between synchronizations, median of `steps` passes after `warmup`",
     }
+    if args.loss != "none":
+        result["config"].update(loss=args.loss, vocab=V,
+                                teacher_top_k=args.top_k if args.loss == "distill" else None)
+        result["loss_hbm_GBps"] = loss_bytes / (res["loss_only"][0] / 1e3) / 1e9
+        result["mean_loss"] = float(row_loss.mean()) * (-1.0 if args.loss == "lm" else 1.0)
     print(json.dumps(result))
 
 

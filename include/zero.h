@@ -575,23 +575,24 @@ zero_status zero_clip_coef_ranks_async(const double *rank_sums_dev, int32_t n_ra
  * Logits: `rows` rows of `vocab` elements of `dtype` (ZERO_F32 / ZERO_BF16),
  * row r at logits + r * row_stride; 1 <= vocab <= ZERO_MAX_VOCAB, row_stride >=
  * vocab.  A logit of -inf has probability zero.  Sums are held in binary32
- * (listed tokens and the teacher's q in binary64), in a fixed order: the same
- * call gives the same bits.  d_logits has the logits' dtype (each element
+ * (the teacher's q in binary64), in a fixed order: the same call gives the same
+ * bits.  d_logits has the logits' dtype (each element
  * rounded once) and its own row stride; elements past a row's vocab are left as
  * they are.  It may be the logits themselves (same pointer and stride): each
  * row is then read before it is written.  2^-20 <= scale <= 2^20.
  *
  * Rows that have no distribution, or no target:
  *   - a negative token, or a teacher's record of negative indices only (and no
- *     NaN value), marks a padding row: it is not read, its outputs and its gradient are zero, and
- *     its top alternatives index -1, log probability -inf;
+ *     NaN value), marks a padding row: it is not read, its outputs and its
+ *     gradient are zero, and its top alternatives index -1, log probability
+ *     -inf;
  *   - upstream weights of zero give a zero gradient, whatever the row holds;
  *   - a row whose logits are all -inf: logprob -inf, entropy 0, a loss of
  *     +inf, no alternatives, gradient zero;
  *   - a row with a NaN or +inf logit: NaN everywhere (alternatives index -1);
  *   - a token, or an index of a teacher's record, >= vocab, or a NaN value in
- *     the record: logprob, loss and the gradient row are NaN.  A NaN gradient has no clip coefficient, so
- *     zero_step_device_clip skips its step.
+ *     the record: logprob, loss and the gradient row are NaN.  A NaN gradient
+ *     has no clip coefficient, so zero_step_device_clip skips its step.
  * Alternatives past the row's finite logits have index -1, log probability
  * -inf.
  *
@@ -613,7 +614,8 @@ zero_status zero_clip_coef_ranks_async(const double *rank_sums_dev, int32_t n_ra
 
 /* Workspace bytes that are enough for each of the calls below on `rows` rows of
  * `vocab` logits (top_k alternatives for zero_logprob; 16-byte aligned device
- * memory).  Where it is 0 the workspace may be NULL. */
+ * memory).  A call that needs none (where this is 0; zero_*_fused on rows that
+ * it holds on the chip) takes a NULL workspace. */
 zero_status zero_loss_workspace_bytes(int64_t rows, int64_t vocab, int32_t top_k, size_t *bytes);
 
 /* Forward: any of logprob [rows], entropy [rows], stats [rows][2] and, with
