@@ -40,7 +40,7 @@ __device__ __forceinline__ float group_max(float x)
         x = __builtin_fmaxf(x, from_lane<kMirror16>(x, x));
     return x;
 }
-constexpr int kCands = 1024;
+constexpr int kCands = 1024, kPad = 16;
 
 __device__ __forceinline__ unsigned ord32(float x)
 {
@@ -70,7 +70,7 @@ struct Select {
     unsigned long long floor64;
     alignas(16) uint16_t gmax[kGroups];
     uint16_t list[kGroups];
-    alignas(16) uint64_t cand[kCands];
+    alignas(16) uint64_t cand[kCands + kPad];
     // the K largest of many candidates, once the groups are done with
     __device__ __forceinline__ uint64_t *best() { return reinterpret_cast<uint64_t *>(gmax); }
 };
@@ -190,53 +190,48 @@ __device__ __forceinline__ void put_ranked(Select &sh, int n, int K, Put put)
         for (int i = tid; i < n; i += NT)
             if (sh.cand[i] >= kth)
                 cand[atomicAdd(&sh.count, 1u)] = sh.cand[i];
-        __syncthreads();
         n = K;
-    } else if ((n & 1) && n < kCands) {
-        if (tid == 0)
-            cand[n] = 0;   // below every key: they are compared in pairs
-        __syncthreads();
     }
+    if (tid < kPad)   // below every key: they are compared in batches
+        cand[n + tid] = 0;
+    __syncthreads();
     for (int i = tid; i < n; i += NT) {
         const uint64_t own = cand[i];
         int rank = 0;
-        for (int j = 0; j < n; j += 2) {
-            const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(cand + j);
-            rank += (o.x > own) + (j + 1 < n && o.y > own);
+        for (int j = 0; j < n; j += kPad) {   // kPad / 2 reads on their way at once
+            ulonglong2 o[kPad / 2];
+#pragma unroll
+            for (int u = 0; u < kPad / 2; ++u)
+                o[u] = *reinterpret_cast<const ulonglong2 *>(cand + j + 2 * u);
+#pragma unroll
+            for (int u = 0; u < kPad / 2; ++u)
+                rank += (o[u].x > own) + (o[u].y > own);
         }
         if (rank < K)
             put(rank, own);
     }
 }
 
-// The K largest logits of chunks [k0, k1).  Group g of their whole chunks is
-// elements kGroup g .. + kGroup - 1; sh.gmax holds the upper 16 bits of its
-// largest logit's order.
-template <typename T, int NT, typename Put>
-__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K, Put put)
+// A bound (the upper 16 bits of a logit's order) that at least K logits of the
+// groups reach, and the list of the groups that reach it; at most Q to a thread.
+template <int NT, int Q>
+__device__ __forceinline__ unsigned list_groups(Select &sh, int groups, int K)
 {
-    constexpr int W = Row<T>::W, NW = NT / kWave, L = kGroup / W, Q = (kGroups + NT - 1) / NT;
+    constexpr int NW = NT / kWave;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    const int groups = (max(hi - lo, 0) + L - 1) / L;
-    const int first = max(k0 * W - row.phase, 0), last = min(k1 * W - row.phase, row.vocab);
-    const int n = max(last - first, 0);
-    // this thread's groups, and the wave's bound
     unsigned g[Q];
 #pragma unroll
     for (int i = 0; i < Q; ++i)
         g[i] = tid + NT * i < groups ? sh.gmax[tid + NT * i] : 0u;
     // the waves with a group for each lane (the first, if none has)
     const int waves = max(min(groups / kWave, NW), 1), want = (K + waves - 1) / waves;
-    const int rounds = (groups + NT - 1) / NT;   // groups of a thread, at most Q
     unsigned bound = 0;
     for (int bit = 15; bit >= 0; --bit) {
         const unsigned v = bound | 1u << bit;
         int have = 0;
 #pragma unroll
         for (int i = 0; i < Q; ++i)
-            if (i < rounds)
-                have += __popcll(__ballot(g[i] >= v));
+            have += __popcll(__ballot(g[i] >= v));
         if (have >= want)
             bound = v;
     }
@@ -251,8 +246,6 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K,
 #pragma unroll
     for (int w = 0; w < NW; ++w)
         bound = min(bound, sh.floor[w]);
-    const float least = bound <= 0x7fu ? -kInf : ord32_value(bound << 16);
-    // the groups that reach the bound
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < Q; ++i)
@@ -270,6 +263,24 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K,
         at += __popcll(m);
     }
     __syncthreads();
+    return bound;
+}
+
+// The K largest logits of chunks [k0, k1).  Group g of their whole chunks is
+// elements kGroup g .. + kGroup - 1; sh.gmax holds the upper 16 bits of its
+// largest logit's order.
+template <typename T, int NT, typename Put>
+__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K, Put put)
+{
+    constexpr int W = Row<T>::W, L = kGroup / W;
+    const int tid = threadIdx.x;
+    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    const int groups = (max(hi - lo, 0) + L - 1) / L;
+    const int first = max(k0 * W - row.phase, 0), last = min(k1 * W - row.phase, row.vocab);
+    const int n = max(last - first, 0);
+    const unsigned bound = groups <= NT ? list_groups<NT, 1>(sh, groups, K)
+                                        : list_groups<NT, (kGroups + NT - 1) / NT>(sh, groups, K);
+    const float least = bound <= 0x7fu ? -kInf : ord32_value(bound << 16);
     const int todo = (int)sh.listed * L;
     auto chunk_of = [&](int j) { return lo + sh.list[j / L] * L + j % L; };
     auto look = [&](const Chunk<T> &ch, int k) {
@@ -324,10 +335,11 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K,
 // -- log probabilities: forward ----------------------------------------------------------
 
 // A row's outputs from its total and the given token's logit (anything where
-// the token is outside the vocabulary); the top alternatives go out separately.
+// the token is outside the vocabulary), by one lane of the workgroup's last wave:
+// the first ranks the top alternatives.
 __device__ __forceinline__ void finish_logprob(const LogprobArgs &a, int64_t row, float l, const Total &t)
 {
-    if (threadIdx.x != 0)
+    if (threadIdx.x != blockDim.x - kWave)
         return;
     const Scale k(a.in.c);
     const bool none = t.empty();
@@ -394,7 +406,7 @@ template <typename T, int NT, bool ENT, bool TOP>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT == kNT ? 8 : 4)))
 void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
 {
-    constexpr int U = 4, W = Row<T>::W;
+    constexpr int U = NT == kWide ? 8 : 4, W = Row<T>::W;   // chunks on their way to a thread
     __shared__ Total tot[NT / kWave];
     __shared__ typename std::conditional<TOP, Select, int>::type sh;
     const int64_t row_i = row0 + blockIdx.x / segs;
@@ -408,7 +420,7 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
     const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    const float given = segs == 1 && tid == 0 ? token_logit<T>(a, row_i) : 0.0f;
+    const float given = segs == 1 ? token_logit<T>(a, row_i) : 0.0f;
     const Scale sc(a.in.c);
     Sum q;
     const int n = max(hi - lo, 0);   // whole chunks
@@ -484,10 +496,21 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
         return;
     }
     const float given = a.in.dtype == ZERO_BF16 ? token_logit<uint16_t>(a, row) : token_logit<float>(a, row);
-    uint64_t mine = 0;   // the first of this thread's keys: most rows have no more
-    if constexpr (TOP)
+    // each segment's alternatives are in order: the least of their ceil(K /
+    // segs)-th ones is reached by K
+    const int step = (a.top_k + segs - 1) / segs - 1;
+    const uint64_t *keys = a.keys + row * segs * a.top_k;
+    uint64_t mine = 0, floor = ~uint64_t(0);   // on their way while the parts are added
+    if constexpr (TOP) {
         if (tid < segs * a.top_k)
-            mine = a.keys[row * segs * a.top_k + tid];
+            mine = keys[tid];
+        if (tid < segs)
+            floor = keys[tid * a.top_k + step];
+        if (tid == 0) {
+            sh.count = 0;
+            sh.floor64 = ~uint64_t(0);
+        }
+    }
     const Total t = join_parts(a.parts + row * segs, segs, Scale(a.in.c), tot);
     finish_logprob(a, row, given, t);
     if constexpr (TOP) {
@@ -495,19 +518,12 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
             put_none(a, row, 0, t);
             return;
         }
-        const uint64_t *keys = a.keys + row * segs * a.top_k;
         const int n = segs * a.top_k;
         const float log2s = log2f(t.s);
-        if (tid == 0) {
-            sh.count = 0;
-            sh.floor64 = ~uint64_t(0);
-        }
-        __syncthreads();
-        // each segment's alternatives are in order: the least of their
-        // ceil(K / segs)-th ones is reached by K
-        const int step = (a.top_k + segs - 1) / segs - 1;
-        for (int i = tid; i < segs; i += kNT)
-            atomicMin(&sh.floor64, (unsigned long long)keys[(int64_t)i * a.top_k + step]);
+        for (int i = tid + kNT; i < segs; i += kNT)
+            floor = min(floor, keys[(int64_t)i * a.top_k + step]);
+        if (tid < segs)
+            atomicMin(&sh.floor64, (unsigned long long)floor);
         __syncthreads();
         uint64_t least = sh.floor64;
         if (least == 0)
