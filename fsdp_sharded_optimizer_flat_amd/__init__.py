@@ -868,10 +868,8 @@ def zero_loss_workspace_bytes(rows: int, vocab: int, top_k: int = 0) -> int:
     return b.value
 
 
-def _on_device(t, dev, what: str):
-    if t.device != dev:
-        raise ValueError(f"{what} is on {t.device}, the logits on {dev}")
-
+# A call on a few rows takes the device about 10 us: these checks pass in one
+# condition each and name what is wrong only when it fails.
 
 def _rows_of(t, what: str):
     """(address, row stride) of a 2-D device tensor whose rows are contiguous."""
@@ -880,50 +878,57 @@ def _rows_of(t, what: str):
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor (got {t.device})")
     n, v = t.shape
-    if v > 1 and t.stride(1) != 1:
+    stride, step = t.stride()
+    if v > 1 and step != 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else max(v, 1)
+    return t.data_ptr(), stride if n > 1 else max(v, 1)
 
 
 def _logits(t):
-    """(address, dtype, rows, vocab, row stride, device) of the logits, which
-    must be on the current device (the calls run on its streams)."""
+    """(address, dtype, rows, vocab, row stride, device index) of the logits,
+    which must be on the current device (the calls run on its streams)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("logits must be a torch tensor")
     ptr, stride = _rows_of(t, "logits")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"logits are on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    dt = ZERO_BF16 if t.dtype == torch.bfloat16 else ZERO_F32 if t.dtype == torch.float32 else None
+    dt = ZERO_BF16 if t.dtype is torch.bfloat16 else ZERO_F32 if t.dtype is torch.float32 else None
     if dt is None:
         raise TypeError(f"logits must be bfloat16 or float32, got {t.dtype}")
-    return ptr, dt, t.shape[0], t.shape[1], stride, t.device
+    n, v = t.shape
+    return ptr, dt, n, v, stride, dev
 
 
-def _row_values(t, n: int, dev, what: str, dtype=None):
+def _on_device(t, dev: int, what: str):
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the logits on cuda:{dev}")
+
+
+def _row_values(t, n: int, dev: int, what: str, dtype=None):
     """Address of a contiguous device tensor of exactly n values (None: NULL)."""
     if t is None:
         return None
-    torch = _torch()
-    if t.dtype != (dtype or torch.float32):
-        raise TypeError(f"{what} must be {dtype or torch.float32}, got {t.dtype}")
-    ptr = _dev_ptr(t, what)
-    if t.numel() != n:
-        raise ValueError(f"{what} holds {t.numel()} values; the call needs {n}")
+    dtype = dtype or _torch().float32
+    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{what} must be a {dtype} tensor, got {getattr(t, 'dtype', type(t))}")
+    if t.get_device() == dev and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    _dev_ptr(t, what)
     _on_device(t, dev, what)
-    return ptr
+    raise ValueError(f"{what} holds {t.numel()} values; the call needs {n}")
 
 
 def _d_logits(t, logits):
-    if t.dtype != logits.dtype or t.shape != logits.shape:
+    if t.dtype is not logits.dtype or t.shape != logits.shape:
         raise ValueError("d_logits must have the logits' shape and dtype")
-    ptr, stride = _rows_of(t, "d_logits")
-    _on_device(t, logits.device, "d_logits")
-    return ptr, stride
+    _on_device(t, logits.get_device(), "d_logits")
+    return _rows_of(t, "d_logits")
 
 
-def _workspace(t, dev):
+def _workspace(t, dev: int):
     if t is None:
         return None, 0
     ptr = _dev_ptr(t, "workspace")
@@ -931,7 +936,7 @@ def _workspace(t, dev):
     return ptr, t.numel() * t.element_size()
 
 
-def _top(index, value, rows: int, dev, what):
+def _top(index, value, rows: int, dev: int, what):
     """(top_k, index address, value address) of (rows, top_k) tensors."""
     if index is None and value is None:
         return 0, None, None
@@ -939,9 +944,16 @@ def _top(index, value, rows: int, dev, what):
         raise ValueError(f"{what[0]} and {what[1]} go together")
     if index.dim() != 2 or index.shape != value.shape or index.shape[0] != rows:
         raise ValueError(f"{what[0]} and {what[1]} must have shape (rows, top_k)")
-    n = index.numel()
-    return (index.shape[1], _row_values(index, n, dev, what[0], _torch().int32),
-            _row_values(value, n, dev, what[1]))
+    k = index.shape[1]
+    return (k, _row_values(index, rows * k, dev, what[0], _torch().int32),
+            _row_values(value, rows * k, dev, what[1]))
+
+
+def _stream_on(stream, dev: int):
+    """_stream, the current stream's handle without an object around it."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def zero_logprob(logits, tokens=None, *, scale: float = 1.0, logprob=None, entropy=None, stats=None,
@@ -956,7 +968,7 @@ def zero_logprob(logits, tokens=None, *, scale: float = 1.0, logprob=None, entro
     _check(_zero_logprob(p, dt, n, v, st, scale, _row_values(tokens, n, dev, "tokens", _torch().int64),
                          _row_values(logprob, n, dev, "logprob"),
                          _row_values(entropy, n, dev, "entropy"),
-                         _row_values(stats, 2 * n, dev, "stats"), k, ip, tp, wp, wb, _stream(stream)),
+                         _row_values(stats, 2 * n, dev, "stats"), k, ip, tp, wp, wb, _stream_on(stream, dev)),
            "zero_logprob")
 
 
@@ -972,7 +984,7 @@ def zero_logprob_grad(logits, tokens, stats, d_logits, *, scale: float = 1.0, d_
                               _row_values(stats, 2 * n, dev, "stats"),
                               _row_values(entropy, n, dev, "entropy"),
                               _row_values(d_logprob, n, dev, "d_logprob"),
-                              _row_values(d_entropy, n, dev, "d_entropy"), gp, gs, _stream(stream)),
+                              _row_values(d_entropy, n, dev, "d_entropy"), gp, gs, _stream_on(stream, dev)),
            "zero_logprob_grad")
 
 
@@ -989,7 +1001,7 @@ def zero_logprob_fused(logits, tokens, d_logits, *, scale: float = 1.0, d_logpro
                                _row_values(d_entropy, n, dev, "d_entropy"),
                                _row_values(logprob, n, dev, "logprob"),
                                _row_values(entropy, n, dev, "entropy"), gp, gs, wp, wb,
-                               _stream(stream)), "zero_logprob_fused")
+                               _stream_on(stream, dev)), "zero_logprob_fused")
 
 
 _RECORD = ("top_index", "top_value")
@@ -1004,7 +1016,7 @@ def zero_distill(logits, top_index, top_value, mode: int, *, scale: float = 1.0,
     k, ip, tp = _top(top_index, top_value, n, dev, _RECORD)
     wp, wb = _workspace(workspace, dev)
     _check(_zero_distill(p, dt, n, v, st, scale, k, ip, tp, mode, _row_values(loss, n, dev, "loss"),
-                         _row_values(stats, 4 * n, dev, "stats"), wp, wb, _stream(stream)),
+                         _row_values(stats, 4 * n, dev, "stats"), wp, wb, _stream_on(stream, dev)),
            "zero_distill")
 
 
@@ -1017,7 +1029,7 @@ def zero_distill_grad(logits, top_index, top_value, mode: int, stats, d_loss, d_
     gp, gs = _d_logits(d_logits, logits)
     _check(_zero_distill_grad(p, dt, n, v, st, scale, k, ip, tp, mode,
                               _row_values(stats, 4 * n, dev, "stats"),
-                              _row_values(d_loss, n, dev, "d_loss"), gp, gs, _stream(stream)),
+                              _row_values(d_loss, n, dev, "d_loss"), gp, gs, _stream_on(stream, dev)),
            "zero_distill_grad")
 
 
@@ -1030,7 +1042,7 @@ def zero_distill_fused(logits, top_index, top_value, mode: int, d_loss, d_logits
     wp, wb = _workspace(workspace, dev)
     _check(_zero_distill_fused(p, dt, n, v, st, scale, k, ip, tp, mode,
                                _row_values(d_loss, n, dev, "d_loss"),
-                               _row_values(loss, n, dev, "loss"), gp, gs, wp, wb, _stream(stream)),
+                               _row_values(loss, n, dev, "loss"), gp, gs, wp, wb, _stream_on(stream, dev)),
            "zero_distill_fused")
 
 
