@@ -131,8 +131,9 @@ __device__ __forceinline__ bool mark_listed(unsigned *bits, int words, const int
 }
 
 // Reads a row's record and the listed tokens' logits (one whole wave calls it).
-// `twice`: some token is named by several entries.  Loops over a lane's entries are kept rolled and the entries in LDS: the wave
-// may hold a row in its registers meanwhile.
+// `twice`: some token is named by several entries.  Loops over a lane's entries are
+// kept rolled and the entries in LDS: the wave may hold a row in its registers
+// meanwhile.
 template <typename T>
 __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, const float *value,
                                              int K, int mode, const T *logits, int vocab,
@@ -295,11 +296,15 @@ constexpr int kBitWords = (int)(kLossMaxSegment / 32) + 8;
 
 // One workgroup per segment of a row: the sum over its tokens that the teacher
 // does not list, which a bitmap in LDS leaves out (subtracting the listed ones
-// from the whole sum would lose the rest's digits where little is left).
+// from the whole sum would lose the rest's digits where little is left).  A wide
+// workgroup (few rows, each whole: latency counts) leaves the record to its last
+// wave, beside the others' sums, and has its first chunks on their way before it
+// looks at anything else.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0, int segs, int cps)
 {
-    constexpr int U = 4, W = Row<T>::W;
+    constexpr bool kApart = NT == kWide;
+    constexpr int U = kApart ? 8 : 4, W = Row<T>::W, NS = kApart ? NT - kWave : NT;
     __shared__ Total tot[NT / kWave];
     __shared__ Teacher te;
     __shared__ alignas(16) unsigned bits[kBitWords];
@@ -311,46 +316,66 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0
     const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    const int n = max(hi - lo, 0);   // whole chunks
+    const __amdgpu_buffer_rsrc_t in = window(row.chunk(lo), n);
+    const bool teaches = tid / kWave == (kApart ? NS / kWave : 0);
+    Chunk<T> ch[U];
+    auto fetch = [&](int b) {   // chunks past the segment are not read
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            ch[u].r = __builtin_bit_cast(decltype(ch[u].r),
+                                         __builtin_amdgcn_raw_buffer_load_b128(
+                                             in, tid * 16, (b + NS * u) * 16, kLoadStreamPolicy));
+    };
+    if (kApart && !teaches)
+        fetch(0);
     if (is_padding(index, value, K)) {
         if (segs == 1)
             pad_distill(a.loss, a.stats, row_i);
         return;
     }
     const Scale sc(a.in.c);
-    if (tid < kWave) {
-        const bool twice = mark_listed(bits, ((k1 - k0) * W + 31) / 32, index, K, row.phase - k0 * W,
-                                       (k1 - k0) * W, a.in.vocab, lane);
-        if (segs == 1)
-            read_teacher(te, index, value, K, a.mode, row.p, a.in.vocab, sc, a.in.scale, twice, lane);
+    bool twice = false;
+    auto read = [&] {
+        read_teacher(te, index, value, K, a.mode, row.p, a.in.vocab, sc, a.in.scale, twice, lane);
+    };
+    if (teaches) {
+        twice = mark_listed(bits, ((k1 - k0) * W + 31) / 32, index, K, row.phase - k0 * W,
+                            (k1 - k0) * W, a.in.vocab, lane);
+        if (!kApart && segs == 1)
+            read();
     }
     __syncthreads();
     Sum q;
-    auto take = [&](const Chunk<T> &ch, int k) {
-        float x[W];
-        ch.widen(x);
-        const int at = (k - k0) * W;
-        const unsigned listed = bits[at >> 5] >> (at & 31) & ((1u << W) - 1);
-        if (listed) {
+    if (kApart && teaches) {
+        if (segs == 1)
+            read();
+    } else {
+        if (!kApart)
+            fetch(0);
+        for (int b = 0; b < n;) {
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                x[i] = listed >> i & 1 ? -kInf : x[i];
+            for (int u = 0; u < U; ++u) {
+                const int first = b + NS * u;
+                if (first >= n)
+                    break;
+                if (first + NS > n && first + tid >= n)
+                    ch[u].clear();
+                float x[W];
+                ch[u].widen(x);
+                const int at = (min(first + tid, n) + lo - k0) * W;
+                const unsigned listed = bits[at >> 5] >> (at & 31) & ((1u << W) - 1);
+                if (listed) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        x[i] = listed >> i & 1 ? -kInf : x[i];
+                }
+                q.add<W, false>(x, sc);
+            }
+            b += NS * U;
+            if (b < n)
+                fetch(b);
         }
-        q.add<W, false>(x, sc);
-    };
-    int k = lo + tid;
-    for (; k + NT * (U - 1) < hi; k += NT * U) {
-        Chunk<T> ch[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            ch[u].stream(row.chunk(k + NT * u));
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            take(ch[u], k + NT * u);
-    }
-    for (; k < hi; k += NT) {
-        Chunk<T> ch;
-        ch.stream(row.chunk(k));
-        take(ch, k);
     }
     const int e = tid < 2 * W ? row.edge(tid, k0, k1) : -1;
     if (e >= 0) {
