@@ -421,9 +421,10 @@ __global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_
 //
 // One workgroup per kNT U chunks of a row, U to a thread, so that neighbouring
 // workgroups sweep the memory in order.  Each wave adds up the record's
-// probabilities for itself; a workgroup that holds no listed token (U = 2 and a
-// vocabulary of 128256: 13 % of them at 64 listed) needs nothing more of the
-// record and no barrier.
+// probabilities for itself; a workgroup that holds no listed token needs nothing
+// more of the record and no barrier.  (The first of sixteen waves adding them up
+// for all, one chunk to a thread: 330 us for 2048 rows of 128256 bf16 and 64
+// listed, where this takes 185: the other waves wait for its reads and products.)
 template <typename T, int U>
 __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs)
 {
@@ -752,17 +753,24 @@ int launch_distill(const DistillArgs &a, int32_t segs, void *stream)
 int launch_distill_grad(const DistillGradArgs &a, void *stream)
 {
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    constexpr int U = 4;
     const bool bf = a.in.dtype == ZERO_BF16;
     const int chunks = bf ? chunks_per<uint16_t>(a.in.vocab, 1) : chunks_per<float>(a.in.vocab, 1);
-    const int segs = (chunks + kNT * U - 1) / (kNT * U);
-    return each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
-        const dim3 grid(n * (unsigned)segs), block(kNT);
-        if (bf)
-            hipLaunchKernelGGL((distill_grad_kernel<uint16_t, U>), grid, block, 0, st, a, r, segs);
-        else
-            hipLaunchKernelGGL((distill_grad_kernel<float, U>), grid, block, 0, st, a, r, segs);
-    });
+    auto launch = [&](auto u) {
+        constexpr int U = decltype(u)::value;
+        const int segs = (chunks + kNT * U - 1) / (kNT * U);
+        return each_launch(a.in.rows, segs, [&](int64_t r, unsigned n) {
+            const dim3 grid(n * (unsigned)segs), block(kNT);
+            if (bf)
+                hipLaunchKernelGGL((distill_grad_kernel<uint16_t, U>), grid, block, 0, st, a, r, segs);
+            else
+                hipLaunchKernelGGL((distill_grad_kernel<float, U>), grid, block, 0, st, a, r, segs);
+        });
+    };
+    // Fewer workgroups add up long records (2048 rows of 128256 bf16, U = 4 and 8:
+    // 185 and 194 us at 64 listed, one to a lane; 216 and 202 at 128; 289 and 230
+    // at 256).
+    return a.top_k <= kWave ? launch(std::integral_constant<int, 4>())
+                            : launch(std::integral_constant<int, 8>());
 }
 
 bool distill_row_held(const LossRows &in)
