@@ -566,7 +566,7 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
         }
         return r;
     };
-    auto read_record = [&](int64_t r, const Row<T> &row, int set) {
+    auto mark_record = [&](int64_t r, const Row<T> &row, int set) {
         const int32_t *index = a.top_index + r * K;
         const bool twice = mark_listed(bitmap[set], (row.chunks * W + 31) / 32, index, K, row.phase,
                                        row.chunks * W, a.in.vocab, lane);
@@ -578,8 +578,11 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
             if (id >= 0 && id < a.in.vocab && c >= row.full_lo && c < row.full_hi)
                 atomicOr(&dirty[set][(c - row.full_lo) % NS], 1u << (c - row.full_lo) / NS);
         }
-        read_teacher(teacher[set], index, a.top_value + r * K, K, a.mode, row.p, a.in.vocab, k,
-                     a.in.scale, twice, lane);
+        return twice;
+    };
+    auto read_record = [&](int64_t r, const Row<T> &row, int set, bool twice) {
+        read_teacher(teacher[set], a.top_index + r * K, a.top_value + r * K, K, a.mode, row.p, a.in.vocab,
+                     k, a.in.scale, twice, lane);
     };
     // What both halves need of a row once its sum is known (barrier, then this).
     auto outcome = [&](int64_t r, const Teacher &te, const Total &t, float &dl, bool &fill) {
@@ -596,14 +599,15 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
     if (!sums) {
         if (lane == 0)
             written = 0;
-        read_record(r, row_at(r), 0);
+        const bool twice = mark_record(r, row_at(r), 0);
         __syncthreads();
+        read_record(r, row_at(r), 0, twice);   // beside the first row's sums
         unsigned all = 0;
         for (int turn = 0;; turn ^= 1) {
             Teacher &te = teacher[turn];
             const int64_t rn = skip_padding(r + gridDim.x);
             if (rn < a.in.rows)
-                read_record(rn, row_at(rn), turn ^ 1);
+                read_record(rn, row_at(rn), turn ^ 1, mark_record(rn, row_at(rn), turn ^ 1));
             __syncthreads();
             const Total t = add_waves<false, NS / kWave>(tot[turn], k);
             float dl;
