@@ -28,16 +28,38 @@ constexpr int kGroup = 64;
 constexpr int kGroups = 2304;   // those of kLossMaxSegment elements, and some to spare
 static_assert(kGroups >= (int)(kLossMaxSegment / kGroup) + 2, "a segment's groups fit");
 
-// The maximum over N neighbouring lanes (8 or 16, aligned), in each of them.
-template <int N>
-__device__ __forceinline__ float group_max(float x)
+// Binary logarithm of the lanes whose chunks of W elements are a group: kGroup
+// elements, or fewer where that leaves less than two groups to an alternative,
+// which makes a low bound and many candidates (1500 rows of 15576 bf16, 200
+// alternatives: 120 us with groups of kGroup, 35 with smaller ones; 64 of 4000:
+// 40 and 12).
+template <int W>
+constexpr int kGroupLog = W == 4 ? 4 : 3;
+template <int W>
+__device__ __forceinline__ int group_lanes(int chunks, int K)
 {
-    static_assert(N == 8 || N == 16, "within a row of 16 lanes");
-    x = __builtin_fmaxf(x, from_lane<kLaneXor1>(x, x));
-    x = __builtin_fmaxf(x, from_lane<kLaneXor2>(x, x));
-    x = __builtin_fmaxf(x, from_lane<kMirror8>(x, x));
-    if constexpr (N == 16)
-        x = __builtin_fmaxf(x, from_lane<kMirror16>(x, x));
+    static_assert(W << kGroupLog<W> == kGroup && 4 * ZERO_MAX_TOP + 2 <= kGroups, "groups fit");
+    int lg = kGroupLog<W>;
+    while (lg > 0 && chunks >> lg < 2 * K)
+        --lg;
+    return lg;
+}
+// The maximum over 2^lg neighbouring lanes (aligned), in each of them.
+template <int W>
+__device__ __forceinline__ float group_max(float x, int lg)
+{
+    if (lg == kGroupLog<W>) {   // one branch in the loop over long rows
+        x = __builtin_fmaxf(x, from_lane<kLaneXor1>(x, x));
+        x = __builtin_fmaxf(x, from_lane<kLaneXor2>(x, x));
+        x = __builtin_fmaxf(x, from_lane<kMirror8>(x, x));
+        return W == 4 ? __builtin_fmaxf(x, from_lane<kMirror16>(x, x)) : x;
+    }
+    if (lg > 0)
+        x = __builtin_fmaxf(x, from_lane<kLaneXor1>(x, x));
+    if (lg > 1)
+        x = __builtin_fmaxf(x, from_lane<kLaneXor2>(x, x));
+    if (lg > 2)
+        x = __builtin_fmaxf(x, from_lane<kMirror8>(x, x));
     return x;
 }
 constexpr int kCands = 1024, kPad = 16;
@@ -267,22 +289,24 @@ __device__ __forceinline__ unsigned list_groups(Select &sh, int groups, int K)
 }
 
 // The K largest logits of chunks [k0, k1).  Group g of their whole chunks is
-// elements kGroup g .. + kGroup - 1; sh.gmax holds the upper 16 bits of its
-// largest logit's order.
+// chunks g 2^lg .. + 2^lg - 1; sh.gmax holds the upper 16 bits of its largest
+// logit's order.
 template <typename T, int NT, typename Put>
-__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int K, Put put)
+__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int lg, int K, Put put)
 {
-    constexpr int W = Row<T>::W, L = kGroup / W;
+    constexpr int W = Row<T>::W;
     const int tid = threadIdx.x;
     const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    const int groups = (max(hi - lo, 0) + L - 1) / L;
+    const int groups = (max(hi - lo, 0) + (1 << lg) - 1) >> lg;
     const int first = max(k0 * W - row.phase, 0), last = min(k1 * W - row.phase, row.vocab);
     const int n = max(last - first, 0);
-    const unsigned bound = groups <= NT ? list_groups<NT, 1>(sh, groups, K)
-                                        : list_groups<NT, (kGroups + NT - 1) / NT>(sh, groups, K);
+    constexpr int Q = (kGroups + NT - 1) / NT, Few = Q < 3 ? Q : 3;
+    const unsigned bound = groups <= NT         ? list_groups<NT, 1>(sh, groups, K)
+                           : groups <= Few * NT ? list_groups<NT, Few>(sh, groups, K)
+                                                : list_groups<NT, Q>(sh, groups, K);
     const float least = bound <= 0x7fu ? -kInf : ord32_value(bound << 16);
-    const int todo = (int)sh.listed * L;
-    auto chunk_of = [&](int j) { return lo + sh.list[j / L] * L + j % L; };
+    const int todo = (int)sh.listed << lg;
+    auto chunk_of = [&](int j) { return lo + (sh.list[j >> lg] << lg) + (j & ((1 << lg) - 1)); };
     auto look = [&](const Chunk<T> &ch, int k) {
         float x[W];
         ch.widen(x);
@@ -424,6 +448,7 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
     const Scale sc(a.in.c);
     Sum q;
     const int n = max(hi - lo, 0);   // whole chunks
+    const int lg = group_lanes<W>(n, a.top_k);
     const __amdgpu_buffer_rsrc_t in = window(row.chunk(lo), n);
     for (int b = 0; b < n; b += NT * U) {
         Chunk<T> ch[U];
@@ -447,9 +472,9 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
                 m = __builtin_fmaxf(m, x[i]);
             q.add_with_max<W, ENT>(x, m, sc);
             if constexpr (TOP) {
-                m = group_max<kGroup / W>(m);
-                if ((tid & (kGroup / W - 1)) == 0 && first + tid < n)
-                    sh.gmax[(first + tid) / (kGroup / W)] = (uint16_t)(ord32(m) >> 16);
+                m = group_max<W>(m, lg);
+                if ((tid & ((1 << lg) - 1)) == 0 && first + tid < n)
+                    sh.gmax[(first + tid) >> lg] = (uint16_t)(ord32(m) >> 16);
             }
         }
     }
@@ -469,12 +494,12 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
                 put_none(a, row_i, 0, t);
         } else if (segs == 1) {
             const float log2s = log2f(t.s);
-            select_top<T, NT>(sh, row, k0, k1, a.top_k,
+            select_top<T, NT>(sh, row, k0, k1, lg, a.top_k,
                               [&](int r, uint64_t key) { put_top(a, row_i, r, key, t, log2s); });
             put_none(a, row_i, elems, t);
         } else {
             uint64_t *out = a.keys + (row_i * segs + seg) * a.top_k;
-            select_top<T, NT>(sh, row, k0, k1, a.top_k,
+            select_top<T, NT>(sh, row, k0, k1, lg, a.top_k,
                               [&](int r, uint64_t key) { out[r] = key; });
             for (int i = elems + tid; i < a.top_k; i += NT)
                 out[i] = 0;   // below every logit's key
