@@ -75,15 +75,19 @@ __device__ __forceinline__ double log64(double x)
 // an entropy, below 16 nats for any vocabulary here.
 constexpr double kLeastRest = 0x1p-20;
 
-// True where a record is padding: no entry, and no NaN value.
+// True where a record is padding: no entry, and no NaN value (whole waves).  Most
+// records name a token first.
 __device__ __forceinline__ bool is_padding(const int32_t *index, const float *value, int K)
 {
-    for (int k = 0; k < K; ++k) {
-        const float v = ld_uniform(value + k);
-        if (ld_uniform(index + k) >= 0 || v != v)
-            return false;
+    if (ld_uniform(index) >= 0)
+        return false;
+    bool some = false;
+#pragma nounroll
+    for (int k = threadIdx.x & (kWave - 1); k < K; k += kWave) {
+        const float v = value[k];
+        some = some || index[k] >= 0 || v != v;
     }
-    return true;
+    return !__any(some);
 }
 
 // The teacher's total and the other tokens' probability from the sum over its
@@ -299,7 +303,8 @@ constexpr int kBitWords = (int)(kLossMaxSegment / 32) + 8;
 // from the whole sum would lose the rest's digits where little is left).  A wide
 // workgroup (few rows, each whole: latency counts) leaves the record to its last
 // wave, beside the others' sums, and has its first chunks on their way before it
-// looks at anything else.
+// looks at anything else: 3 x 50257 fp32 8.1 us; 2048 x 128256 bf16, 64 listed, 91 us,
+// 5.8 TB/s.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0, int segs, int cps)
 {
@@ -425,6 +430,7 @@ __global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_
 // more of the record and no barrier.  (The first of sixteen waves adding them up
 // for all, one chunk to a thread: 330 us for 2048 rows of 128256 bf16 and 64
 // listed, where this takes 185: the other waves wait for its reads and products.)
+// 2048 x 128256 bf16, 64 listed: 181 us, 5.8 TB/s.
 template <typename T, int U>
 __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs)
 {
@@ -529,13 +535,15 @@ __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, in
     }
 }
 
-constexpr int kHeld = 17;   // chunks a thread holds
+constexpr int kHeld = 17;   // chunks a thread holds: 960 threads hold 128256 bf16
 
 // Forward and backward of whole rows, at most kHeld NS chunks each, by NS threads
 // and one more wave, which reads the next row's record while the others sum the
 // row, and writes the listed tokens' gradients while they sum the next one:
 // what takes its time there are a few dependent reads, which would hold up a
 // wave that also has its share of the row.  Records and bitmaps have two places.
+// 4096 x 128256 bf16, 64 listed: 400 us, 5.3 TB/s (497 us with the record in the
+// hands of a wave that also sums); 511 x 50257 26 us.
 template <typename T, int NS, bool SAME>
 __global__ __launch_bounds__(NS + kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_row_kernel(DistillArgs a, DistillGradArgs b)

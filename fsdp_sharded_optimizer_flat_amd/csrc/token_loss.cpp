@@ -135,11 +135,14 @@ int32_t loss_segments(int64_t rows, int64_t vocab, int32_t top_k)
 {
     // One workgroup per row keeps the whole chip busy from about 1024 rows on
     // (4 workgroups on each of 256 compute units).  Fewer rows are cut so that
-    // there are about that many workgroups, in segments of at least 2048
-    // elements and 128 per wanted alternative (two groups of the selection), with at most 4096 alternatives
-    // for the joining workgroup -- unless a workgroup of 1024 threads sums a row
-    // sooner than a second launch joins its segments.  A function of the sizes
-    // alone, so the result does not depend on the device's state.
+    // there are about that many workgroups, in segments of at least 2048 elements
+    // and 128 per wanted alternative, with at most 4096 alternatives for the joining
+    // workgroup -- unless a workgroup of 1024 threads sums a row sooner than a
+    // second launch joins its segments (whole and cut, bf16: 64 rows of 20000 with
+    // five alternatives 8.6 and 10.7 us, of 65536 12.8 and 12.6; 256 of 50304 with
+    // twenty 12.4 and 16.2; 1 of 50304 without any 6.4 and 5.2; distillation, 64 of
+    // 50304, 64 listed, 8.3 and 14.3).  A function of the sizes alone, so the
+    // result does not depend on the device's state.
     if (rows <= kLossWideRows && vocab <= kLossWideVocab)
         return 1;
     const int64_t need = (vocab + kLossMaxSegment - 1) / kLossMaxSegment;

@@ -6,10 +6,8 @@
 
 namespace zero {
 
-// Threads of a token-loss workgroup; also the most listed tokens per row (one
-// per thread).
+// Threads of a token-loss workgroup, unless it holds a row or sums one of few.
 constexpr int kLossBlock = 256;
-static_assert(ZERO_MAX_TOP <= kLossBlock, "one listed token per thread");
 
 // Most elements one workgroup reduces: its bitmap of listed tokens is 16 KiB.
 constexpr int64_t kLossMaxSegment = int64_t(1) << 17;

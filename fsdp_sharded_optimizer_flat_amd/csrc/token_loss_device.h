@@ -15,9 +15,15 @@
 // logits, or parts of rows masked with the type's lowest value, where c m could
 // even leave binary32's range) t = (l - m) c is taken instead.
 //
-// Bound: HBM.  A forward pass reads each logit once; per bf16 element that is 2
-// bytes against 8 to 11 vector issue slots (widen 1, max 1/2, fma 1, exp 4,
-// add 1; entropy: clamp 1, fma 1).
+// Bound: HBM.  A forward pass reads each logit once, a backward pass reads and
+// writes, a fused call too (it holds the row in registers).  A bf16 element is 2
+// bytes against 6 to 9 vector issue slots (widen 1, max 1, fma 1, exp 2, add 1;
+// entropy: clamp 1, product 1, add 1), which a compute unit gets through in 0.7 of
+// the time its share of the bandwidth takes for the bytes: a sweep over many rows
+// hides them, a single row does not (1 x 50304: 3 of 10.7 us).
+// Measured on one MI355X (a sweep that reads and writes reaches 6.7 TB/s there):
+// forward with entropy, 4096 x 128256 bf16, 164 us, 6.4 TB/s; backward, 2048 x
+// 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 748 us, 5.6 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -96,7 +102,7 @@ __device__ __forceinline__ u32x4 pack_chunk(const float (&g)[W])
 // Stores 16 bytes at any element's address (gfx950 takes such stores), for
 // gradients whose rows sit at another 16-byte phase than their logits: reading
 // the logits unaligned instead measured slower (777 x 50257 fp32, loss and
-// gradient: 72 us, and 80 to 93 us with unaligned loads).
+// gradient: 70 us, and 80 to 93 us with unaligned loads).
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <typename T>
 __device__ __forceinline__ void store_any(u32x4 v, T *p)
@@ -627,8 +633,9 @@ inline bool wide_rows(const LossRows &in) { return in.rows <= kLossWideRows && i
 
 // Workgroups of a launch that goes through rows: as many as are resident at once
 // (128 registers a thread: 16 waves on a compute unit), or one per row where
-// each would get four rows or fewer (1024 x 50304 bf16, loss and gradient: 39 us,
-// and 44 us with two rows to a workgroup; 8192 x 128256: 840 and 772 us).
+// each would get four rows or fewer (1024 x 50304 bf16, loss and gradient, when
+// this was chosen: 39 us, and 44 us with two rows to a workgroup; 8192 x 128256,
+// 32 rows to a workgroup: 772 us, and 840 us with a workgroup per row).
 inline unsigned held_grid(int64_t rows, int threads)
 {
     const int64_t most = (int64_t)device_cu_count() * (1024 / threads);

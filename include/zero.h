@@ -583,9 +583,9 @@ zero_status zero_clip_coef_ranks_async(const double *rank_sums_dev, int32_t n_ra
  *
  * Rows that have no distribution, or no target:
  *   - a negative token, or a teacher's record of negative indices only (and no
- *     NaN value), marks a padding row: it is not read, its outputs and its
- *     gradient are zero, and its top alternatives index -1, log probability
- *     -inf;
+ *     NaN value), marks a padding row: whatever its logits hold, its outputs
+ *     and its gradient are zero, and its top alternatives index -1, log
+ *     probability -inf;
  *   - upstream weights of zero give a zero gradient, whatever the row holds;
  *   - a row whose logits are all -inf: logprob -inf, entropy 0, a loss of
  *     +inf, no alternatives, gradient zero;
