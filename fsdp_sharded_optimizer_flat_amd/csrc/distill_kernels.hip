@@ -543,7 +543,7 @@ constexpr int kHeld = 17;   // chunks a thread holds: 960 threads hold 128256 bf
 // what takes its time there are a few dependent reads, which would hold up a
 // wave that also has its share of the row.  Records and bitmaps have two places.
 // 4096 x 128256 bf16, 64 listed: 400 us, 5.3 TB/s (497 us with the record in the
-// hands of a wave that also sums); 511 x 50257 26 us.
+// hands of a wave that also sums); 511 x 50257 30 us.
 template <typename T, int NS, bool SAME>
 __global__ __launch_bounds__(NS + kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_row_kernel(DistillArgs a, DistillGradArgs b)
