@@ -260,8 +260,14 @@ struct Sum {
         for (int i = 0; i < N; ++i) {
             const float t = BIG ? rel(x[i], m, r, k) : __builtin_fmaf(x[i], k.c, -r);
             e[i] = pow2(t);
-            if constexpr (ENT)
-                b[i] = e[i] * __builtin_fmaxf(t, kTiny);
+            if constexpr (ENT) {
+                const float u = __builtin_fmaxf(t, kTiny);
+                b[i] = 0.0f;
+                if (i & 1)
+                    b[i - 1] = __builtin_fmaf(e[i], u, b[i - 1]);
+                else
+                    b[i] = e[i] * u;
+            }
         }
 #pragma unroll
         for (int w = 1; w < N; w *= 2)
@@ -269,7 +275,8 @@ struct Sum {
             for (int i = 0; i + w < N; i += 2 * w) {
                 e[i] += e[i + w];
                 if constexpr (ENT)
-                    b[i] += b[i + w];
+                    if (w > 1)
+                        b[i] += b[i + w];
             }
         s += e[0];
         if constexpr (ENT)
