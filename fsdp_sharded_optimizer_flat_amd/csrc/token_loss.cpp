@@ -186,8 +186,8 @@ extern "C" zero_status zero_logprob(const void *logits, int32_t dtype, int64_t r
     LogprobArgs a{};
     if (zero_status s = check_rows(logits, dtype, rows, vocab, row_stride, scale, &a.in))
         return s;
-    if (top_k < 0 || (logprob && !tokens) || (top_k > 0) != (top_index != nullptr) ||
-        (top_k > 0) != (top_logprob != nullptr))
+    if (top_k < 0 || (rows > 0 && ((logprob && !tokens) || (top_k > 0) != (top_index != nullptr) ||
+                                   (top_k > 0) != (top_logprob != nullptr))))
         return ZERO_EINVAL;
     if (top_k > ZERO_MAX_TOP)
         return ZERO_ERANGE;
@@ -228,8 +228,9 @@ extern "C" zero_status zero_logprob_grad(const void *logits, int32_t dtype, int6
     LogprobGradArgs a{};
     if (zero_status s = check_rows(logits, dtype, rows, vocab, row_stride, scale, &a.in))
         return s;
-    if (d_row_stride < vocab || (!d_logprob && !d_entropy) || (d_logprob && !tokens) ||
-        (d_entropy && !entropy) || (rows > 0 && (!stats || !d_logits)))
+    if (d_row_stride < vocab ||
+        (rows > 0 && ((!d_logprob && !d_entropy) || (d_logprob && !tokens) ||
+                      (d_entropy && !entropy) || !stats || !d_logits)))
         return ZERO_EINVAL;
     if (d_row_stride > (int64_t(1) << 61) / 4 / (rows > 0 ? rows : 1))
         return ZERO_ERANGE;
@@ -262,8 +263,8 @@ extern "C" zero_status zero_logprob_fused(const void *logits, int32_t dtype, int
     LogprobArgs a{};
     if (zero_status s = check_rows(logits, dtype, rows, vocab, row_stride, scale, &a.in))
         return s;
-    if (d_row_stride < vocab || (!d_logprob && !d_entropy) || ((d_logprob || logprob) && !tokens) ||
-        (rows > 0 && !d_logits))
+    if (d_row_stride < vocab ||
+        (rows > 0 && ((!d_logprob && !d_entropy) || ((d_logprob || logprob) && !tokens) || !d_logits)))
         return ZERO_EINVAL;
     if (d_row_stride > (int64_t(1) << 61) / 4 / (rows > 0 ? rows : 1))
         return ZERO_ERANGE;

@@ -292,3 +292,30 @@ def test_columns_of_a_wider_matrix_and_reversed_use():
     assert torch.equal(d.view(torch.int16), x.contiguous().view(torch.int16))
     assert torch.equal(wide[:, :vocab], keep[:, :vocab]) and torch.equal(wide[:, 2 * vocab:], keep[:, 2 * vocab:])
     assert bool(torch.isfinite(ref_logp(y, 1.0)).all())
+
+
+def test_no_rows():
+    """Empty batches through the binding: nothing is written, nothing refused."""
+    x = torch.empty(0, 500, dtype=torch.bfloat16, device=DEV)
+    f, st, st4 = (torch.empty(0, *s, device=DEV) for s in ((), (2,), (4,)))
+    tok = torch.empty(0, dtype=torch.int64, device=DEV)
+    i, v = torch.empty(0, 5, dtype=torch.int32, device=DEV), torch.empty(0, 5, device=DEV)
+    assert z.zero_loss_workspace_bytes(0, 500, 5) == 0
+    z.zero_logprob(x, tok, logprob=f, entropy=f, stats=st, top_index=i, top_logprob=v)
+    z.zero_logprob_grad(x, tok, st, x, d_logprob=f, d_entropy=f, entropy=f)
+    z.zero_logprob_fused(x, tok, x.clone(), d_logprob=f, logprob=f)
+    for mode in MODES.values():
+        z.zero_distill(x, i, v, mode, loss=f, stats=st4)
+        z.zero_distill_grad(x, i, v, mode, st4, f, x)
+        z.zero_distill_fused(x, i, v, mode, f, x.clone(), loss=f)
+    torch.cuda.synchronize()
+
+
+def test_rows_of_one_tensor_are_refused():
+    """Rows that share memory (an expanded tensor) and columns of a transposed one."""
+    x = torch.zeros(1, 500, dtype=torch.bfloat16, device=DEV).expand(4, 500)
+    lp, tok = torch.empty(4, device=DEV), torch.zeros(4, dtype=torch.int64, device=DEV)
+    with pytest.raises(z.ZeroError):
+        z.zero_logprob(x, tok, logprob=lp)
+    with pytest.raises(ValueError):
+        z.zero_logprob(torch.zeros(500, 4, device=DEV).t(), tok, logprob=lp)

@@ -63,6 +63,13 @@ def test_refused_sizes(entry):
 def test_no_rows_is_no_work(entry):
     assert call(entry, rows=0) == z.ZERO_OK
     assert call(entry, rows=0, logits=None) == z.ZERO_OK
+    # tensors of no rows have no address
+    nothing = dict(logits=None, tokens=None, logprob=None, entropy=None, stats=None, top_index=None,
+                   top_logprob=None, top_value=None, d_logprob=None, d_entropy=None, d_logits=None,
+                   loss=None, d_loss=None, workspace=None, wb=0)
+    assert set(nothing) - {"wb"} <= set(A)
+    assert call(entry, rows=0, **nothing) == z.ZERO_OK
+    assert call(entry, rows=0, **{**nothing, "vocab": 0}) == EINVAL
 
 
 def test_refused_pointers():
