@@ -430,7 +430,7 @@ __global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_
 // more of the record and no barrier.  (The first of sixteen waves adding them up
 // for all, one chunk to a thread: 330 us for 2048 rows of 128256 bf16 and 64
 // listed, where this takes 185: the other waves wait for its reads and products.)
-// 2048 x 128256 bf16, 64 listed: 181 us, 5.8 TB/s.
+// 2048 x 128256 bf16, 64 listed: 179 us, 5.9 TB/s.
 template <typename T, int U>
 __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs)
 {
@@ -542,8 +542,8 @@ constexpr int kHeld = 17;   // chunks a thread holds: 960 threads hold 128256 bf
 // row, and writes the listed tokens' gradients while they sum the next one:
 // what takes its time there are a few dependent reads, which would hold up a
 // wave that also has its share of the row.  Records and bitmaps have two places.
-// 4096 x 128256 bf16, 64 listed: 400 us, 5.3 TB/s (497 us with the record in the
-// hands of a wave that also sums); 511 x 50257 30 us.
+// 4096 x 128256 bf16, 64 listed: 398 us, 5.3 TB/s (497 us with the record in the
+// hands of a wave that also sums); 511 x 50257 28 us.
 template <typename T, int NS, bool SAME>
 __global__ __launch_bounds__(NS + kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_row_kernel(DistillArgs a, DistillGradArgs b)

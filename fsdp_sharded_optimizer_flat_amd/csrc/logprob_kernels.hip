@@ -96,7 +96,7 @@ struct Select {
     // the K largest of many candidates, once the groups are done with
     __device__ __forceinline__ uint64_t *best() { return reinterpret_cast<uint64_t *>(gmax); }
 };
-static_assert(ZERO_MAX_TOP * sizeof(uint64_t) <= sizeof(Select::gmax), "room for the best");
+static_assert((ZERO_MAX_TOP + kPad) * sizeof(uint64_t) <= sizeof(Select::gmax), "room for the best");
 
 // One radix pass's choice: the bin of sh.hist (256 bins) that holds the want-th
 // largest entry, and how many lie above it.  Thread b < 256 owns bin b.
@@ -426,8 +426,8 @@ __device__ __forceinline__ void put_none(const LogprobArgs &a, int64_t row, int 
 
 // One workgroup per segment of a row (segs of them): the whole result where
 // segs is 1, else its LossPart and its top keys.  One pass, U chunks to a thread on
-// their way at once, 8 waves on a SIMD: 4096 x 128256 bf16 with entropy 164 us,
-// 6.4 TB/s; 2048 x 128256 with the 64 largest of each row 97 us (86 us without: the
+// their way at once, 8 waves on a SIMD: 4096 x 128256 bf16 with entropy 162 us,
+// 6.5 TB/s; 2048 x 128256 with the 64 largest of each row 97 us (86 us without: the
 // selection is a chain of barriers that other workgroups fill only in part); 64 x
 // 128256 with twenty, cut for 1024 workgroups, 18 us with the joining launch,
 // both latency: loads, four barriers and a second read of the chosen groups; 1 x
@@ -632,8 +632,8 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
 constexpr int kHeld = 16;   // chunks a thread holds: half of its 128 registers
 
 // Forward and backward of whole rows, at most kHeld NT chunks each, read once: 8192
-// x 128256 bf16 748 us, 5.6 TB/s (in two launches, each logit read twice, 1175 us);
-// 1024 x 50304 43 us; 777 x 50257 fp32 at another phase than its gradient 70 us.
+// x 128256 bf16 740 us, 5.7 TB/s (in two launches, each logit read twice, 1175 us);
+// 1024 x 50304 42 us; 777 x 50257 fp32 at another phase than its gradient 69 us.
 // Rows of 256 KB read and written in bursts reach 5.9 to 6.0 TB/s as a plain copy; a
 // workgroup's exponentials, twice over the row, fill most of what is left between
 // its bursts.  1024 threads of 64 registers, half the row to each, spill: 64 us for

@@ -23,8 +23,8 @@
 // TB/s), so no term may be added lightly.  A single row waits for its one compute
 // unit instead (1 x 50304: 5 of 10.7 us).
 // Measured on one MI355X (a sweep that reads and writes reaches 6.7 TB/s there):
-// forward with entropy, 4096 x 128256 bf16, 164 us, 6.4 TB/s; backward, 2048 x
-// 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 748 us, 5.6 TB/s.
+// forward with entropy, 4096 x 128256 bf16, 162 us, 6.5 TB/s; backward, 2048 x
+// 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 740 us, 5.7 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -139,16 +139,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const T *p, int chunks)
     return __builtin_amdgcn_make_buffer_rsrc(scalar(p), 0, __builtin_amdgcn_readfirstlane(chunks) * 16,
                                              kRawBufferWord3);
 }
-// Stores chunk `tid` of a window of `chunks` chunks from p on, written through
-// to memory.  Each store has a window of its own, no offset in a scalar register:
-// MI355X has stored what the next instruction wrote to the data registers of a
-// 16-byte buffer store with such an offset (the compiler leaves no wait between
-// the two then).
+// Stores chunk `tid` of a window of `chunks` chunks from p on, nontemporal.  Not
+// written through to memory (sc1) as well: rows of odd sizes share cache lines between
+// waves, and such halves then go out one by one (loss and gradient of 4096 x 128255
+// bf16 457 us so, 422 without; 777 x 50257 fp32 80 and 70; 4096 x 128256, whole lines,
+// 380 and 374; only the backward sweep over whole lines gains, 319 to 326).  Without
+// the nontemporal hint outputs beyond the memory-side cache lose (4096 x 128256:
+// 413).  Each store has a window of its own, no offset in a scalar register: MI355X
+// has stored what the next instruction wrote to the data registers of a 16-byte
+// buffer store with such an offset (the compiler leaves no wait between the two
+// then).
+constexpr int kLossStorePolicy = 2;   // nt
 template <typename T>
 __device__ __forceinline__ void store_chunks(u32x4 v, T *p, int chunks)
 {
     __builtin_amdgcn_raw_buffer_store_b128(v, window(p, chunks), (int)threadIdx.x * 16, 0,
-                                           kSpanStorePolicy);
+                                           kLossStorePolicy);
 }
 
 // A row cut into chunks that start at 16-byte boundaries: chunk k holds
