@@ -543,14 +543,14 @@ constexpr int kHeld = 17;   // chunks a thread holds: 960 threads hold 128256 bf
 // what takes its time there are a few dependent reads, which would hold up a
 // wave that also has its share of the row.  Records and bitmaps have two places.
 // 4096 x 128256 bf16, 64 listed: 398 us, 5.3 TB/s (497 us with the record in the
-// hands of a wave that also sums); 511 x 50257 28 us.
+// hands of a wave that also sums); 511 x 50257 27 us.
 template <typename T, int NS, bool SAME>
 __global__ __launch_bounds__(NS + kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_row_kernel(DistillArgs a, DistillGradArgs b)
 {
     typedef HeldRow<T, NS, kHeld, SAME> Held;
     constexpr int W = Row<T>::W, N = Held::G * W;
-    constexpr int kWords = ((NS * kHeld * W + 2 * W + 31) / 32 + 3) / 4 * 4;
+    constexpr int kWords = (((NS * kHeld + 1) * W + 31) / 32 + 3) / 4 * 4;
     __shared__ Total tot[2][NS / kWave];
     __shared__ Teacher teacher[2];
     __shared__ alignas(16) unsigned bitmap[2][kWords];   // the row's listed tokens
@@ -584,7 +584,7 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
         for (int i = lane; i < K; i += kWave) {
             const int id = index[i], c = (id + row.phase) / W;
             if (id >= 0 && id < a.in.vocab && c >= row.full_lo && c < row.full_hi)
-                atomicOr(&dirty[set][(c - row.full_lo) % NS], 1u << (c - row.full_lo) / NS);
+                atomicOr(&dirty[set][c % NS], 1u << c / NS);
         }
         return twice;
     };
@@ -654,7 +654,9 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
 #pragma unroll
             for (int j = 0; j < N / W; ++j)
                 if (mine >> (i + j) & 1) {
-                    const int at = (held.row.full_lo + tid + NS * (i + j)) * W;
+                    int t = tid;
+                    asm volatile("" : "+v"(t));   // or the places of all chunks would be kept over all rows
+                    const int at = (t + NS * (i + j)) * W;
                     const unsigned listed = bits[at >> 5] >> (at & 31);
 #pragma unroll
                     for (int w = 0; w < W; ++w)

@@ -617,7 +617,7 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
     const float u = -a.in.scale * (dl + dh * (h - off * kLn2)) * inv;
     const float v = -a.in.scale * dh * kLn2 * inv;
     // the given token's thread; in place: it reads the logit before it writes
-    const bool mine = a.d_logprob && owner_of<T, kNT>(row, (int)tok, k0, kNT) == (int)threadIdx.x;
+    const bool mine = a.d_logprob && owner_of<T, kNT>(row, (int)tok, k0, kNT, seg.lo) == (int)threadIdx.x;
     const float l = mine ? row.at((int)tok) : 0.0f;
     auto grad = [&](float t) { return pow2(t) * (ENT ? __builtin_fmaf(v, __builtin_fmaxf(t, kTiny), u) : u); };
     if (__builtin_fabsf(m) > k.big)
@@ -706,7 +706,7 @@ void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)
         }
         held.map(out, !fill && !big, next, [&](float x) { return grad(__builtin_fmaf(x, k.c, -ref)); });
         // the given token's, after its thread's own store of the element
-        const int owner = owner_of<T, NT>(held.row, (int)tok, 0, held.row.chunks);
+        const int owner = owner_of<T, NT>(held.row, (int)tok, 0, held.row.chunks, 0);
         if (b.d_logprob && !fill && (int)threadIdx.x == (big ? 0 : owner))
             store_one(out + tok, grad(rel(l, m, ref, k)) + a.in.scale * dl);
         held.take(next);

@@ -50,6 +50,8 @@ constexpr float kTiny = -1000.0f;       // t of a probability that is zero, for 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
+constexpr int kLine = 128;   // bytes of a cache line
+
 // 16 bytes of a row: W elements.
 template <typename T>
 struct Chunk;
@@ -139,27 +141,30 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const T *p, int chunks)
     return __builtin_amdgcn_make_buffer_rsrc(scalar(p), 0, __builtin_amdgcn_readfirstlane(chunks) * 16,
                                              kRawBufferWord3);
 }
-// Stores chunk `tid` of a window of `chunks` chunks from p on, nontemporal.  Not
-// written through to memory (sc1) as well: rows of odd sizes share cache lines between
-// waves, and such halves then go out one by one (loss and gradient of 4096 x 128255
-// bf16 457 us so, 422 without; 777 x 50257 fp32 80 and 70; 4096 x 128256, whole lines,
-// 380 and 374; only the backward sweep over whole lines gains, 319 to 326).  Without
-// the nontemporal hint outputs beyond the memory-side cache lose (4096 x 128256:
-// 413).  Each store has a window of its own, no offset in a scalar register: MI355X
-// has stored what the next instruction wrote to the data registers of a 16-byte
-// buffer store with such an offset (the compiler leaves no wait between the two
-// then).
+// Stores chunk `tid` - skip of a window of `chunks` chunks from p on, nontemporal (the
+// threads below skip store nothing: their offset wraps past the window).  Not written
+// through to memory (sc1) as well: where waves share a cache line its halves then go
+// out one by one (loss and gradient of 4096 x 128256 bf16, whole lines, 380 us so and
+// 374 without; with waves that began anywhere in a line, 4096 x 128255, 457 and 422).
+// Without the nontemporal hint outputs beyond the memory-side cache lose (4096 x
+// 128256: 413).  Each store has a window of its own, no offset in a scalar register:
+// MI355X has stored what the next instruction wrote to the data registers of a
+// 16-byte buffer store with such an offset (the compiler leaves no wait between the
+// two then).
 constexpr int kLossStorePolicy = 2;   // nt
 template <typename T>
-__device__ __forceinline__ void store_chunks(u32x4 v, T *p, int chunks)
+__device__ __forceinline__ void store_chunks(u32x4 v, T *p, int chunks, int skip = 0)
 {
-    __builtin_amdgcn_raw_buffer_store_b128(v, window(p, chunks), (int)threadIdx.x * 16, 0,
+    __builtin_amdgcn_raw_buffer_store_b128(v, window(p, chunks), ((int)threadIdx.x - skip) * 16, 0,
                                            kLossStorePolicy);
 }
 
-// A row cut into chunks that start at 16-byte boundaries: chunk k holds
-// elements k W - phase .. + W - 1, whole for full_lo <= k < full_hi; the first
-// and last may stick out of the row and are read element by element.
+// A row cut into 16-byte chunks, counted from the cache line (128 bytes) it starts
+// in, so that waves that take 64 chunks of a row at a time read and write whole
+// lines: chunk k holds elements k W - phase .. + W - 1, whole for full_lo <= k <
+// full_hi; the one before and the one after may hold a few elements of the row and
+// are read element by element.  (Counted from the 16 bytes it starts in: loss and
+// gradient of 4096 x 128255 bf16 422 us, and 378 so; 777 x 50257 fp32 70 and 64.)
 template <typename T>
 struct Row {
     static constexpr int W = Chunk<T>::W;
@@ -168,9 +173,9 @@ struct Row {
     __device__ __forceinline__ Row() : p(nullptr), vocab(0), phase(0), chunks(0), full_lo(0), full_hi(0) {}
     __device__ __forceinline__ Row(const T *p_, int vocab_) : p(p_), vocab(vocab_)
     {
-        phase = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+        phase = (int)((reinterpret_cast<uintptr_t>(p) & (kLine - 1)) / sizeof(T));
         chunks = (vocab + phase + W - 1) / W;
-        full_lo = phase ? 1 : 0;
+        full_lo = (phase + W - 1) / W;
         full_hi = max(full_lo, (vocab + phase) / W);
     }
     __device__ __forceinline__ const T *chunk(int k) const { return p + ((int64_t)k * W - phase); }
@@ -179,9 +184,9 @@ struct Row {
     // chunks [k0, k1), or -1.
     __device__ __forceinline__ int edge(int s, int k0, int k1) const
     {
-        const int k = s < W ? 0 : full_hi;
+        const int k = s < W ? full_lo - 1 : full_hi;
         const int e = k * W - phase + (s & (W - 1));
-        const bool partial = s < W ? full_lo == 1 : full_hi < chunks;
+        const bool partial = s < W ? (phase & (W - 1)) != 0 : full_hi < chunks;
         return partial && k >= k0 && k < k1 && e >= 0 && e < vocab ? e : -1;
     }
 };
@@ -437,14 +442,14 @@ __device__ __forceinline__ u32x4 map_chunk(const Chunk<T> &c, F f)
 }
 
 // The thread that holds element x of chunks [k0, k0 + n) of a row gone through NT
-// at a time, or -1.
+// at a time from chunk `base` on, or -1.
 template <typename T, int NT>
-__device__ __forceinline__ int owner_of(const Row<T> &row, int x, int k0, int n)
+__device__ __forceinline__ int owner_of(const Row<T> &row, int x, int k0, int n, int base)
 {
     constexpr int W = Row<T>::W;
     const int at = x + row.phase, k = at / W;
-    return k < k0 || k >= k0 + n ? -1 : k < row.full_lo ? at
-           : k < row.full_hi     ? (k - max(k0, row.full_lo)) % NT : W + (at & (W - 1));
+    return k < k0 || k >= k0 + n ? -1 : k < row.full_lo ? at & (W - 1)
+           : k < row.full_hi     ? (k - base) % NT : W + (at & (W - 1));
 }
 
 // Chunks [k0, k0 + NT U) of a row of logits, U to a thread: read when it is made,
@@ -528,15 +533,14 @@ struct HeldRow {
     static constexpr int P = parked(NT), P0 = H - P;
     u32x4 *park;  // P NT chunks of LDS
     Row<T> row;
-    int n;        // whole chunks
-    Chunk<T> ch[H];
+    Chunk<T> ch[H];   // chunk NT i + tid of the row
+
     float edge;   // this thread's element of the row's partial first or last chunk
     int e;        // and its index, or -1
 
     __device__ __forceinline__ void take(const Row<T> &next)
     {
         row = next;
-        n = next.full_hi - next.full_lo;
         e = (int)threadIdx.x < 2 * W ? next.edge(threadIdx.x, 0, next.chunks) : -1;
         edge = e >= 0 ? next.at(e) : -kInf;
     }
@@ -546,11 +550,16 @@ struct HeldRow {
         const int m = next.full_hi - next.full_lo;
         const T *first = scalar(next.chunk(next.full_lo));
         const __amdgpu_buffer_rsrc_t rs = window(first, m);
+        // threads below full_lo have no first chunk: their offset wraps past the window
+        const int at = ((int)threadIdx.x - next.full_lo) * 16;
+        int later = at + NT * 16;
+        asm volatile("" : "+v"(later));   // in a register: the wrapped sum, not a wrapped offset plus an immediate
 #pragma unroll
         for (int i = 0; i < H; ++i)
             ch[i].r = __builtin_bit_cast(decltype(ch[i].r),
                                          __builtin_amdgcn_raw_buffer_load_b128(
-                                             rs, (int)threadIdx.x * 16, NT * 16 * i, kLoadStreamPolicy));
+                                             rs, i ? later : at, i ? NT * 16 * (i - 1) : 0,
+                                             kLoadStreamPolicy));
     }
     // Visits the groups of G chunks that hold anything: f(first chunk, values).
     // Values past the row's whole chunks are -inf.
@@ -559,14 +568,15 @@ struct HeldRow {
     {
 #pragma unroll
         for (int i = 0; i < H; i += G) {
-            if (NT * i < n) {
+            if (NT * i < row.full_hi) {
                 float x[W * G];
                 u32x4 raw[G];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    if (NT * (i + j + 1) > n) {   // at most one chunk of the row: kept a branch
-                        asm volatile("");
-                        if (NT * (i + j) + (int)threadIdx.x >= n)
+                    if (i + j == 0 || NT * (i + j + 1) > row.full_hi) {   // kept a branch
+                        int t = threadIdx.x;
+                        asm volatile("" : "+v"(t));   // or the sums below would be kept over all rows
+                        if (t < row.full_lo - NT * (i + j) || t >= row.full_hi - NT * (i + j))
                             ch[i + j].clear();
                     }
                     raw[j] = __builtin_bit_cast(u32x4, ch[i + j].r);
@@ -591,8 +601,8 @@ struct HeldRow {
     template <typename F>
     __device__ __forceinline__ void map(T *out, bool write, const Row<T> &next, F f)
     {
-        T *first = scalar(out + (row.full_lo * W - row.phase));
-        const int m = write ? n : 0;
+        T *first = scalar(out - row.phase);   // chunk 0's
+        const int hi = write ? row.full_hi : 0;
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             Chunk<T> c = ch[i];
@@ -601,10 +611,11 @@ struct HeldRow {
             else   // opaque, or the widened logits of the sums would be kept from there
                 asm volatile("" : "+v"(c.r));
             if constexpr (SAME) {
-                if (NT * i < m)
-                    store_chunks(map_chunk(c, f), first + NT * W * i, m - NT * i);
+                const int skip = i ? 0 : row.full_lo;
+                if (NT * i < hi)
+                    store_chunks(map_chunk(c, f), first + W * (NT * i + skip), hi - NT * i - skip, skip);
             } else {
-                if ((int)threadIdx.x < m - NT * i)
+                if ((int)threadIdx.x < hi - NT * i && (i || (int)threadIdx.x >= row.full_lo))
                     store_any(map_chunk(c, f), first + NT * W * i + threadIdx.x * (unsigned)W);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -631,13 +642,13 @@ inline int each_launch(int64_t rows, int per_row, F f, int threads = kNT)
     return hipSuccess;
 }
 
-// Chunks per workgroup when a row of `vocab` elements at any 16-byte phase is
-// cut for `segs` workgroups.
+// Chunks per workgroup when a row of `vocab` elements at any place in its first
+// cache line is cut for `segs` workgroups.
 template <typename T>
 int chunks_per(int vocab, int segs)
 {
-    constexpr int W = 16 / (int)sizeof(T);
-    const int most = (vocab + 2 * (W - 1)) / W;
+    constexpr int W = 16 / (int)sizeof(T), phase = kLine / (int)sizeof(T) - 1;
+    const int most = (vocab + phase + W - 1) / W;
     return (most + segs - 1) / segs;
 }
 
