@@ -320,17 +320,14 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0
     const T *p = static_cast<const T *>(a.in.logits) + row_i * a.in.stride;
     const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
-    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    const int n = max(hi - lo, 0);   // whole chunks
-    const __amdgpu_buffer_rsrc_t in = window(row.chunk(lo), n);
+    const Sweep<T> sweep(row, k0, k1);
+    const int n = sweep.n;
     const bool teaches = tid / kWave == (kApart ? NS / kWave : 0);
     Chunk<T> ch[U];
-    auto fetch = [&](int b) {   // chunks past the segment are not read
+    auto fetch = [&](int b) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            ch[u].r = __builtin_bit_cast(decltype(ch[u].r),
-                                         __builtin_amdgcn_raw_buffer_load_b128(
-                                             in, tid * 16, (b + NS * u) * 16, kLoadStreamPolicy));
+            ch[u] = sweep.read(b + NS * u);
     };
     if (kApart && !teaches)
         fetch(0);
@@ -364,11 +361,10 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0
                 const int first = b + NS * u;
                 if (first >= n)
                     break;
-                if (first + NS > n && first + tid >= n)
-                    ch[u].clear();
+                sweep.trim(ch[u], first, NS);
                 float x[W];
                 ch[u].widen(x);
-                const int at = (min(first + tid, n) + lo - k0) * W;
+                const int at = (min(max(first + tid, sweep.skip), n) + sweep.from - k0) * W;
                 const unsigned listed = bits[at >> 5] >> (at & 31) & ((1u << W) - 1);
                 if (listed) {
 #pragma unroll

@@ -288,16 +288,15 @@ __device__ __forceinline__ unsigned list_groups(Select &sh, int groups, int K)
     return bound;
 }
 
-// The K largest logits of chunks [k0, k1).  Group g of their whole chunks is
-// chunks g 2^lg .. + 2^lg - 1; sh.gmax holds the upper 16 bits of its largest
+// The K largest logits of chunks [k0, k1).  Group g of their whole chunks is places
+// g 2^lg .. + 2^lg - 1 of the sweep; sh.gmax holds the upper 16 bits of its largest
 // logit's order.
 template <typename T, int NT, typename Put>
-__device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int lg, int K, Put put)
+__device__ void select_top(Select &sh, const Row<T> &row, const Sweep<T> &sweep, int k0, int k1, int lg, int K, Put put)
 {
     constexpr int W = Row<T>::W;
     const int tid = threadIdx.x;
-    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
-    const int groups = (max(hi - lo, 0) + (1 << lg) - 1) >> lg;
+    const int lo = sweep.lo, hi = sweep.hi, groups = (sweep.n + (1 << lg) - 1) >> lg;
     const int first = max(k0 * W - row.phase, 0), last = min(k1 * W - row.phase, row.vocab);
     const int n = max(last - first, 0);
     constexpr int Q = (kGroups + NT - 1) / NT, Few = Q < 3 ? Q : 3;
@@ -306,7 +305,7 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int lg
                                                 : list_groups<NT, Q>(sh, groups, K);
     const float least = bound <= 0x7fu ? -kInf : ord32_value(bound << 16);
     const int todo = (int)sh.listed << lg;
-    auto chunk_of = [&](int j) { return lo + (sh.list[j >> lg] << lg) + (j & ((1 << lg) - 1)); };
+    auto chunk_of = [&](int j) { return sweep.from + (sh.list[j >> lg] << lg) + (j & ((1 << lg) - 1)); };
     auto look = [&](const Chunk<T> &ch, int k) {
         float x[W];
         ch.widen(x);
@@ -318,13 +317,15 @@ __device__ void select_top(Select &sh, const Row<T> &row, int k0, int k1, int lg
     for (int j = tid; j < todo; j += 2 * NT) {   // two reads on their way at once
         const int ka = chunk_of(j), kb = j + NT < todo ? chunk_of(j + NT) : hi;
         Chunk<T> ca, cb;
-        if (ka < hi)
+        const bool has_a = ka >= lo && ka < hi;
+        if (has_a)
             ca.load(row.chunk(ka));
-        if (kb < hi)
+        const bool has_b = kb >= lo && kb < hi;
+        if (has_b)
             cb.load(row.chunk(kb));
-        if (ka < hi)
+        if (has_a)
             look(ca, ka);
-        if (kb < hi)
+        if (has_b)
             look(cb, kb);
     }
     const int e = tid < 2 * W ? row.edge(tid, k0, k1) : -1;
@@ -426,7 +427,7 @@ __device__ __forceinline__ void put_none(const LogprobArgs &a, int64_t row, int 
 
 // One workgroup per segment of a row (segs of them): the whole result where
 // segs is 1, else its LossPart and its top keys.  One pass, U chunks to a thread on
-// their way at once, 8 waves on a SIMD: 4096 x 128256 bf16 with entropy 162 us,
+// their way at once, 8 waves on a SIMD: 4096 x 128256 bf16 with entropy 161 us,
 // 6.5 TB/s; 2048 x 128256 with the 64 largest of each row 97 us (86 us without: the
 // selection is a chain of barriers that other workgroups fill only in part); 64 x
 // 128256 with twenty, cut for 1024 workgroups, 18 us with the joining launch,
@@ -449,27 +450,22 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
     const T *p = static_cast<const T *>(a.in.logits) + row_i * a.in.stride;
     const Row<T> row(p, a.in.vocab);
     const int k0 = min(seg * cps, row.chunks), k1 = min(k0 + cps, row.chunks);
-    const int lo = max(k0, row.full_lo), hi = min(k1, row.full_hi);
+    const Sweep<T> sweep(row, k0, k1);
     const float given = segs == 1 ? token_logit<T>(a, row_i) : 0.0f;
     const Scale sc(a.in.c);
     Sum q;
-    const int n = max(hi - lo, 0);   // whole chunks
-    const int lg = group_lanes<W>(n, a.top_k);
-    const __amdgpu_buffer_rsrc_t in = window(row.chunk(lo), n);
+    const int n = sweep.n, lg = group_lanes<W>(n, a.top_k);
     for (int b = 0; b < n; b += NT * U) {
         Chunk<T> ch[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)   // chunks past the segment are not read
-            ch[u].r = __builtin_bit_cast(decltype(ch[u].r),
-                                         __builtin_amdgcn_raw_buffer_load_b128(
-                                             in, tid * 16, (b + NT * u) * 16, kLoadStreamPolicy));
+        for (int u = 0; u < U; ++u)
+            ch[u] = sweep.read(b + NT * u);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int first = b + NT * u;
             if (first >= n)
                 break;
-            if (first + NT > n && first + tid >= n)
-                ch[u].clear();
+            sweep.trim(ch[u], first, NT);
             float x[W];
             ch[u].widen(x);
             float m = x[0];
@@ -500,12 +496,12 @@ void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
                 put_none(a, row_i, 0, t);
         } else if (segs == 1) {
             const float log2s = log2f(t.s);
-            select_top<T, NT>(sh, row, k0, k1, lg, a.top_k,
+            select_top<T, NT>(sh, row, sweep, k0, k1, lg, a.top_k,
                               [&](int r, uint64_t key) { put_top(a, row_i, r, key, t, log2s); });
             put_none(a, row_i, elems, t);
         } else {
             uint64_t *out = a.keys + (row_i * segs + seg) * a.top_k;
-            select_top<T, NT>(sh, row, k0, k1, lg, a.top_k,
+            select_top<T, NT>(sh, row, sweep, k0, k1, lg, a.top_k,
                               [&](int r, uint64_t key) { out[r] = key; });
             for (int i = elems + tid; i < a.top_k; i += NT)
                 out[i] = 0;   // below every logit's key

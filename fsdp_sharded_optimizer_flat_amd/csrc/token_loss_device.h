@@ -23,7 +23,7 @@
 // TB/s), so no term may be added lightly.  A single row waits for its one compute
 // unit instead (1 x 50304: 5 of 10.7 us).
 // Measured on one MI355X (a sweep that reads and writes reaches 6.7 TB/s there):
-// forward with entropy, 4096 x 128256 bf16, 162 us, 6.5 TB/s; backward, 2048 x
+// forward with entropy, 4096 x 128256 bf16, 161 us, 6.5 TB/s; backward, 2048 x
 // 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 740 us, 5.7 TB/s.
 #pragma once
 
@@ -188,6 +188,43 @@ struct Row {
         const int e = k * W - phase + (s & (W - 1));
         const bool partial = s < W ? (phase & (W - 1)) != 0 : full_hi < chunks;
         return partial && k >= k0 && k < k1 && e >= 0 && e < vocab ? e : -1;
+    }
+};
+
+// Chunks [lo, hi) of a row as a workgroup goes through them, NT threads at a time:
+// its place c is chunk from + c, from being the line that lo lies in, so that the
+// first `skip` places hold nothing (log probabilities of 4096 x 128255 bf16: 180 us
+// where the first thread takes chunk lo, 167 so).
+template <typename T>
+struct Sweep {
+    int lo, hi, skip, from, n;   // n: places
+    __amdgpu_buffer_rsrc_t in;
+    __device__ __forceinline__ Sweep(const Row<T> &row, int k0, int k1)
+        : lo(max(k0, row.full_lo)), hi(max(min(k1, row.full_hi), lo)), skip(lo & (kLine / 16 - 1)), from(lo - skip),
+          n(hi > lo ? hi - from : 0), in(window(row.chunk(lo), hi - lo))
+    {
+    }
+    // Reads place first + tid, first being the same in every lane and 0 or at least
+    // 64; what lies outside is not read (offsets below the first chunk wrap past
+    // the window).
+    __device__ __forceinline__ Chunk<T> read(int first) const
+    {
+        int at = ((int)threadIdx.x - skip) * 16 + (first ? kWave * 16 : 0);
+        asm volatile("" : "+v"(at));   // in a register: the wrapped sum
+        Chunk<T> ch;
+        ch.r = __builtin_bit_cast(decltype(ch.r),
+                                  __builtin_amdgcn_raw_buffer_load_b128(
+                                      in, at, first ? (first - kWave) * 16 : 0, kLoadStreamPolicy));
+        return ch;
+    }
+    // Makes a place outside -inf.
+    __device__ __forceinline__ void trim(Chunk<T> &ch, int first, int threads) const
+    {
+        if (first == 0 || first + threads > n) {
+            const int c = first + (int)threadIdx.x;
+            if (c < skip || c >= n)
+                ch.clear();
+        }
     }
 };
 
