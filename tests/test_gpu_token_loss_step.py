@@ -21,7 +21,7 @@ import oracle  # noqa: E402
 import fsdp_sharded_optimizer_flat_amd as z  # noqa: E402
 from gpu_common import DEV, assert_same_bf16, assert_same_f32, hyper_args, scalars, to_np  # noqa: E402
 from test_gpu_token_loss import (MODES, check_distill, check_logprob, check_logprob_grad,  # noqa: E402
-                                 check_top, gen, make_logits, make_record, ref_logp, workspace)
+                                 check_top, gen, make_logits, make_record, matrix, ref_logp, workspace)
 
 G, Lc = z.ZERO_GLOBAL, z.ZERO_LOCAL
 H = dict(lr=1e-2, b1=0.9, b2=0.95, eps=1e-8, wd=0.1)
@@ -319,3 +319,54 @@ def test_rows_of_one_tensor_are_refused():
         z.zero_logprob(x, tok, logprob=lp)
     with pytest.raises(ValueError):
         z.zero_logprob(torch.zeros(500, 4, device=DEV).t(), tok, logprob=lp)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [1, 5, 31, 64, 67, 517, 2049, 9001])
+def test_every_place_in_a_cache_line(vocab, dtype):
+    """Rows that start at each place of a 128-byte line (an odd stride walks through
+    them), gradients at the same places, at others and in place; what lies between
+    the rows stays as it was."""
+    rows, k = 70, 8
+    stride = vocab + 1 + vocab % 2
+    x = make_logits(rows, vocab, dtype, 500 + vocab, stride, 3)
+    places = {(x[r].data_ptr() // x.element_size()) % (128 // x.element_size()) for r in range(rows)}
+    assert len(places) == 128 // x.element_size()
+    tok = torch.randint(0, vocab, (rows,), generator=gen(1), device=DEV)
+    index, value = make_record(x, k, 1.0, 3)
+    w, h = torch.rand(rows, generator=gen(2), device=DEV), torch.rand(rows, generator=gen(3), device=DEV)
+    ws = workspace(x, k)[0]
+    f = lambda *s: torch.empty(*s, device=DEV)
+    lp, ent, st, st4, loss = f(rows), f(rows), f(rows, 2), f(rows, 4), f(rows)
+    ti, tv = torch.empty(rows, k, dtype=torch.int32, device=DEV), f(rows, k)
+    z.zero_logprob(x, tok, logprob=lp, entropy=ent, stats=st, top_index=ti, top_logprob=tv, workspace=ws)
+    z.zero_distill(x, index, value, MODES["tail"], loss=loss, stats=st4, workspace=ws)
+    torch.cuda.synchronize()
+    check_logprob(x, tok, 1.0, lp, ent, st, "forward")
+    check_top(x, 1.0, k, ti, tv, "forward")
+    check_distill(x, index, value, MODES["tail"], 1.0, loss, None, None, "forward")
+    for out_stride, shift in ((stride, 3), (stride + 2, 4), (vocab, 0)):
+        for fused in (False, True):
+            what = f"stride {out_stride} shift {shift} fused {fused}"
+            out, check = matrix(rows, vocab, dtype, out_stride, shift)
+            if fused:
+                z.zero_logprob_fused(x, tok, out, d_logprob=w, d_entropy=h, logprob=lp, workspace=ws)
+            else:
+                z.zero_logprob_grad(x, tok, st, out, d_logprob=w, d_entropy=h, entropy=ent)
+            torch.cuda.synchronize()
+            check(what)
+            check_logprob_grad(x, tok, 1.0, w, h, out, what)
+            out, check = matrix(rows, vocab, dtype, out_stride, shift)
+            if fused:
+                z.zero_distill_fused(x, index, value, MODES["tail"], w, out, loss=loss, workspace=ws)
+            else:
+                z.zero_distill_grad(x, index, value, MODES["tail"], st4, w, out)
+            torch.cuda.synchronize()
+            check(what)
+            check_distill(x, index, value, MODES["tail"], 1.0, loss if fused else None, w, out, what)
+    y, check = matrix(rows, vocab, dtype, stride, 3)
+    y.copy_(x)
+    z.zero_logprob_fused(y, tok, y, d_logprob=w, d_entropy=h, workspace=ws)
+    torch.cuda.synchronize()
+    check("in place")
+    check_logprob_grad(x, tok, 1.0, w, h, y, "in place")
