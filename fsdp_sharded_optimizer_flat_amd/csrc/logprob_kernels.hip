@@ -628,8 +628,8 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
 constexpr int kHeld = 16;   // chunks a thread holds: half of its 128 registers
 
 // Forward and backward of whole rows, at most kHeld NT chunks each, read once: 8192
-// x 128256 bf16 740 us, 5.7 TB/s (in two launches, each logit read twice, 1175 us);
-// 1024 x 50304 42 us; 777 x 50257 fp32 at another phase than its gradient 69 us.
+// x 128256 bf16 743 us, 5.7 TB/s (in two launches, each logit read twice, 1175 us);
+// 1024 x 50304 42 us; 777 x 50257 fp32 at another phase than its gradient 70 us.
 // Rows of 256 KB read and written in bursts reach 5.9 to 6.0 TB/s as a plain copy; a
 // workgroup's exponentials, twice over the row, fill most of what is left between
 // its bursts.  1024 threads of 64 registers, half the row to each, spill: 64 us for

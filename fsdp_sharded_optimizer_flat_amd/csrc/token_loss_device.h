@@ -19,12 +19,12 @@
 // writes, a fused call too (it holds the row in registers).  A bf16 element is 2
 // bytes against 7 to 10 vector issue slots (widen 1, max 1, fma 1, exp 2, add 1,
 // bookkeeping 1; entropy: clamp, product and sum 1 each): with the entropy the
-// vector units are as busy as the memory (counters: all of their cycles at 6.4
+// vector units are as busy as the memory (counters: 0.93 of their cycles at 6.5
 // TB/s), so no term may be added lightly.  A single row waits for its one compute
 // unit instead (1 x 50304: 5 of 10.7 us).
 // Measured on one MI355X (a sweep that reads and writes reaches 6.7 TB/s there):
 // forward with entropy, 4096 x 128256 bf16, 161 us, 6.5 TB/s; backward, 2048 x
-// 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 740 us, 5.7 TB/s.
+// 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 743 us, 5.7 TB/s.
 #pragma once
 
 #include <algorithm>
