@@ -599,7 +599,8 @@ struct HeldRow {
                                              kLoadStreamPolicy));
     }
     // Visits the groups of G chunks that hold anything: f(first chunk, values).
-    // Values past the row's whole chunks are -inf.
+    // Values past the row's whole chunks are -inf, as are those past the H chunks
+    // of a thread, where G does not divide H (i + j < H is known once unrolled).
     template <typename F>
     __device__ __forceinline__ void each_group(F f)
     {
@@ -610,6 +611,12 @@ struct HeldRow {
                 u32x4 raw[G];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
+                    if (i + j >= H) {
+#pragma unroll
+                        for (int w = 0; w < W; ++w)
+                            x[j * W + w] = -kInf;
+                        continue;
+                    }
                     if (i + j == 0 || NT * (i + j + 1) > row.full_hi) {   // kept a branch
                         int t = threadIdx.x;
                         asm volatile("" : "+v"(t));   // or the sums below would be kept over all rows
@@ -626,7 +633,7 @@ struct HeldRow {
                 f(i, x);
 #pragma unroll
                 for (int j = 0; j < G; ++j)
-                    if (i + j >= P0)
+                    if (i + j >= P0 && i + j < H)
                         park[NT * (i + j - P0) + threadIdx.x] = __builtin_bit_cast(u32x4, raw[j]);
             }
             __builtin_amdgcn_sched_barrier(0);
