@@ -498,8 +498,8 @@ __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, in
     const float coef = (float)(w * (total * (double)pow2(rest_ln * kLog2E) - rest)) * pow2(-off);
     if (here)   // in place: the listed logits are read before any is overwritten
         __syncthreads();
-    if (tm == -kInf)
-        fill_row(row, out, k0, k0 + kNT * U, 0.0f);
+    if (tm == -kInf)   // all others are masked: NaN where a listed logit is NaN or +inf
+        fill_row(row, out, k0, k0 + kNT * U, ln != ln ? __builtin_nanf("") : 0.0f);
     else if (__builtin_fabsf(tm) > k.big)
         seg.map(row, out, [&](float x) { return coef * pow2((x - tm) * k.c); });
     else
@@ -681,9 +681,9 @@ void distill_row_kernel(DistillArgs a, DistillGradArgs b)
         const float share = t.s * pow2(shift_of(t.m, whole.m, k)) / whole.s;
         const float coef = (float)(w * (te.total * (double)share - te.rest)) / t.s;
         const float m = t.m, ref = m * k.c;
-        if (fill || t.empty())
+        if (fill || t.empty())   // NaN too where a listed logit is NaN or +inf and all others are masked
             fill_row<T, NS>(held.row, out, 0, held.row.chunks,
-                            fill && te.bad && dl != 0.0f ? __builtin_nanf("") : 0.0f);
+                            dl != 0.0f && (te.bad || whole.s != whole.s) ? __builtin_nanf("") : 0.0f);
         else if (big)   // rare: from memory, so that the held row's code is not there twice
             for (int k0 = 0; k0 < held.row.chunks; k0 += NS)
                 RowPart<T, NS, 1>(held.row, k0).map(held.row, out,
