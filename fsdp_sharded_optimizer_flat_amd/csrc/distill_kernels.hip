@@ -266,7 +266,8 @@ __device__ __forceinline__ void finish_distill(Teacher &te, const Total &tail, c
                 v += rest * ((double)(kLn2 * log2f((float)rest)) - (double)(tail.empty() ? -kInf : lp));
             }
         }
-        loss[row] = te.bad ? __builtin_nanf("") : (float)v;
+        // a NaN in the row reaches v only through entries with a probability
+        loss[row] = te.bad || t.s != t.s ? __builtin_nanf("") : (float)v;
     }
     if (stats) {
         stats[4 * row] = t.empty() ? -kInf : t.m;

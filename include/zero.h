@@ -588,7 +588,9 @@ zero_status zero_clip_coef_ranks_async(const double *rank_sums_dev, int32_t n_ra
  *     probability -inf;
  *   - upstream weights of zero give a zero gradient, whatever the row holds;
  *   - a row whose logits are all -inf: logprob -inf, entropy 0, a loss of
- *     +inf, no alternatives, gradient zero;
+ *     +inf (0 where every q is zero), no alternatives, gradient zero;
+ *   - a teacher's record that gives no token a probability (ZERO_DISTILL_RENORM
+ *     over values of -inf only): loss and gradient zero;
  *   - a row with a NaN or +inf logit: NaN everywhere (alternatives index -1);
  *   - a token, or an index of a teacher's record, >= vocab, or a NaN value in
  *     the record: logprob, loss and the gradient row are NaN.  A NaN gradient

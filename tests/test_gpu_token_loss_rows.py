@@ -69,3 +69,33 @@ def test_nan_among_the_listed_of_a_masked_row(rows, vocab, dtype):
                 assert bool((loss2[kinds == 4] == INF).all())
                 assert bool(torch.isfinite(out[kinds == 4]).all())
             check_distill(x[f], index[f], value[f], mode, 1.0, loss2[f], dl[f], out[f], f"fused {fused}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", MASKED)
+def test_record_without_a_finite_value(rows, vocab, dtype):
+    """Values of -inf only, renormalised: no distribution, so the loss and the
+    gradient are zero -- but NaN over a row that holds a NaN or +inf, listed (1) or
+    not (2)."""
+    x = make_logits(rows, vocab, dtype, 78)
+    index, value = make_record(x, 12, 1.0, 5)
+    value.fill_(-INF)
+    kinds = torch.arange(rows, device=DEV) % 4
+    x[kinds == 1, 0] = NAN
+    index[kinds == 1, 2] = 0
+    x[kinds == 2, vocab - 1] = INF
+    index[kinds == 2] = torch.where(index[kinds == 2] == vocab - 1, 1, index[kinds == 2])
+    x[kinds == 3] = -INF
+    dl = torch.rand(rows, generator=gen(4), device=DEV) + 0.5
+    ws, _ = workspace(x)
+    bad = (kinds == 1) | (kinds == 2)
+    for fused in (False, True):
+        loss, st, out = torch.full((rows,), 5.0, device=DEV), torch.empty(rows, 4, device=DEV), torch.full_like(x, 9.0)
+        if fused:
+            z.zero_distill_fused(x, index, value, MODES["renorm"], dl, out, loss=loss, workspace=ws)
+        else:
+            z.zero_distill(x, index, value, MODES["renorm"], loss=loss, stats=st, workspace=ws)
+            z.zero_distill_grad(x, index, value, MODES["renorm"], st, dl, out)
+        torch.cuda.synchronize()
+        assert bool(torch.isnan(loss[bad]).all()) and bool((loss[~bad] == 0).all()), fused
+        assert bool(torch.isnan(out[bad]).all()) and bool((out[~bad] == 0).all()), fused
