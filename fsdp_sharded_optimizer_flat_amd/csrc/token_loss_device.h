@@ -240,15 +240,18 @@ __device__ __forceinline__ float rel(float l, float m, float r, const Scale &k)
 {
     return __builtin_fabsf(m) > k.big ? (l - m) * k.c : __builtin_fmaf(l, k.c, -r);
 }
-// t of reference m against reference n, as the sums were formed.
-__device__ __forceinline__ float shift_of(float m, float n, const Scale &k)
-{
-    return __builtin_fabsf(m) > k.big || __builtin_fabsf(n) > k.big ? (m - n) * k.c : m * k.c - n * k.c;
-}
 // c m - fl(c m): what the sums' reference R is off the exact one by.
 __device__ __forceinline__ float residue(float m, const Scale &k)
 {
     return __builtin_fabsf(m) > k.big ? 0.0f : __builtin_fmaf(m, k.c, -(m * k.c));
+}
+// t of reference m against reference n, as the sums were formed: R of either is
+// fl(c m), or c m itself beyond kBig.  Where one of them is of each kind (|c m|
+// around 2^20, fl(c m) off by up to 2^-5 there) the difference of the two kinds counts.
+__device__ __forceinline__ float shift_of(float m, float n, const Scale &k)
+{
+    return __builtin_fabsf(m) > k.big || __builtin_fabsf(n) > k.big ? (m - n) * k.c - residue(m, k) + residue(n, k)
+                                                                    : m * k.c - n * k.c;
 }
 __device__ __forceinline__ float pow2(float t) { return __builtin_amdgcn_exp2f(t); }
 

@@ -120,6 +120,41 @@ def test_gradients_of_large_and_tiny_logits(rows, vocab, dtype):
                     big_distill_grad(x, index, value, mode, scale, dl, out, f"{name} {what} {where} fused {fused}")
 
 
+@pytest.mark.parametrize("rows,vocab", [(8, 300), (8, 5003), (8, 37003), (300, 20011), (3, 140001)])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 16, 2.0 ** -10])
+def test_references_around_the_change_of_formula(rows, vocab, scale):
+    """Logits a few nats apart whose binary logarithms c l lie around 2^20, where a
+    reference beyond it takes t = (l - m) c and one below it c l - fl(c m): partial
+    sums of both kinds meet in a row.  The differences of such logits are exact
+    and t is as small as in ordinary rows, so their tolerances hold."""
+    base = 2.0 ** 20 / (scale * math.log2(math.e))
+    x = (torch.randn(rows, vocab, generator=gen(6), device=DEV, dtype=torch.float64) * 3.0 / scale)
+    x[1::2] -= 2 * base                    # to - base below
+    x = (x + base).float()
+    tok = torch.randint(0, vocab, (rows,), generator=gen(1), device=DEV)
+    dl = torch.rand(rows, generator=gen(4), device=DEV) + 0.5
+    dh = torch.rand(rows, generator=gen(5), device=DEV) + 0.1
+    ws, _ = workspace(x)
+    f = lambda *s: torch.empty(*s, device=DEV)
+    lp, h, st, st4, loss = f(rows), f(rows), f(rows, 2), f(rows, 4), f(rows)
+    index, _ = make_record(x - x.mean(1, keepdim=True), 20, scale, 3)
+    value = torch.log_softmax(torch.randn(rows, 20, generator=gen(8), device=DEV), 1) - 0.5
+    out = torch.empty_like(x)
+    z.zero_logprob(x, tok, scale=scale, logprob=lp, entropy=h, stats=st, workspace=ws)
+    check_logprob(x, tok, scale, lp, h, st, "forward")
+    z.zero_logprob_grad(x, tok, st, out, scale=scale, d_logprob=dl, d_entropy=dh, entropy=h)
+    check_logprob_grad(x, tok, scale, dl, dh, out, "backward")
+    z.zero_logprob_fused(x, tok, out, scale=scale, d_logprob=dl, d_entropy=dh, logprob=lp, entropy=h, workspace=ws)
+    check_logprob(x, tok, scale, lp, h, None, "fused")
+    check_logprob_grad(x, tok, scale, dl, dh, out, "fused")
+    for mode in MODES.values():
+        z.zero_distill(x, index, value, mode, scale=scale, loss=loss, stats=st4, workspace=ws)
+        z.zero_distill_grad(x, index, value, mode, st4, dl, out, scale=scale)
+        check_distill(x, index, value, mode, scale, loss, dl, out, f"mode {mode}")
+        z.zero_distill_fused(x, index, value, mode, dl, out, scale=scale, loss=loss, workspace=ws)
+        check_distill(x, index, value, mode, scale, loss, dl, out, f"mode {mode} fused")
+
+
 # -- rows without a distribution, under a mask ---------------------------------------------------
 
 MASKED = [(9, 3001), (300, 3001), (9, 40007), (9, 140001)]
