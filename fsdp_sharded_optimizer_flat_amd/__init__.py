@@ -862,7 +862,8 @@ def zero_gradnorm_traffic(layout: Layout, rank: int, n_grads: int, grad_dtype: i
 
 def zero_loss_workspace_bytes(rows: int, vocab: int, top_k: int = 0) -> int:
     """Bytes of a workspace (a device tensor) that is enough for every
-    token-loss call on ``rows`` rows of ``vocab`` logits."""
+    token-loss call on ``rows`` rows of ``vocab`` logits with up to ``top_k``
+    alternatives.  Fewer rows may need more: ask for each number of rows."""
     b = sz()
     _check(_zero_loss_workspace_bytes(rows, vocab, top_k, C.byref(b)), "zero_loss_workspace_bytes")
     return b.value

@@ -170,10 +170,14 @@ extern "C" zero_status zero_loss_workspace_bytes(int64_t rows, int64_t vocab, in
         return ZERO_EINVAL;
     if (vocab > ZERO_MAX_VOCAB || rows > ZERO_MAX_LOSS_ROWS || top_k > ZERO_MAX_TOP)
         return ZERO_ERANGE;
-    // the forward calls' split depends on top_k, the fused ones' does not
-    const Workspace f = workspace_layout(rows, loss_segments(rows, vocab, top_k), top_k, false);
-    const Workspace g = workspace_layout(rows, loss_segments(rows, vocab, 0), 0, true);
-    *bytes = (size_t)(f.bytes > g.bytes ? f.bytes : g.bytes);
+    // the forward calls' split depends on top_k, the fused ones' does not; with fewer
+    // alternatives a row may be cut further and need more for its partial results
+    int64_t most = workspace_layout(rows, loss_segments(rows, vocab, 0), 0, true).bytes;
+    for (int32_t k = 0; k <= top_k; ++k) {
+        const int64_t f = workspace_layout(rows, loss_segments(rows, vocab, k), k, false).bytes;
+        most = f > most ? f : most;
+    }
+    *bytes = (size_t)most;
     return ZERO_OK;
 }
 

@@ -615,9 +615,10 @@ zero_status zero_clip_coef_ranks_async(const double *rank_sums_dev, int32_t n_ra
 #define ZERO_DISTILL_TAIL 1
 
 /* Workspace bytes that are enough for each of the calls below on `rows` rows of
- * `vocab` logits (top_k alternatives for zero_logprob; 16-byte aligned device
- * memory).  A call that needs none (where this is 0; zero_*_fused on rows that
- * it holds on the chip) takes a NULL workspace. */
+ * `vocab` logits (up to top_k alternatives for zero_logprob; 16-byte aligned
+ * device memory).  Fewer rows may need more, because they are cut for more
+ * workgroups: ask for each number of rows.  A call that needs none (where this is
+ * 0; zero_*_fused on rows that it holds on the chip) takes a NULL workspace. */
 zero_status zero_loss_workspace_bytes(int64_t rows, int64_t vocab, int32_t top_k, size_t *bytes);
 
 /* Forward: any of logprob [rows], entropy [rows], stats [rows][2] and, with
