@@ -977,7 +977,7 @@ def zero_logprob_grad(logits, tokens, stats, d_logits, *, scale: float = 1.0, d_
                       d_entropy=None, entropy=None, stream=None):
     """Enqueue the backward pass: ``d_logits`` (which may be ``logits``) from
     the upstream gradients ``d_logprob`` and ``d_entropy``, the forward call's
-    ``stats`` and, with ``d_entropy``, its ``entropy``."""
+    ``tokens``, ``stats`` and, with ``d_entropy``, its ``entropy``."""
     p, dt, n, v, st, dev = _logits(logits)
     gp, gs = _d_logits(d_logits, logits)
     _check(_zero_logprob_grad(p, dt, n, v, st, scale,

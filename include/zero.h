@@ -634,7 +634,8 @@ zero_status zero_logprob(const void *logits, int32_t dtype, int64_t rows, int64_
 
 /* Backward: d_logits from the upstream gradients d_logprob and d_entropy
  * [rows] (either may be NULL: zero) and the forward call's stats and, with
- * d_entropy, entropy.  tokens may be NULL where d_logprob is. */
+ * d_entropy, entropy.  tokens: the forward call's, which mark its padding rows;
+ * NULL where they were NULL there and d_logprob is NULL. */
 zero_status zero_logprob_grad(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
                               int64_t row_stride, float scale, const int64_t *tokens,
                               const float *stats, const float *entropy,

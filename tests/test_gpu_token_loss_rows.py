@@ -239,6 +239,31 @@ def test_record_without_a_finite_value(rows, vocab, dtype):
         assert bool(torch.isnan(out[bad]).all()) and bool((out[~bad] == 0).all()), fused
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", MASKED)
+def test_entropy_gradient_alone_with_padding(rows, vocab, dtype):
+    """An entropy term without one of the log probability: padding rows, marked by
+    the tokens of the forward and the backward call, have none; without tokens
+    every row has one."""
+    x = make_logits(rows, vocab, dtype, 79)
+    tok = torch.randint(0, vocab, (rows,), generator=gen(1), device=DEV)
+    tok[::3] = -5
+    real = tok >= 0
+    dh = torch.randn(rows, generator=gen(2), device=DEV)
+    ws, _ = workspace(x)
+    for t, f in ((tok, real), (None, real | True)):
+        y = x if t is None else x.masked_fill(~real[:, None], NAN)
+        st, h, h2 = (torch.empty(rows, *s, device=DEV) for s in ((2,), (), ()))
+        out, out2 = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+        z.zero_logprob(y, t, entropy=h, stats=st, workspace=ws)
+        z.zero_logprob_grad(y, t, st, out, d_entropy=dh, entropy=h)
+        z.zero_logprob_fused(y, t, out2, d_entropy=dh, entropy=h2, workspace=ws)
+        torch.cuda.synchronize()
+        for g, e in ((out, h), (out2, h2)):
+            check_logprob_grad(x[f], torch.zeros_like(tok)[f], 1.0, None, dh[f], g[f], f"tokens {t is not None}")
+            assert bool((g[~f] == 0).all()) and bool((e[~f] == 0).all())
+
+
 # -- several rows to a workgroup -------------------------------------------------------------------
 
 def resident(threads):
