@@ -729,6 +729,15 @@ def setup_step(wl, fused=False, stage_chunk=None, stagger_kib=None, norm_only=No
     return ns
 
 
+def random_logits(n, tokens, vocab, dev):
+    """Normal bf16 logits of deviation 2 for n ranks' tokens."""
+    import torch
+    x = torch.empty(n, tokens, vocab, dtype=torch.bfloat16, device=dev)
+    for r in range(n):
+        x[r] = torch.randn(tokens, vocab, device=dev) * 2.0
+    return x
+
+
 def streamed_bench(args):
     """The per-unit step streamed beside a backward stand-in (one GPU).
 
@@ -810,28 +819,29 @@ def streamed_bench(args):
     loss_bytes = 0
     if args.loss != "none":
         V = workloads.VOCAB_GPT2L
-        logits = (torch.randn(tok, V, device=dev) * 2.0).to(torch.bfloat16)
-        d_logits = torch.empty(n, tok, V, dtype=torch.bfloat16, device=dev)
+        # each rank's own, so that no rank's are read from a cache another filled
+        logits = random_logits(n, tok, V, dev)
+        d_logits = torch.empty_like(logits)
         targets = torch.randint(0, V, (n, tok), device=dev)
         row_loss = torch.empty(n, tok, device=dev)
         weight = torch.full((tok,), (-1.0 if args.loss == "lm" else 1.0) / tok, device=dev)
         loss_ws = torch.empty(max(z.zero_loss_workspace_bytes(tok, V, args.top_k), 1),
                               dtype=torch.uint8, device=dev)
-        loss_bytes = n * tok * V * 2 * 2
+        loss_bytes = logits.nbytes + d_logits.nbytes
         if args.loss == "distill":
-            teacher = (torch.randn(tok, V, device=dev) * 2.0).to(torch.bfloat16)
+            teacher = random_logits(n, tok, V, dev)
             top_i = torch.empty(tok, args.top_k, dtype=torch.int32, device=dev)
             top_v = torch.empty(tok, args.top_k, device=dev)
-            loss_bytes = n * tok * V * 2 * 3
+            loss_bytes += teacher.nbytes
 
     def loss():
         for r in range(n):
             if args.loss == "lm":
-                z.zero_logprob_fused(logits, targets[r], d_logits[r], d_logprob=weight,
+                z.zero_logprob_fused(logits[r], targets[r], d_logits[r], d_logprob=weight,
                                      logprob=row_loss[r], workspace=loss_ws)
             elif args.loss == "distill":
-                z.zero_logprob(teacher, top_index=top_i, top_logprob=top_v, workspace=loss_ws)
-                z.zero_distill_fused(logits, top_i, top_v, z.ZERO_DISTILL_RENORM, weight, d_logits[r],
+                z.zero_logprob(teacher[r], top_index=top_i, top_logprob=top_v, workspace=loss_ws)
+                z.zero_distill_fused(logits[r], top_i, top_v, z.ZERO_DISTILL_RENORM, weight, d_logits[r],
                                      loss=row_loss[r], workspace=loss_ws)
 
     def produce(u, slot):
@@ -968,6 +978,8 @@ def streamed_bench(args):
     if args.loss != "none":
         result["config"].update(loss=args.loss, vocab=V,
                                 teacher_top_k=args.top_k if args.loss == "distill" else None)
+        # a rate of HBM where the ranks' logits together exceed the memory-side cache (256 MB)
+        result["loss_bytes"] = loss_bytes
         result["loss_hbm_GBps"] = loss_bytes / (res["loss_only"][0] / 1e3) / 1e9
         result["mean_loss"] = float(row_loss.mean()) * (-1.0 if args.loss == "lm" else 1.0)
     print(json.dumps(result))
