@@ -21,7 +21,7 @@ struct Teacher {
     float logit[ZERO_MAX_TOP];      // the student's
     float listed_max, listed_sum;   // of the listed tokens, each once
     float max, log2z;               // of the row: largest logit, binary logarithm of the sum
-    int any, bad;                   // an entry at all; one outside the vocabulary or with a NaN value
+    int bad;                        // an entry outside the vocabulary or with a NaN value
 };
 
 // The backward pass's share of it.
@@ -144,15 +144,13 @@ __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, 
                                              const Scale &sc, float scale, bool twice, int lane)
 {
     const bool renorm = mode == ZERO_DISTILL_RENORM;
-    bool some = false, bad = false;
+    bool bad = false;
     float top = kLowest, lm = -kInf;
 #pragma nounroll
     for (int k = lane; k < K; k += kWave) {
         int id = index[k];
         const float val = value[k];
-        const bool nan = val != val;
-        some = some || id >= 0 || nan;
-        bad = bad || id >= vocab || nan;
+        bad = bad || id >= vocab || val != val;
         id = id < 0 || id >= vocab ? -1 : id;
         const float l = id >= 0 ? grad_at<T>(logits, id) : -kInf;
         te.index[k] = te.lead[k] = id;
@@ -162,7 +160,6 @@ __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, 
             top = __builtin_fmaxf(top, val);
         lm = __builtin_fmaxf(lm, l);
     }
-    some = __any(some);
     bad = __any(bad);
     lm = wave_max(lm);
     // q: exp of the given value, or the softmax over the entries
@@ -223,7 +220,6 @@ __device__ __forceinline__ void read_teacher(Teacher &te, const int32_t *index, 
         te.cross = cross;
         te.listed_max = ref;
         te.listed_sum = ls;
-        te.any = some;
         te.bad = bad;
     }
 }
