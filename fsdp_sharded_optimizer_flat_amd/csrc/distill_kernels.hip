@@ -300,8 +300,8 @@ constexpr int kBitWords = (int)(kLossMaxSegment / 32) + 8;
 // from the whole sum would lose the rest's digits where little is left).  A wide
 // workgroup (few rows, each whole: latency counts) leaves the record to its last
 // wave, beside the others' sums, and has its first chunks on their way before it
-// looks at anything else: 3 x 50257 fp32 8.1 us; 2048 x 128256 bf16, 64 listed, 91 us,
-// 5.8 TB/s.
+// looks at anything else: 3 x 50257 fp32 8.2 us; 2048 x 128256 bf16, 64 listed, 93 us,
+// 5.6 TB/s.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a, int64_t row0, int segs, int cps)
 {
@@ -422,8 +422,8 @@ __global__ __launch_bounds__(kNT) void distill_join_kernel(DistillArgs a, int64_
 // probabilities for itself; a workgroup that holds no listed token needs nothing
 // more of the record and no barrier.  (The first of sixteen waves adding them up
 // for all, one chunk to a thread: 330 us for 2048 rows of 128256 bf16 and 64
-// listed, where this takes 185: the other waves wait for its reads and products.)
-// 2048 x 128256 bf16, 64 listed: 179 us, 5.9 TB/s.
+// listed, where this takes 184: the other waves wait for its reads and products.)
+// 2048 x 128256 bf16: 32 listed 179 us, 5.9 TB/s, 64 listed 184, 256 listed 230.
 template <typename T, int U>
 __global__ __launch_bounds__(kNT) void distill_grad_kernel(DistillGradArgs a, int64_t row0, int segs)
 {
@@ -535,8 +535,9 @@ constexpr int kHeld = 17;   // chunks a thread holds: 960 threads hold 128256 bf
 // row, and writes the listed tokens' gradients while they sum the next one:
 // what takes its time there are a few dependent reads, which would hold up a
 // wave that also has its share of the row.  Records and bitmaps have two places.
-// 4096 x 128256 bf16, 64 listed: 398 us, 5.3 TB/s (497 us with the record in the
-// hands of a wave that also sums); 511 x 50257 27 us.
+// 4096 x 128256 bf16, 64 listed: 399 us, 5.3 TB/s (497 us with the record in the
+// hands of a wave that also sums); 511 x 50257 27 us.  A copy kernel that only holds
+// such rows, 1024 and 512 threads to a row, takes 361 and 22.
 template <typename T, int NS, bool SAME>
 __global__ __launch_bounds__(NS + kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_row_kernel(DistillArgs a, DistillGradArgs b)
@@ -774,7 +775,7 @@ int launch_distill_grad(const DistillGradArgs &a, void *stream)
         });
     };
     // Fewer workgroups add up long records (2048 rows of 128256 bf16, U = 4 and 8:
-    // 185 and 194 us at 64 listed, one to a lane; 216 and 202 at 128; 289 and 230
+    // 186 and 195 us at 64 listed, one to a lane; 213 and 202 at 128; 286 and 230
     // at 256).
     return a.top_k <= kWave ? launch(std::integral_constant<int, 4>())
                             : launch(std::integral_constant<int, 8>());

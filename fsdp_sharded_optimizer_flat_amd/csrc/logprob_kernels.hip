@@ -427,12 +427,12 @@ __device__ __forceinline__ void put_none(const LogprobArgs &a, int64_t row, int 
 
 // One workgroup per segment of a row (segs of them): the whole result where
 // segs is 1, else its LossPart and its top keys.  One pass, U chunks to a thread on
-// their way at once, 8 waves on a SIMD: 4096 x 128256 bf16 with entropy 161 us,
-// 6.5 TB/s; 2048 x 128256 with the 64 largest of each row 97 us (86 us without: the
+// their way at once, 8 waves on a SIMD: 4096 x 128256 bf16 with entropy 162 us,
+// 6.5 TB/s; 2048 x 128256 with the 64 largest of each row 98 us (82 us without: the
 // selection is a chain of barriers that other workgroups fill only in part); 64 x
 // 128256 with twenty, cut for 1024 workgroups, 18 us with the joining launch,
 // both latency: loads, four barriers and a second read of the chosen groups; 1 x
-// 50304 with five 10.7 us, one workgroup, half of it for the sums.
+// 50304 with five 10.9 us, one workgroup, half of it for the sums.
 template <typename T, int NT, bool ENT, bool TOP>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT == kNT ? 8 : 4)))
 void logprob_kernel(LogprobArgs a, int64_t row0, int segs, int cps)
@@ -586,8 +586,8 @@ __global__ __launch_bounds__(kNT) void logprob_join_kernel(LogprobArgs a, int64_
 // 2^t inv this is [j = t] scale d_lp - p_j (u + v t), u and v the row's.
 // One workgroup per kNT chunks of a row, one to a thread: neighbouring workgroups
 // sweep the memory in order, as a copy does (2048 x 50304 fp32 with an entropy
-// gradient: 123 us, 6.7 TB/s; cut for fewer workgroups, several chunks to a thread,
-// 159 us).
+// gradient: 124 us, 6.6 TB/s; cut for fewer workgroups, several chunks to a thread,
+// 159 us; 2048 x 128256 bf16, with or without it: 165 us, 6.4 TB/s).
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, int64_t row0, int segs)
 {
@@ -628,12 +628,12 @@ __global__ __launch_bounds__(kNT) void logprob_grad_kernel(LogprobGradArgs a, in
 constexpr int kHeld = 16;   // chunks a thread holds: half of its 128 registers
 
 // Forward and backward of whole rows, at most kHeld NT chunks each, read once: 8192
-// x 128256 bf16 743 us, 5.7 TB/s (in two launches, each logit read twice, 1175 us);
-// 1024 x 50304 42 us; 777 x 50257 fp32 at another phase than its gradient 70 us.
-// Rows of 256 KB read and written in bursts reach 5.9 to 6.0 TB/s as a plain copy; a
-// workgroup's exponentials, twice over the row, fill most of what is left between
-// its bursts.  1024 threads of 64 registers, half the row to each, spill: 64 us for
-// 1024 x 50304.
+// x 128256 bf16 746 us, 5.6 TB/s (in two launches, each logit read twice, 1175 us);
+// 1024 x 50304 42 us; 777 x 50257 fp32 at another phase than its gradient 70 us, at
+// the same 65.  A copy kernel of the same loads, barrier and stores, without the
+// mathematics, takes 712 us for 8192 rows of 256512 bytes, 39 for 1024 of 100608 and 62
+// for 777 of 201024.  1024 threads of 64 registers, half the row to each, spill: 64
+// us for 1024 x 50304.
 template <typename T, int NT, bool ENT, bool SAME>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4)))
 void logprob_row_kernel(LogprobArgs a, LogprobGradArgs b)

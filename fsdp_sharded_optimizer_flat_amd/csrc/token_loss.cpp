@@ -137,12 +137,20 @@ int32_t loss_segments(int64_t rows, int64_t vocab, int32_t top_k)
     // (4 workgroups on each of 256 compute units).  Fewer rows are cut so that
     // there are about that many workgroups, in segments of at least 2048 elements
     // and 128 per wanted alternative, with at most 4096 alternatives for the joining
-    // workgroup -- unless a workgroup of 1024 threads sums a row sooner than a
-    // second launch joins its segments (whole and cut, bf16: 64 rows of 20000 with
-    // five alternatives 8.6 and 10.7 us, of 65536 12.8 and 12.6; 256 of 50304 with
-    // twenty 12.4 and 16.2; 1 of 50304 without any 6.4 and 5.2; distillation, 64 of
-    // 50304, 64 listed, 8.3 and 14.3).  A function of the sizes alone, so the
-    // result does not depend on the device's state.
+    // workgroup.  Up to 256 rows of at most 65536 elements stay whole: a workgroup of
+    // 1024 threads sums a row sooner than a second launch joins its segments, except
+    // for few long rows without many alternatives (bf16, whole and cut, us):
+    //     rows x elements   entropy    and top 5    and top 20   distillation, 64 listed
+    //       1 x  20000     5.6   6.4    8.7  10.1    9.1  10.5     6.3  13.2
+    //       1 x  50304     7.6   6.6   11.6  11.3   11.9  12.4     8.2  13.3
+    //       1 x  65536     8.0   6.4   12.5  12.0   12.8  12.7     9.3  13.2
+    //      16 x  50304     8.3   7.5   12.5  12.6   12.7  13.8     8.9  14.2
+    //      64 x  20000     6.9   7.9   10.0  12.1   10.3  12.3     7.4  15.2
+    //      64 x  65536     9.0   9.0   13.9  14.0   15.1  16.2    10.7  16.0
+    //     256 x  50304    10.2  12.5   14.5  17.6   15.2  19.7    11.2  19.5
+    // There is one border for all calls; where cut rows win it costs up to 1.6 us.  A
+    // function of the sizes alone, so the result does not depend on the device's
+    // state.
     if (rows <= kLossWideRows && vocab <= kLossWideVocab)
         return 1;
     const int64_t need = (vocab + kLossMaxSegment - 1) / kLossMaxSegment;

@@ -19,12 +19,13 @@
 // writes, a fused call too (it holds the row in registers).  A bf16 element is 2
 // bytes against 7 to 10 vector issue slots (widen 1, max 1, fma 1, exp 2, add 1,
 // bookkeeping 1; entropy: clamp, product and sum 1 each): with the entropy the
-// vector units are as busy as the memory (counters: 0.93 of their cycles at 6.5
+// vector units are as busy as the memory (counters: 0.92 of their cycles at 6.5
 // TB/s), so no term may be added lightly.  A single row waits for its one compute
-// unit instead (1 x 50304: 5 of 10.7 us).
-// Measured on one MI355X (a sweep that reads and writes reaches 6.7 TB/s there):
-// forward with entropy, 4096 x 128256 bf16, 161 us, 6.5 TB/s; backward, 2048 x
-// 50304 fp32, 123 us, 6.7 TB/s; fused, 8192 x 128256 bf16, 743 us, 5.7 TB/s.
+// unit instead (1 x 50304: 5 of 10.9 us).
+// Log probabilities on one MI355X (a sweep that reads and writes reaches 6.4 to 6.7
+// TB/s there): forward with entropy, 4096 x 128256 bf16, 162 us, 6.5 TB/s;
+// backward with entropy, 2048 x 50304 fp32, 124 us, 6.6 TB/s, 2048 x 128256 bf16,
+// 165 us, 6.4 TB/s; loss and gradient, 8192 x 128256 bf16, 746 us, 5.6 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -104,8 +105,9 @@ __device__ __forceinline__ u32x4 pack_chunk(const float (&g)[W])
 }
 // Stores 16 bytes at any element's address (gfx950 takes such stores), for
 // gradients whose rows sit at another 16-byte phase than their logits: reading
-// the logits unaligned instead measured slower (777 x 50257 fp32, loss and
-// gradient: 70 us, and 80 to 93 us with unaligned loads).
+// the logits unaligned instead measured slower (log probabilities, loss and gradient
+// of 777 x 50257 fp32 in rows of 50304, the gradient's rows back to back: 70 us, and 80
+// to 93 us with unaligned loads).
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <typename T>
 __device__ __forceinline__ void store_any(u32x4 v, T *p)
@@ -144,10 +146,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const T *p, int chunks)
 // Stores chunk `tid` - skip of a window of `chunks` chunks from p on, nontemporal (the
 // threads below skip store nothing: their offset wraps past the window).  Not written
 // through to memory (sc1) as well: where waves share a cache line its halves then go
-// out one by one (loss and gradient of 4096 x 128256 bf16, whole lines, 380 us so and
-// 374 without; with waves that began anywhere in a line, 4096 x 128255, 457 and 422).
-// Without the nontemporal hint outputs beyond the memory-side cache lose (4096 x
-// 128256: 413).  Each store has a window of its own, no offset in a scalar register:
+// out one by one (log probabilities, loss and gradient of 4096 x 128256 bf16, whole
+// lines, 380 us so and 374 without; with waves that began anywhere in a line, 4096 x
+// 128255, 457 and 422).  Without the nontemporal hint outputs beyond the memory-side
+// cache lose (4096 x 128256: 413).  Each store has a window of its own, no offset in a scalar register:
 // MI355X has stored what the next instruction wrote to the data registers of a
 // 16-byte buffer store with such an offset (the compiler leaves no wait between the
 // two then).
@@ -163,8 +165,9 @@ __device__ __forceinline__ void store_chunks(u32x4 v, T *p, int chunks, int skip
 // in, so that waves that take 64 chunks of a row at a time read and write whole
 // lines: chunk k holds elements k W - phase .. + W - 1, whole for full_lo <= k <
 // full_hi; the one before and the one after may hold a few elements of the row and
-// are read element by element.  (Counted from the 16 bytes it starts in: loss and
-// gradient of 4096 x 128255 bf16 422 us, and 378 so; 777 x 50257 fp32 70 and 64.)
+// are read element by element.  (Counted from the 16 bytes it starts in: log
+// probabilities, loss and gradient of 4096 x 128255 bf16 422 us, and 378 so; 777 x
+// 50257 fp32, logits and gradient back to back, 70 and 64.)
 template <typename T>
 struct Row {
     static constexpr int W = Chunk<T>::W;
@@ -705,9 +708,10 @@ inline bool wide_rows(const LossRows &in) { return in.rows <= kLossWideRows && i
 
 // Workgroups of a launch that goes through rows: as many as are resident at once
 // (128 registers a thread: 16 waves on a compute unit), or one per row where
-// each would get four rows or fewer (1024 x 50304 bf16, loss and gradient, when
-// this was chosen: 39 us, and 44 us with two rows to a workgroup; 8192 x 128256,
-// 32 rows to a workgroup: 772 us, and 840 us with a workgroup per row).
+// each would get four rows or fewer.  Log probabilities, loss and gradient in bf16,
+// going through rows and a workgroup per row: 8192 x 128256 (32 rows each) 748 and
+// 784 us; 4096 x 50304 (eight) 155 and 147; 2048 x 50304 (four) 82 and 81; 1024 x 50304
+// (two) 43 and 46: around the border the two are within 7 %.
 inline unsigned held_grid(int64_t rows, int threads)
 {
     const int64_t most = (int64_t)device_cu_count() * (1024 / threads);
