@@ -5,6 +5,7 @@
 
 #include <cmath>
 
+#include "call_check.h"
 #include "token_loss.h"
 
 namespace zero {
@@ -12,43 +13,6 @@ namespace zero {
 namespace {
 
 constexpr double kLog2E = 1.4426950408889634074;
-
-int esize(int32_t d) { return d == ZERO_BF16 ? 2 : 4; }
-
-// A buffer of the call: `bytes` from p, elements of `align` bytes.
-struct Span {
-    const void *p;
-    int64_t bytes;
-    int align;
-};
-
-bool overlaps(const Span &a, const Span &b)
-{
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0)
-        return false;
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
-}
-
-// The outputs must be aligned and apart from each other and from the inputs.
-zero_status check_spans(const Span *in, int n_in, const Span *out, int n_out)
-{
-    for (int i = 0; i < n_in; ++i)
-        if ((uintptr_t)in[i].p % (uintptr_t)in[i].align)
-            return ZERO_EALIGN;
-    for (int i = 0; i < n_out; ++i)
-        if ((uintptr_t)out[i].p % (uintptr_t)out[i].align)
-            return ZERO_EALIGN;
-    for (int i = 0; i < n_out; ++i) {
-        for (int k = 0; k < n_in; ++k)
-            if (overlaps(out[i], in[k]))
-                return ZERO_EINVAL;
-        for (int k = 0; k < i; ++k)
-            if (overlaps(out[i], out[k]))
-                return ZERO_EINVAL;
-    }
-    return ZERO_OK;
-}
 
 // Sizes and the logits of a call; fills `r`.
 zero_status check_rows(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
@@ -79,7 +43,6 @@ Span matrix(const void *p, const LossRows &r, int64_t stride)
     return {p, r.rows > 0 ? ((r.rows - 1) * stride + r.vocab) * es : 0, es};
 }
 Span logits_span(const LossRows &r) { return matrix(r.logits, r, r.stride); }
-Span vec(const void *p, int64_t n, int es) { return {p, p ? n * es : 0, es}; }
 
 // The gradient may be written over the logits, row for row, but must not
 // overlap them otherwise.
@@ -93,7 +56,6 @@ bool in_place(const LossRows &r, const void *d_logits, int64_t d_stride)
 struct Workspace {
     int64_t stats = 0, entropy = 0, parts = 0, keys = 0, bytes = 0;
 };
-int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
 Workspace workspace_layout(int64_t rows, int32_t segs, int32_t top_k, bool fused)
 {
     Workspace w;
@@ -116,18 +78,10 @@ Workspace workspace_layout(int64_t rows, int32_t segs, int32_t top_k, bool fused
 
 zero_status check_workspace(const void *ws, size_t have, const Workspace &w)
 {
-    if (w.bytes == 0)
-        return ZERO_OK;
-    if (!ws)
-        return ZERO_EINVAL;
-    if ((uintptr_t)ws % 16)
-        return ZERO_EALIGN;
-    return have < (size_t)w.bytes ? ZERO_ENOSPC : ZERO_OK;
+    return check_workspace_bytes(ws, have, w.bytes);
 }
 
 char *at(void *ws, int64_t off) { return static_cast<char *>(ws) + off; }
-
-zero_status done(int e, const char *where) { return e == hipSuccess ? ZERO_OK : hip_fail(e, where); }
 
 }  // namespace
 
