@@ -42,6 +42,11 @@ ZERO_NOALLOC_SCRATCH_BYTES = 16 << 20
 ZERO_CAP_STEP, ZERO_CAP_STEP1, ZERO_CAP_NORM = 0, 1, 2
 ZERO_MAX_VOCAB, ZERO_MAX_TOP, ZERO_MAX_LOSS_ROWS = 1 << 20, 256, 0x7FFFFFFF
 ZERO_DISTILL_RENORM, ZERO_DISTILL_TAIL = 0, 1
+ZERO_MAX_SEQUENCES = 1 << 20
+ZERO_SEQUENCE_MEAN, ZERO_SEQUENCE_SUM = 0, 1
+ZERO_PREFER_SIGMOID, ZERO_PREFER_HINGE, ZERO_PREFER_SQUARED = 0, 1, 2
+ZERO_MAX_HIDDEN, ZERO_MAX_EMBEDDING_ROWS = 1 << 20, 1 << 20
+ZERO_ACT8_BLOCK = 32
 
 i32, i64, f32, f64, vp, sz = C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_void_p, C.c_size_t
 
@@ -178,6 +183,23 @@ _zero_distill_grad = _sig("zero_distill_grad", i32, vp, i32, i64, i64, i64, f32,
                           vp, vp, i64, vp)
 _zero_distill_fused = _sig("zero_distill_fused", i32, vp, i32, i64, i64, i64, f32, i32, vp, vp, i32,
                            vp, vp, vp, i64, vp, sz, vp)
+_zero_sequence_loss_workspace_bytes = _sig("zero_sequence_loss_workspace_bytes", i32, i64, i64,
+                                           C.POINTER(sz))
+_zero_policy_loss = _sig("zero_policy_loss", i32, vp, vp, vp, vp, i32, vp, i64, vp, i64, f64, f64, f64,
+                         i32, vp, vp, vp, vp, vp, vp, sz, vp)
+_zero_preference_loss = _sig("zero_preference_loss", i32, vp, vp, vp, i64, vp, i64, i32, f64, f64, f64,
+                             i32, vp, vp, vp, vp, vp, sz, vp)
+_zero_embedding = _sig("zero_embedding", i32, vp, i32, i64, i64, i64, vp, i64, f32, vp, i32, i64, vp)
+_zero_embedding_grad_workspace_bytes = _sig("zero_embedding_grad_workspace_bytes", i32, i64, i64, i64,
+                                            C.POINTER(sz))
+_zero_embedding_grad = _sig("zero_embedding_grad", i32, vp, i32, i64, i64, i64, vp, f32, vp, i32, i64,
+                            i64, i32, vp, sz, vp)
+_zero_act8_pack = _sig("zero_act8_pack", i32, vp, i32, i64, i64, i64, vp, vp, vp)
+_zero_act8_unpack = _sig("zero_act8_unpack", i32, vp, vp, i64, i64, vp, i32, i64, vp)
+_zero_act8_weight_grad_workspace_bytes = _sig("zero_act8_weight_grad_workspace_bytes", i32, i64, i64,
+                                              i64, C.POINTER(sz))
+_zero_act8_weight_grad = _sig("zero_act8_weight_grad", i32, vp, i64, i64, i64, vp, vp, i64, vp, i32, i64,
+                              i32, vp, sz, vp)
 _zero_strerror = _sig("zero_strerror", C.c_char_p, i32)
 _zero_last_hip_error = _sig("zero_last_hip_error", C.c_char_p)
 _zero_abi_version = _sig("zero_abi_version", i32)
@@ -197,6 +219,10 @@ EXPORTED = ["zero_layout_bytes", "zero_pack", "zero_pack_rows", "zero_reshard",
             "zero_set_waves_per_cu", "zero_get_waves_per_cu", "zero_get_waves_per_cu_for",
             "zero_loss_workspace_bytes", "zero_logprob", "zero_logprob_grad", "zero_logprob_fused",
             "zero_distill", "zero_distill_grad", "zero_distill_fused",
+            "zero_sequence_loss_workspace_bytes", "zero_policy_loss", "zero_preference_loss",
+            "zero_embedding", "zero_embedding_grad_workspace_bytes", "zero_embedding_grad",
+            "zero_act8_pack", "zero_act8_unpack", "zero_act8_weight_grad_workspace_bytes",
+            "zero_act8_weight_grad",
             "zero_strerror", "zero_last_hip_error", "zero_abi_version"]
 
 
@@ -875,7 +901,7 @@ def zero_loss_workspace_bytes(rows: int, vocab: int, top_k: int = 0) -> int:
 def _rows_of(t, what: str):
     """(address, row stride) of a 2-D device tensor whose rows are contiguous."""
     if t.dim() != 2:
-        raise ValueError(f"{what} must have two dimensions (rows, vocab)")
+        raise ValueError(f"{what} must have two dimensions")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor (got {t.device})")
     n, v = t.shape
@@ -1045,6 +1071,202 @@ def zero_distill_fused(logits, top_index, top_value, mode: int, d_loss, d_logits
                                _row_values(d_loss, n, dev, "d_loss"),
                                _row_values(loss, n, dev, "loss"), gp, gs, wp, wb, _stream_on(stream, dev)),
            "zero_distill_fused")
+
+
+# -- sequence losses ------------------------------------------------------------------------
+
+def _on_current_device(t, what: str) -> int:
+    """Index of the device of a tensor that names it for the call, which must be
+    the current one (the calls run on its streams)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must be a device tensor (got {t.device})")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def zero_sequence_loss_workspace_bytes(n_tokens: int, n_seqs: int) -> int:
+    """Bytes of a workspace (a device tensor) that is enough for either sequence
+    loss on ``n_tokens`` positions of ``n_seqs`` sequences (pairs count twice)."""
+    b = sz()
+    _check(_zero_sequence_loss_workspace_bytes(n_tokens, n_seqs, C.byref(b)),
+           "zero_sequence_loss_workspace_bytes")
+    return b.value
+
+
+def _sequences(logprob, offsets, tokens):
+    """(device index, n_tokens, n_seqs, offsets address, tokens address)"""
+    dev = _on_current_device(logprob, "logprob")
+    n, b = logprob.numel(), offsets.numel() - 1
+    if b < 0:
+        raise ValueError("offsets must hold the sequences' starts and the last one's end")
+    i64t = _torch().int64
+    return (dev, n, b, _row_values(offsets, b + 1, dev, "offsets", i64t),
+            _row_values(tokens, n, dev, "tokens", i64t))
+
+
+def zero_policy_loss(logprob, old_logprob, advantage, offsets, *, tokens=None, ref_logprob=None,
+                     per_token: bool = False, clip_low: float = 0.2, clip_high: float = 0.2,
+                     kl_coef: float = 0.0, mode: int = ZERO_SEQUENCE_MEAN, d_loss=None, loss=None,
+                     kl=None, clipped=None, d_logprob=None, workspace=None, stream=None):
+    """Enqueue the clipped policy loss of packed sequences and its gradient.
+
+    ``logprob``, ``old_logprob``, ``ref_logprob`` float32 (n_tokens,); sequence b
+    is positions ``offsets[b]`` to ``offsets[b + 1] - 1`` (int64 on the device);
+    positions whose ``tokens`` (int64) are negative are no targets.  ``advantage``
+    is one value per position (``per_token``) or per sequence.  Outputs left None
+    are not computed: ``loss``, ``kl`` float32 and ``clipped`` int32 (n_seqs,),
+    ``d_logprob`` float32 (n_tokens,) from the upstream ``d_loss`` (n_seqs,)."""
+    dev, n, b, off, tok = _sequences(logprob, offsets, tokens)
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_policy_loss(_row_values(logprob, n, dev, "logprob"),
+                             _row_values(old_logprob, n, dev, "old_logprob"),
+                             _row_values(ref_logprob, n, dev, "ref_logprob"),
+                             _row_values(advantage, n if per_token else b, dev, "advantage"),
+                             int(per_token), tok, n, off, b, clip_low, clip_high, kl_coef, mode,
+                             _row_values(d_loss, b, dev, "d_loss"), _row_values(loss, b, dev, "loss"),
+                             _row_values(kl, b, dev, "kl"),
+                             _row_values(clipped, b, dev, "clipped", _torch().int32),
+                             _row_values(d_logprob, n, dev, "d_logprob"), wp, wb,
+                             _stream_on(stream, dev)), "zero_policy_loss")
+
+
+def zero_preference_loss(logprob, offsets, *, tokens=None, ref_logprob=None,
+                         kind: int = ZERO_PREFER_SIGMOID, beta: float = 0.1, margin: float = 0.0,
+                         smoothing: float = 0.0, mode: int = ZERO_SEQUENCE_SUM, d_loss=None, loss=None,
+                         reward=None, d_logprob=None, workspace=None, stream=None):
+    """Enqueue the preference loss of pairs of packed sequences (pair p: sequence
+    p chosen, n_pairs + p rejected) and its gradient; see zero_policy_loss for
+    the sequences.  ``loss`` and ``d_loss`` (n_pairs,), ``reward`` (2 n_pairs,)."""
+    dev, n, b, off, tok = _sequences(logprob, offsets, tokens)
+    if b % 2:
+        raise ValueError(f"offsets name {b} sequences; pairs need an even number")
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_preference_loss(_row_values(logprob, n, dev, "logprob"),
+                                 _row_values(ref_logprob, n, dev, "ref_logprob"), tok, n, off, b // 2,
+                                 kind, beta, margin, smoothing, mode,
+                                 _row_values(d_loss, b // 2, dev, "d_loss"),
+                                 _row_values(loss, b // 2, dev, "loss"),
+                                 _row_values(reward, b, dev, "reward"),
+                                 _row_values(d_logprob, n, dev, "d_logprob"), wp, wb,
+                                 _stream_on(stream, dev)), "zero_preference_loss")
+
+
+# -- embedding --------------------------------------------------------------------------------
+
+def _matrix(t, dev: int, what: str, rows=None, cols=None):
+    """(address, dtype, rows, cols, row stride) of a 2-D device tensor, bfloat16
+    or float32, whose rows are contiguous; of the given shape where one is given."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch tensor")
+    dt = ZERO_BF16 if t.dtype is torch.bfloat16 else ZERO_F32 if t.dtype is torch.float32 else None
+    if dt is None:
+        raise TypeError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+    ptr, stride = _rows_of(t, what)
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the call runs on cuda:{dev}")
+    n, c = t.shape
+    if (rows is not None and n != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}; the call needs "
+                         f"({n if rows is None else rows}, {c if cols is None else cols})")
+    return ptr, dt, n, c, stride
+
+
+def zero_embedding(table, tokens, out, *, scale: float = 1.0, stream=None):
+    """Enqueue ``out[r] = scale * table[tokens[r]]``: ``table`` (vocab, hidden) and
+    ``out`` (rows, hidden) bfloat16 or float32 each, ``tokens`` int64 (rows,);
+    a negative token gives a row of zeros, one past the table a row of NaN."""
+    dev = _on_current_device(table, "table")
+    tp, tdt, v, h, ts = _matrix(table, dev, "table")
+    op, odt, n, _, os_ = _matrix(out, dev, "out", cols=h)
+    _check(_zero_embedding(tp, tdt, v, h, ts, _row_values(tokens, n, dev, "tokens", _torch().int64), n,
+                           scale, op, odt, os_, _stream_on(stream, dev)), "zero_embedding")
+
+
+def zero_embedding_grad_workspace_bytes(rows: int, vocab: int, hidden: int) -> int:
+    """Bytes of a workspace (a device tensor) that is enough for
+    zero_embedding_grad of these sizes."""
+    b = sz()
+    _check(_zero_embedding_grad_workspace_bytes(rows, vocab, hidden, C.byref(b)),
+           "zero_embedding_grad_workspace_bytes")
+    return b.value
+
+
+def zero_embedding_grad(d_out, tokens, d_table, *, scale: float = 1.0, accumulate: bool = False,
+                        workspace=None, stream=None):
+    """Enqueue the gradient of the table: ``d_table[v]`` = (with ``accumulate``
+    +=) scale times the sum of the ``d_out`` rows whose token is v.  ``d_table``
+    may be a parameter's place in a gradient bucket."""
+    dev = _on_current_device(d_out, "d_out")
+    gp, gdt, n, h, gs = _matrix(d_out, dev, "d_out")
+    tp, tdt, v, _, ts = _matrix(d_table, dev, "d_table", cols=h)
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_embedding_grad(gp, gdt, n, h, gs, _row_values(tokens, n, dev, "tokens", _torch().int64),
+                                scale, tp, tdt, v, ts, int(accumulate), wp, wb,
+                                _stream_on(stream, dev)), "zero_embedding_grad")
+
+
+# -- 8-bit activation checkpoints ---------------------------------------------------------------
+
+def _checkpoint(codes, scales, rows: int, cols: int, dev: int):
+    """Addresses of a checkpoint's codes and scales."""
+    u8 = _torch().uint8
+    blocks = (cols + ZERO_ACT8_BLOCK - 1) // ZERO_ACT8_BLOCK
+    for t, n, what in ((codes, cols, "codes"), (scales, blocks, "scales")):
+        if t.shape != (rows, n):
+            raise ValueError(f"{what} has shape {tuple(t.shape)}; the call needs ({rows}, {n})")
+    return (_row_values(codes, rows * cols, dev, "codes", u8),
+            _row_values(scales, rows * blocks, dev, "scales", u8))
+
+
+def zero_act8_pack(x, codes, scales, stream=None):
+    """Enqueue the packing of ``x`` (rows, cols), bfloat16 or float32, into
+    ``codes`` (rows, cols) and ``scales`` (rows, ceil(cols / ZERO_ACT8_BLOCK)),
+    both uint8."""
+    dev = _on_current_device(x, "x")
+    p, dt, n, c, st = _matrix(x, dev, "x")
+    cp, sp = _checkpoint(codes, scales, n, c, dev)
+    _check(_zero_act8_pack(p, dt, n, c, st, cp, sp, _stream_on(stream, dev)), "zero_act8_pack")
+
+
+def zero_act8_unpack(codes, scales, x, stream=None):
+    """Enqueue the values that a checkpoint stands for, rounded to x's type."""
+    dev = _on_current_device(x, "x")
+    p, dt, n, c, st = _matrix(x, dev, "x")
+    cp, sp = _checkpoint(codes, scales, n, c, dev)
+    _check(_zero_act8_unpack(cp, sp, n, c, p, dt, st, _stream_on(stream, dev)), "zero_act8_unpack")
+
+
+def zero_act8_weight_grad_workspace_bytes(rows: int, out_features: int, cols: int) -> int:
+    """Bytes of a workspace (a device tensor) that is enough for
+    zero_act8_weight_grad of these sizes."""
+    b = sz()
+    _check(_zero_act8_weight_grad_workspace_bytes(rows, out_features, cols, C.byref(b)),
+           "zero_act8_weight_grad_workspace_bytes")
+    return b.value
+
+
+def zero_act8_weight_grad(d_y, codes, scales, d_w, *, accumulate: bool = False, workspace=None,
+                          stream=None):
+    """Enqueue a weight's gradient ``d_w`` (out_features, cols) = (with
+    ``accumulate`` +=) ``d_y^T x'`` from ``d_y`` (rows, out_features) bfloat16
+    and the checkpoint of x (rows, cols).  ``d_w`` may be a parameter's place in a
+    gradient bucket."""
+    dev = _on_current_device(d_y, "d_y")
+    yp, ydt, n, o, ys = _matrix(d_y, dev, "d_y")
+    if ydt != ZERO_BF16:
+        raise TypeError(f"d_y must be bfloat16, got {d_y.dtype}")
+    wtp, wdt, _, c, ws = _matrix(d_w, dev, "d_w", rows=o)
+    cp, sp = _checkpoint(codes, scales, n, c, dev)
+    wp, wb = _workspace(workspace, dev)
+    _check(_zero_act8_weight_grad(yp, n, o, ys, cp, sp, c, wtp, wdt, ws, int(accumulate), wp, wb,
+                                  _stream_on(stream, dev)), "zero_act8_weight_grad")
 
 
 # -- sharded checkpoint ---------------------------------------------------------------------

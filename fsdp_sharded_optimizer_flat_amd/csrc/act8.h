@@ -1,0 +1,30 @@
+// act8.h -- what the entry points of the 8-bit activation checkpoints (act8.cpp)
+// hand to the kernels (act8_kernels.hip, act8_gemm_kernels.hip).  Not part of the
+// public ABI.
+#pragma once
+
+#include "zero_internal.h"
+
+namespace zero {
+
+constexpr int kActBlock = ZERO_ACT8_BLOCK;
+
+struct Act8Args {
+    void *x;                  // read by pack, written by unpack
+    uint8_t *codes, *scales;
+    int64_t rows, stride;
+    int32_t cols, blocks, dtype;
+};
+int launch_act8_pack(const Act8Args &a, void *stream);
+int launch_act8_unpack(const Act8Args &a, void *stream);
+
+struct Act8GradArgs {
+    const uint16_t *d_y;
+    const uint8_t *codes, *scales;
+    void *d_w;
+    int64_t rows, dy_stride, w_stride;
+    int32_t out, cols, blocks, w_dtype, accumulate;
+};
+int launch_act8_weight_grad(const Act8GradArgs &a, void *stream);
+
+}  // namespace zero

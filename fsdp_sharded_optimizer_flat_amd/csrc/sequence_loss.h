@@ -1,0 +1,39 @@
+// sequence_loss.h -- what the sequence-loss entry points (sequence_loss.cpp) hand
+// to the kernels (sequence_loss_kernels.hip).  Not part of the public ABI.
+#pragma once
+
+#include "zero_internal.h"
+
+namespace zero {
+
+// The packed sequences of a call.
+struct Sequences {
+    const int64_t *tokens;    // NULL: every position is a target
+    const int64_t *offsets;   // n + 1
+    int64_t n_tokens, n;
+    int32_t mode;
+};
+
+struct PolicyArgs {
+    Sequences seq;
+    const float *logprob, *old_logprob, *ref_logprob, *advantage, *d_loss;
+    int32_t per_token;
+    double low, high;             // 1 - clip_low, 1 + clip_high
+    double log_low, log_high;     // their logarithms
+    double kl_coef;
+    float *loss, *kl, *d_logprob;
+    int32_t *clipped;
+};
+int launch_policy_loss(const PolicyArgs &a, void *stream);
+
+struct PreferenceArgs {
+    Sequences seq;                // n = 2 pairs
+    const float *logprob, *ref_logprob, *d_loss;
+    int64_t pairs;
+    int32_t kind;
+    double beta, margin, smoothing;
+    float *loss, *reward, *d_logprob;
+};
+int launch_preference_loss(const PreferenceArgs &a, void *stream);
+
+}  // namespace zero

@@ -683,6 +683,185 @@ zero_status zero_distill_fused(const void *logits, int32_t dtype, int64_t rows, 
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Sequence losses -- from the log probabilities of given tokens (zero_logprob)
+ * to a loss over whole sequences and the d_logprob that zero_logprob_grad and
+ * zero_logprob_fused take.  n_tokens positions hold packed sequences: sequence b
+ * is offsets[b] .. offsets[b + 1] - 1.  A position is a target where tokens is
+ * NULL or its token is not negative (the padding rows of the token losses;
+ * prompts).  agg is the sum over a sequence's targets (ZERO_SEQUENCE_SUM) or
+ * their mean (ZERO_SEQUENCE_MEAN); of no targets it is 0.
+ *
+ *   clipped policy loss with a KL term, for a target with r = exp(logprob -
+ *   old_logprob), advantage A and x = ref_logprob - logprob:
+ *     term = max(-r A, -min(max(r, 1 - clip_low), 1 + clip_high) A)
+ *     k    = exp(x) - 1 - x                      (0 without ref_logprob)
+ *     loss = agg(term + kl_coef k), kl = agg(k) per sequence
+ *     clipped = the targets with r beyond the border (A > 0: above 1 + clip_high,
+ *               A < 0: below 1 - clip_low), whose term does not depend on r
+ *     d_logprob = d_loss w (-[not clipped] r A - kl_coef (exp(x) - 1)),
+ *               w = 1, or 1 / targets for the mean
+ *
+ *   preference loss of n_pairs pairs; pair p is sequence p (chosen) and n_pairs +
+ *   p (rejected):
+ *     s = agg(logprob - ref_logprob)             (agg(logprob) without)
+ *     reward = beta s;  h = reward_chosen - reward_rejected - margin
+ *     loss = (1 - smoothing) ln(1 + e^-h) + smoothing ln(1 + e^h)  ZERO_PREFER_SIGMOID
+ *            max(0, 1 - h)                                         ZERO_PREFER_HINGE
+ *            ((h - 1/2) / beta)^2                                  ZERO_PREFER_SQUARED
+ *     d_logprob = d_loss beta w loss'(h) for chosen targets, its negative for
+ *               rejected ones
+ *
+ * Terms and sums are binary64, in a fixed order; each output is rounded once
+ * (the gradient of a policy loss averaged over its targets may be rounded twice).
+ *
+ * Whatever a position that is no target holds, it adds nothing and its gradient
+ * is zero.  Positions of no sequence (before offsets[0], from offsets[n_seqs]
+ * on) keep what d_logprob holds there.  NaN among a sequence's targets makes its
+ * loss and their gradients NaN, which makes zero_step_device_clip skip its step;
+ * x = +inf (a target of probability zero) makes k infinite.  A d_loss of 0 gives
+ * gradients of 0 where the slope is finite.  Offsets are clamped to 0 ..
+ * n_tokens; they must not decrease (where they do, nothing outside the arrays is
+ * touched, but what the outputs hold is not defined).
+ *
+ * All pointers are device pointers, aligned to their elements.  Outputs must
+ * not overlap each other or an input.  Async on `stream`; nothing is allocated and
+ * the calls can be captured in a graph.  A workspace serves one call at a time.
+ * Errors: EINVAL (NULL, negative sizes, bad enum, a coefficient out of its range,
+ * overlapping buffers, no output), ERANGE (n_tokens > ZERO_MAX_LOSS_ROWS, more
+ * than ZERO_MAX_SEQUENCES sequences), EALIGN, ENOSPC, EHIP.  No sequences: nothing
+ * is done.
+ * ------------------------------------------------------------------------ */
+#define ZERO_MAX_SEQUENCES (1 << 20)
+#define ZERO_SEQUENCE_MEAN 0
+#define ZERO_SEQUENCE_SUM 1
+#define ZERO_PREFER_SIGMOID 0
+#define ZERO_PREFER_HINGE 1
+#define ZERO_PREFER_SQUARED 2
+
+/* Workspace bytes that are enough for either call below on n_tokens positions
+ * of n_seqs sequences (16-byte aligned device memory; where this is 0 a NULL
+ * workspace). */
+zero_status zero_sequence_loss_workspace_bytes(int64_t n_tokens, int64_t n_seqs, size_t *bytes);
+
+/* advantage: one value per position (per_token nonzero, [n_tokens]) or per
+ * sequence ([n_seqs]).  ref_logprob may be NULL (then kl is NULL and kl_coef 0).
+ * loss, kl, clipped [n_seqs] and d_logprob [n_tokens] may be NULL, not all of
+ * them; d_logprob needs d_loss [n_seqs].  0 <= clip_low <= 1, 0 <= clip_high,
+ * which may be infinite, 0 <= kl_coef. */
+zero_status zero_policy_loss(const float *logprob, const float *old_logprob,
+                             const float *ref_logprob, const float *advantage, int32_t per_token,
+                             const int64_t *tokens, int64_t n_tokens, const int64_t *offsets,
+                             int64_t n_seqs, double clip_low, double clip_high, double kl_coef,
+                             int32_t mode, const float *d_loss, float *loss, float *kl,
+                             int32_t *clipped, float *d_logprob, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* offsets: 2 n_pairs + 1.  loss [n_pairs], reward [2 n_pairs] and d_logprob
+ * [n_tokens] may be NULL, not all of them; d_logprob needs d_loss [n_pairs].
+ * beta > 0, margin finite, 0 <= smoothing <= 1 (0 unless ZERO_PREFER_SIGMOID). */
+zero_status zero_preference_loss(const float *logprob, const float *ref_logprob,
+                                 const int64_t *tokens, int64_t n_tokens, const int64_t *offsets,
+                                 int64_t n_pairs, int32_t kind, double beta, double margin,
+                                 double smoothing, int32_t mode, const float *d_loss, float *loss,
+                                 float *reward, float *d_logprob, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Embedding -- where a forward pass starts and a backward pass ends: the rows of
+ * a table that tokens name, and the gradient of that table, which is written to
+ * (or added onto) its place in the unit's gradient bucket.
+ *
+ *     out_r = scale table[token_r]
+ *     d_table[v] (+)= scale sum_{r: token_r = v} d_out_r     in ascending order of r
+ *
+ * A negative token is a padding row: its out row is zero, its d_out row is not
+ * read.  A token >= vocab gives a NaN out row (as in the token losses, so that the
+ * step of a bad batch is skipped) and adds nothing to the gradient.
+ *
+ * Tables and activations are ZERO_F32 or ZERO_BF16 each, in rows of `hidden`
+ * elements, row r at base + r * stride; elements past a row's hidden stay as they
+ * are.  Sums are binary32, in an order that the sizes alone decide (the same call
+ * gives the same bits); each output is rounded once.  accumulate = 0 writes the
+ * whole of d_table, zeros where no token names a row; accumulate = 1 adds to the
+ * rows that tokens name (one more rounding) and leaves the others as they are.
+ *
+ * Device pointers, aligned to their elements; outputs must not overlap inputs.
+ * Async on `stream`, no allocation, capturable; a workspace serves one call at a
+ * time.  Errors: EINVAL, ERANGE (vocab > ZERO_MAX_VOCAB, hidden >
+ * ZERO_MAX_HIDDEN, rows > ZERO_MAX_EMBEDDING_ROWS for the gradient,
+ * ZERO_MAX_LOSS_ROWS for the lookup, a scale that is not finite is EINVAL),
+ * EALIGN, ENOSPC, EHIP.  No rows: the lookup does nothing, the gradient is zero.
+ * ------------------------------------------------------------------------ */
+#define ZERO_MAX_HIDDEN (1 << 20)
+#define ZERO_MAX_EMBEDDING_ROWS (1 << 20)   /* of one gradient call; accumulate over more */
+
+zero_status zero_embedding(const void *table, int32_t dtype, int64_t vocab, int64_t hidden,
+                           int64_t row_stride, const int64_t *tokens, int64_t rows, float scale,
+                           void *out, int32_t out_dtype, int64_t out_stride, void *stream);
+
+/* Workspace bytes that are enough for the gradient call of these sizes (16-byte
+ * aligned device memory). */
+zero_status zero_embedding_grad_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden,
+                                                size_t *bytes);
+
+zero_status zero_embedding_grad(const void *d_out, int32_t dtype, int64_t rows, int64_t hidden,
+                                int64_t row_stride, const int64_t *tokens, float scale,
+                                void *d_table, int32_t table_dtype, int64_t vocab,
+                                int64_t table_stride, int32_t accumulate, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit activation checkpoints -- what a layer's forward pass keeps for its
+ * backward pass, in 8.25 bits an element: [p4 section 3] leaves activations
+ * beside the model state, and what a backward pass forms from them is a unit's
+ * weight gradient, in its bucket.
+ *
+ * Each row of `cols` elements is cut into blocks of ZERO_ACT8_BLOCK (the last may be
+ * shorter).  A block's scale is the least power of two s = 2^e, e >= -127, with
+ * max |x| <= 448 s over its finite elements (2^-127 where there are none), kept as
+ * the byte e + 127; an element is kept as x / s rounded to e4m3 (four significant
+ * bits, ties to even, steps of 2^-9 below 2^-6; no infinities), as one byte.  A NaN
+ * or an infinity is kept as NaN (0x7f).  codes: rows x cols bytes, scales: rows x
+ * ceil(cols / ZERO_ACT8_BLOCK) bytes, both without gaps.  A scale byte of 255 makes
+ * its block NaN.
+ *
+ *   zero_act8_pack          x -> codes, scales
+ *   zero_act8_unpack        x' = code * scale, rounded to the output's type
+ *   zero_act8_weight_grad   d_w[o][c] (+)= sum_r d_y[r][o] x'[r][c]
+ *
+ * The weight gradient's factors d_y (bf16) and x' (exact in bf16, but for elements
+ * below its normal range) are multiplied on the matrix cores, sums are binary32 in an
+ * order that the sizes alone decide; each element of d_w [out_features][cols] is
+ * rounded once to its type, or, with accumulate = 1, added to what is there (one
+ * more rounding).
+ *
+ * x and d_w are ZERO_F32 or ZERO_BF16.  Device pointers, aligned to their elements;
+ * outputs must not overlap inputs or each other.  Async on `stream`, no allocation,
+ * capturable; a workspace serves one call at a time.  Errors: EINVAL, ERANGE (rows >
+ * ZERO_MAX_LOSS_ROWS, cols or out_features > ZERO_MAX_HIDDEN), EALIGN, ENOSPC, EHIP.
+ * No rows: pack and unpack do nothing, the weight gradient is zero.
+ * ------------------------------------------------------------------------ */
+#define ZERO_ACT8_BLOCK 32
+
+zero_status zero_act8_pack(const void *x, int32_t dtype, int64_t rows, int64_t cols,
+                           int64_t row_stride, uint8_t *codes, uint8_t *scales, void *stream);
+
+zero_status zero_act8_unpack(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                             int64_t cols, void *x, int32_t dtype, int64_t row_stride,
+                             void *stream);
+
+/* Workspace bytes that are enough for the weight gradient of these sizes
+ * (16-byte aligned device memory; where this is 0 a NULL workspace). */
+zero_status zero_act8_weight_grad_workspace_bytes(int64_t rows, int64_t out_features,
+                                                  int64_t cols, size_t *bytes);
+
+zero_status zero_act8_weight_grad(const uint16_t *d_y, int64_t rows, int64_t out_features,
+                                  int64_t dy_stride, const uint8_t *codes, const uint8_t *scales,
+                                  int64_t cols, void *d_w, int32_t w_dtype, int64_t w_stride,
+                                  int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* ------------------------------------------------------------------------
  * Sharded checkpoint -- [p1 Implementation notes]: each rank writes its own
  * shard of the checkpoint, and a checkpoint saved at one N is resharded to a
  * different N when it is loaded; [p4 section 5, FSDP1 vs FSDP2]: the state
