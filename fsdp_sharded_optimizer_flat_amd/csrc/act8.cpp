@@ -75,6 +75,11 @@ zero_status check_grad_sizes(int64_t rows, int64_t out_features, int64_t cols)
         return ZERO_EINVAL;
     return out_features > ZERO_MAX_HIDDEN ? ZERO_ERANGE : ZERO_OK;
 }
+int64_t whole_quads(int64_t cols) { return (cols + 3) / 4 * 4; }
+int64_t parts_bytes(const Act8Split &s, int64_t out, int64_t cols)
+{
+    return s.splits > 1 ? s.splits * out * whole_quads(cols) * 4 : 0;
+}
 }  // namespace
 
 extern "C" zero_status zero_act8_weight_grad_workspace_bytes(int64_t rows, int64_t out_features,
@@ -84,7 +89,7 @@ extern "C" zero_status zero_act8_weight_grad_workspace_bytes(int64_t rows, int64
         return ZERO_EINVAL;
     if (zero_status s = check_grad_sizes(rows, out_features, cols))
         return s;
-    *bytes = 0;
+    *bytes = (size_t)parts_bytes(act8_split(rows, out_features, cols), out_features, cols);
     return ZERO_OK;
 }
 
@@ -104,11 +109,18 @@ extern "C" zero_status zero_act8_weight_grad(const uint16_t *d_y, int64_t rows,
     if (!stride_fits(rows, dy_stride) || !stride_fits(out_features, w_stride))
         return ZERO_ERANGE;
     const int64_t blocks = blocks_of(cols);
+    const Act8Split split = act8_split(rows, out_features, cols);
+    const int64_t need = parts_bytes(split, out_features, cols);
+    if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, need))
+        return s;
     const Span in[] = {matrix(d_y, rows, out_features, dy_stride, 2), vec(codes, rows * cols, 1),
                        vec(scales, rows * blocks, 1)};
-    const Span out[] = {matrix(d_w, out_features, cols, w_stride, esize(w_dtype))};
-    if (zero_status s = check_spans(in, 3, out, 1))
+    const Span out[] = {matrix(d_w, out_features, cols, w_stride, esize(w_dtype)),
+                        {need ? workspace : nullptr, need, 16}};
+    if (zero_status s = check_spans(in, 3, out, 2))
         return s;
+    if (rows == 0 && accumulate)
+        return ZERO_OK;
     Act8GradArgs a{};
     a.d_y = d_y;
     a.codes = codes;
@@ -122,5 +134,9 @@ extern "C" zero_status zero_act8_weight_grad(const uint16_t *d_y, int64_t rows,
     a.blocks = (int32_t)blocks;
     a.w_dtype = w_dtype;
     a.accumulate = accumulate;
+    a.tile = split.tile;
+    a.splits = split.splits;
+    a.columns = (int32_t)whole_quads(cols);
+    a.parts = static_cast<float *>(workspace);
     return done(launch_act8_weight_grad(a, stream), "zero_act8_weight_grad");
 }

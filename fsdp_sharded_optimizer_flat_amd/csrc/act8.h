@@ -24,7 +24,14 @@ struct Act8GradArgs {
     void *d_w;
     int64_t rows, dy_stride, w_stride;
     int32_t out, cols, blocks, w_dtype, accumulate;
+    int32_t tile, splits;     // d_w's tiles; workgroups that share a tile's rows
+    int32_t columns;          // of the parts: cols rounded up to whole quads
+    float *parts;             // splits x out x columns, where splits > 1
 };
+struct Act8Split {
+    int32_t tile, splits;
+};
+Act8Split act8_split(int64_t rows, int64_t out, int64_t cols);
 int launch_act8_weight_grad(const Act8GradArgs &a, void *stream);
 
 }  // namespace zero

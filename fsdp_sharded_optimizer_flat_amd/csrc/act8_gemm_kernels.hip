@@ -1,5 +1,17 @@
 // act8_gemm_kernels.hip -- a weight's gradient from an 8-bit activation checkpoint:
 // d_w[o][c] = sum_r d_y[r][o] x'[r][c] on the matrix cores.
+//
+// Both factors lie in memory by rows r, the index summed over, so a lane of a
+// matrix instruction needs eight of one column: tiles go to LDS as they lie (codes
+// widened to bf16 on the way, one instruction for two codes and their scale, exact)
+// and come back transposed (ds_read_b64_tr_b16: 16 lanes read four rows of 16
+// columns, each gets a column).  Rows of a tile are cut into pairs of 16-byte
+// chunks, pair p of row r at place p ^ (r & 7), so that the rows that one read
+// touches lie in different banks.  Which of a step's 32 rows a lane holds is the
+// same for both factors and otherwise free: lanes 16 g .. 16 g + 15 hold rows 4 g ..
+// 4 g + 3 and 16 more.
+#include <algorithm>
+
 #include "act8_device.h"
 
 namespace zero {
@@ -8,68 +20,244 @@ namespace {
 using namespace dev;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
+typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kTileO = 128, kTileC = 128, kTileR = 32;
+constexpr int kRows = 64;   // rows r of a tile
 
-// A workgroup of four waves per 128 x 128 tile of d_w; a wave forms 64 x 64 of it
-// from 16 x 16 x 32 products, the columns as the product's rows, so that a lane
-// holds four neighbouring columns.
-template <typename O>
-__global__ __launch_bounds__(256) void weight_grad_kernel(Act8GradArgs a)
+__device__ __forceinline__ unsigned widen_pair(unsigned w, float s, bool high)
 {
-    __shared__ uint16_t xs[kTileR][kTileC], ys[kTileR][kTileO];
+    return __builtin_bit_cast(unsigned, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+}
+
+// 16 bytes at p, of which n are within the array.
+__device__ __forceinline__ u32x4 load_within(const uint8_t *p, int64_t n)
+{
+    if (n >= 16)
+        return *reinterpret_cast<const u32x4_at1 *>(p);
+    unsigned w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n)
+            w[i / 4] |= (unsigned)p[i] << (8 * (i % 4));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// A workgroup of four waves per B x B tile of d_w, a wave per quarter.  FAST: rows
+// of both factors are whole 16-byte chunks at 16-byte addresses.
+template <int B, bool FAST, typename O>
+__global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
+{
+    constexpr int N = B / 32;                    // 16 x 16 products of a wave, by rows and by columns
+    constexpr int RowBytes = B * 2, Pairs = B / 16;
+    constexpr int XPer = kRows * Pairs / 256, YPer = 2 * XPer;
+    constexpr int Bytes = kRows * RowBytes;
+    __shared__ __attribute__((aligned(16))) char sh[4 * Bytes];   // x', d_y; two tiles each
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int c0 = blockIdx.x * kTileC, o0 = blockIdx.y * kTileO;
-    const int wc = wave % 2 * 64, wo = wave / 2 * 64;
-    f32x4 acc[4][4] = {};   // [column tile][out tile]
-    for (int64_t r0 = 0; r0 < a.rows; r0 += kTileR) {
-        for (int i = tid; i < kTileR * kTileC; i += 256) {
-            const int r = i / kTileC, k = i % kTileC;
-            const int64_t row = r0 + r;
-            const int c = c0 + k, o = o0 + k;
-            float x = 0.0f;
-            if (row < a.rows && c < a.cols) {
-                float f[4];
-                widen_codes(a.codes[row * a.cols + c],
-                            scale_of(a.scales[row * a.blocks + c / kActBlock]), f);
-                x = f[0];
+    const int c0 = blockIdx.x * B, o0 = blockIdx.y * B;
+    const int tiles = (int)((a.rows + kRows - 1) / kRows);
+    const int per = (tiles + a.splits - 1) / a.splits;
+    const int first = blockIdx.z * per, n = min(per, tiles - first);
+
+    u32x4 xr[XPer], yr[YPer];
+    unsigned sr[XPer];
+    auto load = [&](int t) {
+        const int64_t r0 = (int64_t)(first + t) * kRows;
+        const uint8_t *xb = a.codes + r0 * a.cols + c0, *sb = a.scales + r0 * a.blocks + c0 / kActBlock;
+        const uint8_t *yb = reinterpret_cast<const uint8_t *>(a.d_y + r0 * a.dy_stride + o0);
+        const int64_t left = a.rows - r0;   // >= 1
+        if constexpr (FAST) {
+            const int64_t most = 0x7fffffff;
+            auto window = [&](const uint8_t *p, int64_t bytes) {
+                return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)min(bytes, most),
+                                                         kRawBufferWord3);
+            };
+            const auto xw = window(xb, left * a.cols - c0), sw = window(sb, left * a.blocks - c0 / kActBlock);
+            const auto yw = window(yb, ((left - 1) * a.dy_stride + a.out - o0) * 2);
+#pragma unroll
+            for (int i = 0; i < XPer; ++i) {
+                const int k = tid + i * 256, r = k / Pairs, p = k % Pairs;
+                xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xw, r * a.cols + p * 16, 0, 0));
+                sr[i] = __builtin_amdgcn_raw_buffer_load_b8(sw, r * a.blocks + p / 2, 0, 0);
             }
-            xs[r][k] = to_bf16(x);
-            ys[r][k] = row < a.rows && o < a.out ? a.d_y[row * a.dy_stride + o] : 0;
+#pragma unroll
+            for (int i = 0; i < YPer; ++i) {
+                const int k = tid + i * 256, r = k / (2 * Pairs), p = k % (2 * Pairs);
+                yr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      yw, (r * (int)a.dy_stride + p * 8) * 2, 0, 0));
+            }
+        } else {
+            // columns past a row's end may hold the next row's: they reach no output
+#pragma unroll
+            for (int i = 0; i < XPer; ++i) {
+                const int k = tid + i * 256, r = k / Pairs, p = k % Pairs;
+                const int64_t at = (int64_t)r * a.cols + p * 16, sat = (int64_t)r * a.blocks + p / 2;
+                xr[i] = load_within(xb + at, r < left ? left * a.cols - c0 - at : 0);
+                sr[i] = r < left && sat < left * a.blocks - c0 / kActBlock ? sb[sat] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < YPer; ++i) {
+                const int k = tid + i * 256, r = k / (2 * Pairs), p = k % (2 * Pairs);
+                const int64_t at = (r * a.dy_stride + p * 8) * 2;
+                yr[i] = load_within(yb + at, r < left ? ((left - 1) * a.dy_stride + a.out - o0) * 2 - at : 0);
+            }
         }
-        __syncthreads();
-        bf16x8 x[4], y[4];
-        for (int t = 0; t < 4; ++t)
-            for (int j = 0; j < 8; ++j) {
-                x[t][j] = __builtin_bit_cast(__bf16, xs[lane / 16 * 8 + j][wc + t * 16 + lane % 16]);
-                y[t][j] = __builtin_bit_cast(__bf16, ys[lane / 16 * 8 + j][wo + t * 16 + lane % 16]);
-            }
-        for (int s = 0; s < 4; ++s)
-            for (int t = 0; t < 4; ++t)
-                acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[s], y[t], acc[s][t], 0, 0, 0);
-        __syncthreads();
+    };
+    auto place = [&](int r, int chunk) { return r * RowBytes + ((chunk / 2 ^ (r & 7)) * 32) + chunk % 2 * 16; };
+    auto store = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < XPer; ++i) {
+            const int k = tid + i * 256, r = k / Pairs, p = k % Pairs;
+            const float s = __uint_as_float(sr[i] << 23);
+            const unsigned w[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
+            unsigned v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = widen_pair(w[j / 2], s, j % 2);
+            char *q = sh + buf * Bytes;
+            *reinterpret_cast<u32x4 *>(q + place(r, 2 * p)) = u32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<u32x4 *>(q + place(r, 2 * p + 1)) = u32x4{v[4], v[5], v[6], v[7]};
+        }
+#pragma unroll
+        for (int i = 0; i < YPer; ++i) {
+            const int k = tid + i * 256, r = k / (2 * Pairs), p = k % (2 * Pairs);
+            *reinterpret_cast<u32x4 *>(sh + (2 + buf) * Bytes + place(r, p)) = yr[i];
+        }
+    };
+    // where a lane reads in a tile: its row of the first four, and product t's columns
+    const int row = lane / 16 * 4 + lane % 16 / 4;
+    int xat[N], yat[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        xat[t] = row * RowBytes + (((wave % 2 * N + t) ^ (row & 7)) * 32) + lane % 4 * 8;
+        yat[t] = row * RowBytes + (((wave / 2 * N + t) ^ (row & 7)) * 32) + lane % 4 * 8;
     }
-    for (int s = 0; s < 4; ++s)
-        for (int t = 0; t < 4; ++t)
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + wc + s * 16 + lane / 16 * 4 + j, o = o0 + wo + t * 16 + lane % 16;
-                if (c < a.cols && o < a.out) {
-                    O *p = static_cast<O *>(a.d_w) + (int64_t)o * a.w_stride + c;
-                    *p = narrow<O>(a.accumulate ? widen<O>(*p) + acc[s][t][j] : acc[s][t][j]);
-                }
+    auto column = [&](int at) {
+        typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+        union {
+            i16x4 h[2];
+            bf16x8 v;
+        } u;
+        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)((lds_char *)sh + at));
+        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)((lds_char *)sh + at + 16 * RowBytes));
+        return u.v;
+    };
+    struct Step {
+        bf16x8 x[N], y[N];
+    };
+    auto read = [&](int buf, int half, Step &s) {
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+            s.y[t] = column((2 + buf) * Bytes + half * 32 * RowBytes + yat[t]);
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+            s.x[t] = column(buf * Bytes + half * 32 * RowBytes + xat[t]);
+    };
+    f32x4 acc[N][N] = {};   // [columns][out]
+    auto multiply = [&](const Step &s) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s.x[i], s.y[j], acc[i][j], 0, 0, 0);
+    };
+    if (n > 0) {
+        Step s0, s1;
+        load(0);
+        store(0);
+        if (n > 1)
+            load(1);
+        __syncthreads();
+        read(0, 0, s0);
+        for (int t = 0; t < n; ++t) {
+            const int buf = t & 1;
+            read(buf, 1, s1);
+            multiply(s0);
+            if (t + 1 < n)
+                store(buf ^ 1);
+            __syncthreads();
+            if (t + 2 < n)
+                load(t + 2);
+            if (t + 1 < n)
+                read(buf ^ 1, 0, s0);
+            multiply(s1);
+        }
+    }
+    // a lane holds four neighbouring columns of a row of d_w
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int c = c0 + wave % 2 * (B / 2) + i * 16 + lane / 16 * 4;
+            const int o = o0 + wave / 2 * (B / 2) + j * 16 + lane % 16;
+            if (o >= a.out || c >= a.cols)
+                continue;
+            const int m = min(a.cols - c, 4);
+            float v[4] = {acc[i][j].x, acc[i][j].y, acc[i][j].z, acc[i][j].w};
+            if (a.splits > 1) {
+                float *p = a.parts + ((int64_t)blockIdx.z * a.out + o) * a.columns + c;
+                *reinterpret_cast<f32x4 *>(p) = acc[i][j];
+                continue;
             }
+            put4(static_cast<O *>(a.d_w) + (int64_t)o * a.w_stride + c, m, v, a.accumulate);
+        }
+}
+
+// The parts of each element added in order; four columns to a thread.
+template <typename O>
+__global__ __launch_bounds__(kBlock) void join_splits_kernel(Act8GradArgs a)
+{
+    const int quads = a.columns / 4;
+    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    if (i >= (int64_t)quads * a.out)
+        return;
+    const int o = (int)(i / quads), c = (int)(i - (int64_t)o * quads) * 4;
+    f32x4 sum = {};
+    for (int s = 0; s < a.splits; ++s)
+        sum += *reinterpret_cast<const f32x4 *>(a.parts + ((int64_t)s * a.out + o) * a.columns + c);
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+    put4(static_cast<O *>(a.d_w) + (int64_t)o * a.w_stride + c, min(a.cols - c, 4), v, a.accumulate);
+}
+
+template <int B, typename O>
+void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
+{
+    const dim3 grid((a.cols + B - 1) / B, (a.out + B - 1) / B, a.splits);
+    const bool fast = a.out % 8 == 0 && a.dy_stride % 8 == 0 && a.dy_stride < 1 << 23 && a.cols % 16 == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.d_y) | reinterpret_cast<uintptr_t>(a.codes)) % 16 == 0;
+    if (fast)
+        hipLaunchKernelGGL((weight_grad_kernel<B, true, O>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((weight_grad_kernel<B, false, O>), grid, dim3(256), 0, st, a);
+    if (a.splits > 1)
+        hipLaunchKernelGGL((join_splits_kernel<O>), dim3((unsigned)(((int64_t)a.columns / 4 * a.out + kBlock - 1) / kBlock)),
+                           dim3(kBlock), 0, st, a);
 }
 
 }  // namespace
 
+Act8Split act8_split(int64_t rows, int64_t out, int64_t cols)
+{
+    auto tiles = [&](int64_t b) { return ((out + b - 1) / b) * ((cols + b - 1) / b); };
+    if (tiles(256) >= 160)
+        return {256, 1};
+    const int64_t steps = (rows + kRows - 1) / kRows;
+    const int64_t want = (512 + tiles(128) - 1) / tiles(128);
+    const int64_t s = std::max<int64_t>(1, std::min(want, steps / 4));
+    return {128, (int32_t)s};
+}
+
 int launch_act8_weight_grad(const Act8GradArgs &a, void *stream)
 {
-    const dim3 grid((a.cols + kTileC - 1) / kTileC, (a.out + kTileO - 1) / kTileO);
-    if (a.w_dtype == ZERO_F32)
-        hipLaunchKernelGGL((weight_grad_kernel<float>), grid, dim3(256), 0, reinterpret_cast<hipStream_t>(stream), a);
-    else
-        hipLaunchKernelGGL((weight_grad_kernel<uint16_t>), grid, dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                           a);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    by_types(ZERO_F32, a.w_dtype, [&](auto, auto o) {
+        if (a.tile == 256)
+            weight_grad_of<256, decltype(o)>(a, st);
+        else
+            weight_grad_of<128, decltype(o)>(a, st);
+    });
     return hipGetLastError();
 }
 
