@@ -61,128 +61,157 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     const int per = (tiles + a.splits - 1) / a.splits;
     const int first = blockIdx.z * per, n = min(per, tiles - first);
 
+    // A tile on its way: chunk i of x' and of d_y in registers.  Rows behind the last
+    // are zeros; columns past a row's end may hold the next row's, which reach no
+    // output.
     u32x4 xr[XPer], yr[YPer];
     unsigned sr[XPer];
-    auto load = [&](int t) {
+    struct Source {
+        const uint8_t *x, *s, *y;
+        int64_t left;                        // rows from the tile's first on; <= 0: none
+        __amdgpu_buffer_rsrc_t xw, sw, yw;   // FAST: bounded to the arrays
+    };
+    auto source = [&](int t) {
+        Source f;
         const int64_t r0 = (int64_t)(first + t) * kRows;
-        const uint8_t *xb = a.codes + r0 * a.cols + c0, *sb = a.scales + r0 * a.blocks + c0 / kActBlock;
-        const uint8_t *yb = reinterpret_cast<const uint8_t *>(a.d_y + r0 * a.dy_stride + o0);
-        const int64_t left = a.rows - r0;   // >= 1
+        f.left = a.rows - r0;
+        f.x = a.codes + r0 * a.cols + c0;
+        f.s = a.scales + r0 * a.blocks + c0 / kActBlock;
+        f.y = reinterpret_cast<const uint8_t *>(a.d_y + r0 * a.dy_stride + o0);
         if constexpr (FAST) {
-            const int64_t most = 0x7fffffff;
             auto window = [&](const uint8_t *p, int64_t bytes) {
-                return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)min(bytes, most),
-                                                         kRawBufferWord3);
+                const int64_t n = f.left > 0 ? min(max(bytes, int64_t(0)), int64_t(0x7fffffff)) : 0;
+                return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)n, kRawBufferWord3);
             };
-            const auto xw = window(xb, left * a.cols - c0), sw = window(sb, left * a.blocks - c0 / kActBlock);
-            const auto yw = window(yb, ((left - 1) * a.dy_stride + a.out - o0) * 2);
-#pragma unroll
-            for (int i = 0; i < XPer; ++i) {
-                const int k = tid + i * 256, r = k / Pairs, p = k % Pairs;
-                xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xw, r * a.cols + p * 16, 0, 0));
-                sr[i] = __builtin_amdgcn_raw_buffer_load_b8(sw, r * a.blocks + p / 2, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < YPer; ++i) {
-                const int k = tid + i * 256, r = k / (2 * Pairs), p = k % (2 * Pairs);
-                yr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                      yw, (r * (int)a.dy_stride + p * 8) * 2, 0, 0));
-            }
+            f.xw = window(f.x, f.left * a.cols - c0);
+            f.sw = window(f.s, f.left * a.blocks - c0 / kActBlock);
+            f.yw = window(f.y, ((f.left - 1) * a.dy_stride + a.out - o0) * 2);
+        }
+        return f;
+    };
+    // Chunk i of a thread: XRows i (YRows i) rows below its first.
+    constexpr int XRows = 256 / Pairs, YRows = 128 / Pairs;
+    const int xrow = tid / Pairs, xpair = tid % Pairs, yrow = tid / (2 * Pairs), yoct = tid % (2 * Pairs);
+    const int xoff = xrow * a.cols + xpair * 16, soff = xrow * a.blocks + xpair / 2;
+    const int yoff = (yrow * (int)a.dy_stride + yoct * 8) * 2;   // used where FAST, which bounds the stride
+    auto load_x = [&](const Source &f, int i) {
+        if constexpr (FAST) {
+            xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.xw, xoff, i * XRows * a.cols, 0));
+            sr[i] = __builtin_amdgcn_raw_buffer_load_b8(f.sw, soff, i * XRows * a.blocks, 0);
         } else {
-            // columns past a row's end may hold the next row's: they reach no output
-#pragma unroll
-            for (int i = 0; i < XPer; ++i) {
-                const int k = tid + i * 256, r = k / Pairs, p = k % Pairs;
-                const int64_t at = (int64_t)r * a.cols + p * 16, sat = (int64_t)r * a.blocks + p / 2;
-                xr[i] = load_within(xb + at, r < left ? left * a.cols - c0 - at : 0);
-                sr[i] = r < left && sat < left * a.blocks - c0 / kActBlock ? sb[sat] : 0;
-            }
-#pragma unroll
-            for (int i = 0; i < YPer; ++i) {
-                const int k = tid + i * 256, r = k / (2 * Pairs), p = k % (2 * Pairs);
-                const int64_t at = (r * a.dy_stride + p * 8) * 2;
-                yr[i] = load_within(yb + at, r < left ? ((left - 1) * a.dy_stride + a.out - o0) * 2 - at : 0);
-            }
+            const int r = xrow + i * XRows;
+            const int64_t at = (int64_t)r * a.cols + xpair * 16, sat = (int64_t)r * a.blocks + xpair / 2;
+            xr[i] = load_within(f.x + at, r < f.left ? f.left * a.cols - c0 - at : 0);
+            sr[i] = r < f.left && sat < f.left * a.blocks - c0 / kActBlock ? f.s[sat] : 0;
         }
     };
-    auto place = [&](int r, int chunk) { return r * RowBytes + ((chunk / 2 ^ (r & 7)) * 32) + chunk % 2 * 16; };
-    auto store = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < XPer; ++i) {
-            const int k = tid + i * 256, r = k / Pairs, p = k % Pairs;
-            const float s = __uint_as_float(sr[i] << 23);
-            const unsigned w[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
-            unsigned v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = widen_pair(w[j / 2], s, j % 2);
-            char *q = sh + buf * Bytes;
-            *reinterpret_cast<u32x4 *>(q + place(r, 2 * p)) = u32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<u32x4 *>(q + place(r, 2 * p + 1)) = u32x4{v[4], v[5], v[6], v[7]};
-        }
-#pragma unroll
-        for (int i = 0; i < YPer; ++i) {
-            const int k = tid + i * 256, r = k / (2 * Pairs), p = k % (2 * Pairs);
-            *reinterpret_cast<u32x4 *>(sh + (2 + buf) * Bytes + place(r, p)) = yr[i];
+    auto load_y = [&](const Source &f, int i) {
+        if constexpr (FAST) {
+            yr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  f.yw, yoff, i * YRows * (int)a.dy_stride * 2, 0));
+        } else {
+            const int r = yrow + i * YRows;
+            const int64_t at = (r * a.dy_stride + yoct * 8) * 2;
+            yr[i] = load_within(f.y + at, r < f.left ? ((f.left - 1) * a.dy_stride + a.out - o0) * 2 - at : 0);
         }
     };
-    // where a lane reads in a tile: its row of the first four, and product t's columns
+    // Where a thread's first chunks go in a tile (the rows below are multiples of 8
+    // further, so their places differ by whole rows), where a lane reads: its row of the
+    // first four and product 0's columns, product t's being this ^ 32 t.  All change to
+    // the other tile by ^ Bytes.
+    static_assert(XRows % 8 == 0 && YRows % 8 == 0, "");
+    int xto = xrow * RowBytes + ((xpair ^ (xrow & 7)) * 32);
+    int yto = 2 * Bytes + yrow * RowBytes + ((yoct / 2 ^ (yrow & 7)) * 32) + yoct % 2 * 16;
     const int row = lane / 16 * 4 + lane % 16 / 4;
-    int xat[N], yat[N];
+    int xat = row * RowBytes + ((wave % 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
+    int yat = 2 * Bytes + row * RowBytes + ((wave / 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
+    auto store_x = [&](int i) {
+        const float s = __uint_as_float(sr[i] << 23);
+        const unsigned w[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
+        unsigned v[8];
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-        xat[t] = row * RowBytes + (((wave % 2 * N + t) ^ (row & 7)) * 32) + lane % 4 * 8;
-        yat[t] = row * RowBytes + (((wave / 2 * N + t) ^ (row & 7)) * 32) + lane % 4 * 8;
-    }
-    auto column = [&](int at) {
+        for (int j = 0; j < 8; ++j)
+            v[j] = widen_pair(w[j / 2], s, j % 2);
+        u32x4 *q = reinterpret_cast<u32x4 *>(sh + xto + i * XRows * RowBytes);
+        q[0] = u32x4{v[0], v[1], v[2], v[3]};
+        q[1] = u32x4{v[4], v[5], v[6], v[7]};
+    };
+    auto store_y = [&](int i) { *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[i]; };
+    auto column = [&](int at, int t, int half) {
         typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
         union {
             i16x4 h[2];
             bf16x8 v;
         } u;
-        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)((lds_char *)sh + at));
-        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)((lds_char *)sh + at + 16 * RowBytes));
+        lds_char *p = (lds_char *)sh + (at ^ t * 32);
+        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + half * 32 * RowBytes));
+        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + (half * 32 + 16) * RowBytes));
         return u.v;
     };
-    struct Step {
-        bf16x8 x[N], y[N];
-    };
-    auto read = [&](int buf, int half, Step &s) {
-#pragma unroll
-        for (int t = 0; t < N; ++t)
-            s.y[t] = column((2 + buf) * Bytes + half * 32 * RowBytes + yat[t]);
-#pragma unroll
-        for (int t = 0; t < N; ++t)
-            s.x[t] = column(buf * Bytes + half * 32 * RowBytes + xat[t]);
-    };
+    // A tile's products in 2 N groups: group g = half N + i multiplies columns i of
+    // that half's rows with all of d_y's.  x' is read kAhead groups before, a half's d_y
+    // during the half before.
+    constexpr int kGroups = 2 * N, kAhead = 3;
+    bf16x8 x[4], y[2][N];
     f32x4 acc[N][N] = {};   // [columns][out]
-    auto multiply = [&](const Step &s) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s.x[i], s.y[j], acc[i][j], 0, 0, 0);
-    };
     if (n > 0) {
-        Step s0, s1;
-        load(0);
-        store(0);
-        if (n > 1)
-            load(1);
+        for (int t = 0; t < 2; ++t) {
+            const Source f = source(t);
+#pragma unroll
+            for (int i = 0; i < XPer; ++i)
+                load_x(f, i);
+#pragma unroll
+            for (int i = 0; i < YPer; ++i)
+                load_y(f, i);
+            if (t == 1)
+                break;
+#pragma unroll
+            for (int i = 0; i < XPer; ++i)
+                store_x(i);
+#pragma unroll
+            for (int i = 0; i < YPer; ++i)
+                store_y(i);
+        }
+        xto ^= Bytes, yto ^= Bytes;
         __syncthreads();
-        read(0, 0, s0);
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g)
+            x[g] = column(xat, g, 0);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            y[0][j] = column(yat, j, 0);
         for (int t = 0; t < n; ++t) {
-            const int buf = t & 1;
-            read(buf, 1, s1);
-            multiply(s0);
-            if (t + 1 < n)
-                store(buf ^ 1);
-            __syncthreads();
-            if (t + 2 < n)
-                load(t + 2);
-            if (t + 1 < n)
-                read(buf ^ 1, 0, s0);
-            multiply(s1);
+            const Source f = source(t + 2);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                if (g == kGroups - kAhead) {
+                    __syncthreads();   // the next tile is there, this one is read
+                    xat ^= Bytes, yat ^= Bytes, xto ^= Bytes, yto ^= Bytes;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                const int ahead = (g + kAhead) % kGroups;
+                x[ahead % 4] = column(xat, ahead % N, ahead / N);
+                if (g < N)
+                    y[1][g] = column(yat, g, 1);
+                else
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j * kAhead / N == g - (kGroups - kAhead))
+                            y[0][j] = column(yat, j, 0);
+                // the next tile's chunks to LDS, the one's after it on their way
+                if (g < YPer) {
+                    store_y(g);
+                    load_y(f, g);
+                }
+                if (g % 3 == 1 && g / 3 < XPer) {
+                    store_x(g / 3);
+                    load_x(f, g / 3);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    acc[g % N][j] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[g % 4], y[g / N][j], acc[g % N][j], 0, 0, 0);
+            }
         }
     }
     // a lane holds four neighbouring columns of a row of d_w
