@@ -106,7 +106,7 @@ extern "C" zero_status zero_act8_weight_grad(const uint16_t *d_y, int64_t rows,
         return s;
     if (dy_stride < out_features || w_stride < cols || !d_w || (rows > 0 && (!d_y || !codes || !scales)))
         return ZERO_EINVAL;
-    if (!stride_fits(rows, dy_stride) || !stride_fits(out_features, w_stride))
+    if (dy_stride > 8 * (int64_t)ZERO_MAX_HIDDEN || !stride_fits(out_features, w_stride))
         return ZERO_ERANGE;
     const int64_t blocks = blocks_of(cols);
     const Act8Split split = act8_split(rows, out_features, cols);

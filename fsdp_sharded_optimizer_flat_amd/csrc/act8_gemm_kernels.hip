@@ -32,17 +32,14 @@ __device__ __forceinline__ unsigned widen_pair(unsigned w, float s, bool high)
                                              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
 }
 
-// 16 bytes at p, of which n are within the array.
-__device__ __forceinline__ u32x4 load_within(const uint8_t *p, int64_t n)
+// v's bytes moved down by n > 0, zeros (16 and more: only zeros) behind them.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int n)
 {
-    if (n >= 16)
-        return *reinterpret_cast<const u32x4_at1 *>(p);
-    unsigned w[4] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < n)
-            w[i / 4] |= (unsigned)p[i] << (8 * (i % 4));
-    return u32x4{w[0], w[1], w[2], w[3]};
+    const int bits = min(n, 16) * 8;
+    const uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+    const uint64_t l = bits < 64 ? lo >> bits | hi << 1 << (63 - bits) : bits < 128 ? hi >> (bits - 64) : 0;
+    const uint64_t h = bits < 64 ? hi >> bits : 0;
+    return u32x4{(unsigned)l, (unsigned)(l >> 32), (unsigned)h, (unsigned)(h >> 32)};
 }
 
 // A workgroup of four waves per B x B tile of d_w, a wave per quarter.  FAST: rows
@@ -63,29 +60,32 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
 
     // A tile on its way: chunk i of x' and of d_y in registers.  Rows behind the last
     // are zeros; columns past a row's end may hold the next row's, which reach no
-    // output.
+    // output.  FAST: windows that end where the arrays do (what lies past them reads as
+    // zero).  Else a chunk that would reach past its array is read from the array's last
+    // 16 bytes and shifted when it is stored.
     u32x4 xr[XPer], yr[YPer];
     unsigned sr[XPer];
     struct Source {
-        const uint8_t *x, *s, *y;
-        int64_t left;                        // rows from the tile's first on; <= 0: none
-        __amdgpu_buffer_rsrc_t xw, sw, yw;   // FAST: bounded to the arrays
+        const uint8_t *x, *s, *y;            // from the tile's first row and column on
+        int xend, send, yend;                // bytes from there to the arrays' ends, 2^31 - 1 at most
+        __amdgpu_buffer_rsrc_t xw, sw, yw;
     };
     auto source = [&](int t) {
         Source f;
-        const int64_t r0 = (int64_t)(first + t) * kRows;
-        f.left = a.rows - r0;
+        // a tile behind the last is read, as the last, but not used
+        const int64_t r0 = (int64_t)min(first + t, tiles - 1) * kRows, left = a.rows - r0;
+        auto bound = [](int64_t bytes) { return (int)min(bytes, int64_t(0x7fffffff)); };
         f.x = a.codes + r0 * a.cols + c0;
         f.s = a.scales + r0 * a.blocks + c0 / kActBlock;
         f.y = reinterpret_cast<const uint8_t *>(a.d_y + r0 * a.dy_stride + o0);
+        f.xend = bound(left * a.cols - c0);
+        f.send = bound(left * a.blocks - c0 / kActBlock);
+        f.yend = bound(((left - 1) * a.dy_stride + a.out - o0) * 2);
         if constexpr (FAST) {
-            auto window = [&](const uint8_t *p, int64_t bytes) {
-                const int64_t n = f.left > 0 ? min(max(bytes, int64_t(0)), int64_t(0x7fffffff)) : 0;
-                return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)n, kRawBufferWord3);
+            auto window = [](const uint8_t *p, int n) {
+                return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, n, kRawBufferWord3);
             };
-            f.xw = window(f.x, f.left * a.cols - c0);
-            f.sw = window(f.s, f.left * a.blocks - c0 / kActBlock);
-            f.yw = window(f.y, ((f.left - 1) * a.dy_stride + a.out - o0) * 2);
+            f.xw = window(f.x, f.xend), f.sw = window(f.s, f.send), f.yw = window(f.y, f.yend);
         }
         return f;
     };
@@ -93,27 +93,22 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     constexpr int XRows = 256 / Pairs, YRows = 128 / Pairs;
     const int xrow = tid / Pairs, xpair = tid % Pairs, yrow = tid / (2 * Pairs), yoct = tid % (2 * Pairs);
     const int xoff = xrow * a.cols + xpair * 16, soff = xrow * a.blocks + xpair / 2;
-    const int yoff = (yrow * (int)a.dy_stride + yoct * 8) * 2;   // used where FAST, which bounds the stride
+    const int yoff = (yrow * (int)a.dy_stride + yoct * 8) * 2;
+    const int xstep = XRows * a.cols, sstep = XRows * a.blocks, ystep = YRows * (int)a.dy_stride * 2;
     auto load_x = [&](const Source &f, int i) {
         if constexpr (FAST) {
-            xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.xw, xoff, i * XRows * a.cols, 0));
-            sr[i] = __builtin_amdgcn_raw_buffer_load_b8(f.sw, soff, i * XRows * a.blocks, 0);
+            xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.xw, xoff, i * xstep, 0));
+            sr[i] = __builtin_amdgcn_raw_buffer_load_b8(f.sw, soff, i * sstep, 0);
         } else {
-            const int r = xrow + i * XRows;
-            const int64_t at = (int64_t)r * a.cols + xpair * 16, sat = (int64_t)r * a.blocks + xpair / 2;
-            xr[i] = load_within(f.x + at, r < f.left ? f.left * a.cols - c0 - at : 0);
-            sr[i] = r < f.left && sat < f.left * a.blocks - c0 / kActBlock ? f.s[sat] : 0;
+            xr[i] = *reinterpret_cast<const u32x4_at1 *>(f.x + min(xoff + i * xstep, f.xend - 16));
+            sr[i] = f.s[min(soff + i * sstep, f.send - 1)];
         }
     };
     auto load_y = [&](const Source &f, int i) {
-        if constexpr (FAST) {
-            yr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  f.yw, yoff, i * YRows * (int)a.dy_stride * 2, 0));
-        } else {
-            const int r = yrow + i * YRows;
-            const int64_t at = (r * a.dy_stride + yoct * 8) * 2;
-            yr[i] = load_within(f.y + at, r < f.left ? ((f.left - 1) * a.dy_stride + a.out - o0) * 2 - at : 0);
-        }
+        if constexpr (FAST)
+            yr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.yw, yoff, i * ystep, 0));
+        else
+            yr[i] = *reinterpret_cast<const u32x4_at1 *>(f.y + min(yoff + i * ystep, f.yend - 16));
     };
     // Where a thread's first chunks go in a tile (the rows below are multiples of 8
     // further, so their places differ by whole rows), where a lane reads: its row of the
@@ -125,7 +120,14 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     const int row = lane / 16 * 4 + lane % 16 / 4;
     int xat = row * RowBytes + ((wave % 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
     int yat = 2 * Bytes + row * RowBytes + ((wave / 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
-    auto store_x = [&](int i) {
+    auto store_x = [&](const Source &f, int i) {
+        if constexpr (!FAST) {
+            const int over = xoff + i * xstep - (f.xend - 16);
+            if (over > 0) {
+                xr[i] = shift_down(xr[i], over);
+                sr[i] = over >= 16 ? 0 : sr[i];   // no row: not even a NaN scale
+            }
+        }
         const float s = __uint_as_float(sr[i] << 23);
         const unsigned w[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
         unsigned v[8];
@@ -136,7 +138,14 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         q[0] = u32x4{v[0], v[1], v[2], v[3]};
         q[1] = u32x4{v[4], v[5], v[6], v[7]};
     };
-    auto store_y = [&](int i) { *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[i]; };
+    auto store_y = [&](const Source &f, int i) {
+        if constexpr (!FAST) {
+            const int over = yoff + i * ystep - (f.yend - 16);
+            if (over > 0)
+                yr[i] = shift_down(yr[i], over);
+        }
+        *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[i];
+    };
     auto column = [&](int at, int t, int half) {
         typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
         union {
@@ -155,22 +164,23 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     bf16x8 x[4], y[2][N];
     f32x4 acc[N][N] = {};   // [columns][out]
     if (n > 0) {
+        Source now;   // of the chunks in registers
         for (int t = 0; t < 2; ++t) {
-            const Source f = source(t);
+            now = source(t);
 #pragma unroll
             for (int i = 0; i < XPer; ++i)
-                load_x(f, i);
+                load_x(now, i);
 #pragma unroll
             for (int i = 0; i < YPer; ++i)
-                load_y(f, i);
+                load_y(now, i);
             if (t == 1)
                 break;
 #pragma unroll
             for (int i = 0; i < XPer; ++i)
-                store_x(i);
+                store_x(now, i);
 #pragma unroll
             for (int i = 0; i < YPer; ++i)
-                store_y(i);
+                store_y(now, i);
         }
         xto ^= Bytes, yto ^= Bytes;
         __syncthreads();
@@ -181,7 +191,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         for (int j = 0; j < N; ++j)
             y[0][j] = column(yat, j, 0);
         for (int t = 0; t < n; ++t) {
-            const Source f = source(t + 2);
+            const Source f = source(t + 2);   // chunk by chunk in the places of now's
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 if (g == kGroups - kAhead) {
@@ -200,11 +210,11 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                             y[0][j] = column(yat, j, 0);
                 // the next tile's chunks to LDS, the one's after it on their way
                 if (g < YPer) {
-                    store_y(g);
+                    store_y(now, g);
                     load_y(f, g);
                 }
                 if (g % 3 == 1 && g / 3 < XPer) {
-                    store_x(g / 3);
+                    store_x(now, g / 3);
                     load_x(f, g / 3);
                 }
 #pragma unroll
@@ -212,6 +222,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                     acc[g % N][j] =
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[g % 4], y[g / N][j], acc[g % N][j], 0, 0, 0);
             }
+            now = f;
         }
     }
     // a lane holds four neighbouring columns of a row of d_w
@@ -234,6 +245,23 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         }
 }
 
+// Arrays of fewer than 16 bytes: an element to a thread.
+template <typename O>
+__global__ __launch_bounds__(kBlock) void weight_grad_of_few_kernel(Act8GradArgs a)
+{
+    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    if (i >= (int64_t)a.out * a.cols)
+        return;
+    const int o = (int)(i / a.cols), c = (int)(i - (int64_t)o * a.cols);
+    float sum[4] = {};
+    for (int64_t r = 0; r < a.rows; ++r) {
+        float x[4];
+        widen_codes(a.codes[r * a.cols + c], scale_of(a.scales[r * a.blocks + c / kActBlock]), x);
+        sum[0] += widen<uint16_t>(a.d_y[r * a.dy_stride + o]) * widen<uint16_t>(to_bf16(x[0]));
+    }
+    put4(static_cast<O *>(a.d_w) + (int64_t)o * a.w_stride + c, 1, sum, a.accumulate);
+}
+
 // The parts of each element added in order; four columns to a thread.
 template <typename O>
 __global__ __launch_bounds__(kBlock) void join_splits_kernel(Act8GradArgs a)
@@ -254,7 +282,7 @@ template <int B, typename O>
 void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 {
     const dim3 grid((a.cols + B - 1) / B, (a.out + B - 1) / B, a.splits);
-    const bool fast = a.out % 8 == 0 && a.dy_stride % 8 == 0 && a.dy_stride < 1 << 23 && a.cols % 16 == 0 &&
+    const bool fast = a.out % 8 == 0 && a.dy_stride % 8 == 0 && a.cols % 16 == 0 &&
                       (reinterpret_cast<uintptr_t>(a.d_y) | reinterpret_cast<uintptr_t>(a.codes)) % 16 == 0;
     if (fast)
         hipLaunchKernelGGL((weight_grad_kernel<B, true, O>), grid, dim3(256), 0, st, a);
@@ -282,7 +310,10 @@ int launch_act8_weight_grad(const Act8GradArgs &a, void *stream)
 {
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     by_types(ZERO_F32, a.w_dtype, [&](auto, auto o) {
-        if (a.tile == 256)
+        if (a.rows * a.cols < 16 || (a.rows - 1) * a.dy_stride + a.out < 8)
+            hipLaunchKernelGGL((weight_grad_of_few_kernel<decltype(o)>),
+                               dim3((unsigned)(((int64_t)a.out * a.cols + kBlock - 1) / kBlock)), dim3(kBlock), 0, st, a);
+        else if (a.tile == 256)
             weight_grad_of<256, decltype(o)>(a, st);
         else
             weight_grad_of<128, decltype(o)>(a, st);

@@ -838,7 +838,8 @@ zero_status zero_embedding_grad(const void *d_out, int32_t dtype, int64_t rows, 
  * x and d_w are ZERO_F32 or ZERO_BF16.  Device pointers, aligned to their elements;
  * outputs must not overlap inputs or each other.  Async on `stream`, no allocation,
  * capturable; a workspace serves one call at a time.  Errors: EINVAL, ERANGE (rows >
- * ZERO_MAX_LOSS_ROWS, cols or out_features > ZERO_MAX_HIDDEN), EALIGN, ENOSPC, EHIP.
+ * ZERO_MAX_LOSS_ROWS, cols or out_features > ZERO_MAX_HIDDEN, dy_stride > 8
+ * ZERO_MAX_HIDDEN), EALIGN, ENOSPC, EHIP.
  * No rows: pack and unpack do nothing, the weight gradient is zero.
  * ------------------------------------------------------------------------ */
 #define ZERO_ACT8_BLOCK 32
