@@ -120,14 +120,27 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     const int row = lane / 16 * 4 + lane % 16 / 4;
     int xat = row * RowBytes + ((wave % 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
     int yat = 2 * Bytes + row * RowBytes + ((wave / 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
-    auto store_x = [&](const Source &f, int i) {
-        if constexpr (!FAST) {
+    // Before a tile is stored, if it is one at the arrays' ends: chunks read early to
+    // their places.
+    auto settle = [&](const Source &f) {
+        if (f.xend >= (kRows - 1) * a.cols + B && f.yend >= ((kRows - 1) * (int)a.dy_stride + B) * 2)
+            return;
+#pragma unroll
+        for (int i = 0; i < XPer; ++i) {
             const int over = xoff + i * xstep - (f.xend - 16);
             if (over > 0) {
                 xr[i] = shift_down(xr[i], over);
                 sr[i] = over >= 16 ? 0 : sr[i];   // no row: not even a NaN scale
             }
         }
+#pragma unroll
+        for (int i = 0; i < YPer; ++i) {
+            const int over = yoff + i * ystep - (f.yend - 16);
+            if (over > 0)
+                yr[i] = shift_down(yr[i], over);
+        }
+    };
+    auto store_x = [&](int i) {
         const float s = __uint_as_float(sr[i] << 23);
         const unsigned w[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
         unsigned v[8];
@@ -138,12 +151,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         q[0] = u32x4{v[0], v[1], v[2], v[3]};
         q[1] = u32x4{v[4], v[5], v[6], v[7]};
     };
-    auto store_y = [&](const Source &f, int i) {
-        if constexpr (!FAST) {
-            const int over = yoff + i * ystep - (f.yend - 16);
-            if (over > 0)
-                yr[i] = shift_down(yr[i], over);
-        }
+    auto store_y = [&](int i) {
         *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[i];
     };
     auto column = [&](int at, int t, int half) {
@@ -175,12 +183,14 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                 load_y(now, i);
             if (t == 1)
                 break;
+            if constexpr (!FAST)
+                settle(now);
 #pragma unroll
             for (int i = 0; i < XPer; ++i)
-                store_x(now, i);
+                store_x(i);
 #pragma unroll
             for (int i = 0; i < YPer; ++i)
-                store_y(now, i);
+                store_y(i);
         }
         xto ^= Bytes, yto ^= Bytes;
         __syncthreads();
@@ -191,6 +201,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         for (int j = 0; j < N; ++j)
             y[0][j] = column(yat, j, 0);
         for (int t = 0; t < n; ++t) {
+            if constexpr (!FAST)
+                settle(now);
             const Source f = source(t + 2);   // chunk by chunk in the places of now's
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
@@ -210,11 +222,11 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                             y[0][j] = column(yat, j, 0);
                 // the next tile's chunks to LDS, the one's after it on their way
                 if (g < YPer) {
-                    store_y(now, g);
+                    store_y(g);
                     load_y(f, g);
                 }
                 if (g % 3 == 1 && g / 3 < XPer) {
-                    store_x(now, g / 3);
+                    store_x(g / 3);
                     load_x(f, g / 3);
                 }
 #pragma unroll
