@@ -210,29 +210,32 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                     __syncthreads();   // the next tile is there, this one is read
                     xat ^= Bytes, yat ^= Bytes, xto ^= Bytes, yto ^= Bytes;
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                const int ahead = (g + kAhead) % kGroups;
-                x[ahead % 4] = column(xat, ahead % N, ahead / N);
-                if (g < N)
-                    y[1][g] = column(yat, g, 1);
-                else
+                // work for the shadow of each product: two reads of x', of d_y, the next
+                // tile's chunks to LDS, the one's after it on their way
+                auto beside = [&](int j) {
+                    const int ahead = (g + kAhead) % kGroups;
+                    if (j == 0)
+                        x[ahead % 4] = column(xat, ahead % N, ahead / N);
+                    if (g < N && j == 1)
+                        y[1][g] = column(yat, g, 1);
+                    if (g >= kGroups - kAhead && (j * kAhead + kAhead - 1) / N == g - (kGroups - kAhead))
+                        y[0][j] = column(yat, j, 0);
+                    if (g < YPer && j == N / 2) {
+                        store_y(g);
+                        load_y(f, g);
+                    }
+                    if (g % 3 == 1 && g / 3 < XPer && j == N - 2) {
+                        store_x(g / 3);
+                        load_x(f, g / 3);
+                    }
+                };
 #pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (j * kAhead / N == g - (kGroups - kAhead))
-                            y[0][j] = column(yat, j, 0);
-                // the next tile's chunks to LDS, the one's after it on their way
-                if (g < YPer) {
-                    store_y(g);
-                    load_y(f, g);
-                }
-                if (g % 3 == 1 && g / 3 < XPer) {
-                    store_x(g / 3);
-                    load_x(f, g / 3);
-                }
-#pragma unroll
-                for (int j = 0; j < N; ++j)
+                for (int j = 0; j < N; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
                     acc[g % N][j] =
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[g % 4], y[g / N][j], acc[g % N][j], 0, 0, 0);
+                    beside(j);
+                }
             }
             now = f;
         }
