@@ -51,6 +51,9 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     constexpr int RowBytes = B * 2, Pairs = B / 16;
     constexpr int XPer = kRows * Pairs / 256, YPer = 2 * XPer;
     constexpr int Bytes = kRows * RowBytes;
+    // Tiles on their way in registers: a small tile's products are over before memory
+    // answers (8192 x 1280 x 1280, 100 workgroups: 128 us with one, 89 with three).
+    constexpr int kDepth = B == 256 ? 1 : 3;
     __shared__ __attribute__((aligned(16))) char sh[4 * Bytes];   // x', d_y; two tiles each
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int c0 = blockIdx.x * B, o0 = blockIdx.y * B;
@@ -63,8 +66,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     // output.  FAST: windows that end where the arrays do (what lies past them reads as
     // zero).  Else a chunk that would reach past its array is read from the array's last
     // 16 bytes and shifted when it is stored.
-    u32x4 xr[XPer], yr[YPer];
-    unsigned sr[XPer];
+    u32x4 xr[kDepth][XPer], yr[kDepth][YPer];
+    unsigned sr[kDepth][XPer];
     struct Source {
         const uint8_t *x, *s, *y;            // from the tile's first row and column on
         int xend, send, yend;                // bytes from there to the arrays' ends, 2^31 - 1 at most
@@ -95,20 +98,20 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     const int xoff = xrow * a.cols + xpair * 16, soff = xrow * a.blocks + xpair / 2;
     const int yoff = (yrow * (int)a.dy_stride + yoct * 8) * 2;
     const int xstep = XRows * a.cols, sstep = XRows * a.blocks, ystep = YRows * (int)a.dy_stride * 2;
-    auto load_x = [&](const Source &f, int i) {
+    auto load_x = [&](const Source &f, int d, int i) {
         if constexpr (FAST) {
-            xr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.xw, xoff, i * xstep, 0));
-            sr[i] = __builtin_amdgcn_raw_buffer_load_b8(f.sw, soff, i * sstep, 0);
+            xr[d][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.xw, xoff, i * xstep, 0));
+            sr[d][i] = __builtin_amdgcn_raw_buffer_load_b8(f.sw, soff, i * sstep, 0);
         } else {
-            xr[i] = *reinterpret_cast<const u32x4_at1 *>(f.x + min(xoff + i * xstep, f.xend - 16));
-            sr[i] = f.s[min(soff + i * sstep, f.send - 1)];
+            xr[d][i] = *reinterpret_cast<const u32x4_at1 *>(f.x + i * xstep + min(xoff, f.xend - 16 - i * xstep));
+            sr[d][i] = (f.s + i * sstep)[min(soff, f.send - 1 - i * sstep)];
         }
     };
-    auto load_y = [&](const Source &f, int i) {
+    auto load_y = [&](const Source &f, int d, int i) {
         if constexpr (FAST)
-            yr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.yw, yoff, i * ystep, 0));
+            yr[d][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f.yw, yoff, i * ystep, 0));
         else
-            yr[i] = *reinterpret_cast<const u32x4_at1 *>(f.y + min(yoff + i * ystep, f.yend - 16));
+            yr[d][i] = *reinterpret_cast<const u32x4_at1 *>(f.y + i * ystep + min(yoff, f.yend - 16 - i * ystep));
     };
     // Where a thread's first chunks go in a tile (the rows below are multiples of 8
     // further, so their places differ by whole rows), where a lane reads: its row of the
@@ -122,27 +125,27 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     int yat = 2 * Bytes + row * RowBytes + ((wave / 2 * N ^ (row & 7)) * 32) + lane % 4 * 8;
     // Before a tile is stored, if it is one at the arrays' ends: chunks read early to
     // their places.
-    auto settle = [&](const Source &f) {
+    auto settle = [&](const Source &f, int d) {
         if (f.xend >= (kRows - 1) * a.cols + B && f.yend >= ((kRows - 1) * (int)a.dy_stride + B) * 2)
             return;
 #pragma unroll
         for (int i = 0; i < XPer; ++i) {
             const int over = xoff + i * xstep - (f.xend - 16);
             if (over > 0) {
-                xr[i] = shift_down(xr[i], over);
-                sr[i] = over >= 16 ? 0 : sr[i];   // no row: not even a NaN scale
+                xr[d][i] = shift_down(xr[d][i], over);
+                sr[d][i] = over >= 16 ? 0 : sr[d][i];   // no row: not even a NaN scale
             }
         }
 #pragma unroll
         for (int i = 0; i < YPer; ++i) {
             const int over = yoff + i * ystep - (f.yend - 16);
             if (over > 0)
-                yr[i] = shift_down(yr[i], over);
+                yr[d][i] = shift_down(yr[d][i], over);
         }
     };
-    auto store_x = [&](int i) {
-        const float s = __uint_as_float(sr[i] << 23);
-        const unsigned w[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
+    auto store_x = [&](int d, int i) {
+        const float s = __uint_as_float(sr[d][i] << 23);
+        const unsigned w[4] = {xr[d][i].x, xr[d][i].y, xr[d][i].z, xr[d][i].w};
         unsigned v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -151,8 +154,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         q[0] = u32x4{v[0], v[1], v[2], v[3]};
         q[1] = u32x4{v[4], v[5], v[6], v[7]};
     };
-    auto store_y = [&](int i) {
-        *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[i];
+    auto store_y = [&](int d, int i) {
+        *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[d][i];
     };
     auto column = [&](int at, int t, int half) {
         typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
@@ -172,26 +175,28 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     bf16x8 x[4], y[2][N];
     f32x4 acc[N][N] = {};   // [columns][out]
     if (n > 0) {
-        Source now;   // of the chunks in registers
-        for (int t = 0; t < 2; ++t) {
-            now = source(t);
+        Source held[kDepth];   // of the chunks in registers
+        auto fetch = [&](int d, int t) {
+            held[d] = source(t);
 #pragma unroll
             for (int i = 0; i < XPer; ++i)
-                load_x(now, i);
+                load_x(held[d], d, i);
 #pragma unroll
             for (int i = 0; i < YPer; ++i)
-                load_y(now, i);
-            if (t == 1)
-                break;
-            if constexpr (!FAST)
-                settle(now);
+                load_y(held[d], d, i);
+        };
 #pragma unroll
-            for (int i = 0; i < XPer; ++i)
-                store_x(i);
+        for (int d = 0; d < kDepth; ++d)
+            fetch(d, d);
+        if constexpr (!FAST)
+            settle(held[0], 0);
 #pragma unroll
-            for (int i = 0; i < YPer; ++i)
-                store_y(i);
-        }
+        for (int i = 0; i < XPer; ++i)
+            store_x(0, i);
+#pragma unroll
+        for (int i = 0; i < YPer; ++i)
+            store_y(0, i);
+        fetch(0, kDepth);
         xto ^= Bytes, yto ^= Bytes;
         __syncthreads();
 #pragma unroll
@@ -200,10 +205,10 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
 #pragma unroll
         for (int j = 0; j < N; ++j)
             y[0][j] = column(yat, j, 0);
-        for (int t = 0; t < n; ++t) {
+        auto step = [&](int d, int t) {   // tile t; d: where tile t + 1 is held
             if constexpr (!FAST)
-                settle(now);
-            const Source f = source(t + 2);   // chunk by chunk in the places of now's
+                settle(held[d], d);
+            const Source f = source(t + 1 + kDepth);   // chunk by chunk in the places of held[d]'s
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 if (g == kGroups - kAhead) {
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                     xat ^= Bytes, yat ^= Bytes, xto ^= Bytes, yto ^= Bytes;
                 }
                 // work for the shadow of each product: two reads of x', of d_y, the next
-                // tile's chunks to LDS, the one's after it on their way
+                // tile's chunks to LDS, a later one's on their way
                 auto beside = [&](int j) {
                     const int ahead = (g + kAhead) % kGroups;
                     if (j == 0)
@@ -221,12 +226,12 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                     if (g >= kGroups - kAhead && (j * kAhead + kAhead - 1) / N == g - (kGroups - kAhead))
                         y[0][j] = column(yat, j, 0);
                     if (g < YPer && j == N / 2) {
-                        store_y(g);
-                        load_y(f, g);
+                        store_y(d, g);
+                        load_y(f, d, g);
                     }
                     if (g % 3 == 1 && g / 3 < XPer && j == N - 2) {
-                        store_x(g / 3);
-                        load_x(f, g / 3);
+                        store_x(d, g / 3);
+                        load_x(f, d, g / 3);
                     }
                 };
 #pragma unroll
@@ -237,7 +242,17 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                     beside(j);
                 }
             }
-            now = f;
+            held[d] = f;
+        };
+        if constexpr (kDepth == 1) {
+            for (int t = 0; t < n; ++t)
+                step(0, t);
+        } else {
+            for (int t = 0; t < n; t += kDepth)
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i)
+                    if (t + i < n)
+                        step((i + 1) % kDepth, t + i);
         }
     }
     // a lane holds four neighbouring columns of a row of d_w
@@ -310,15 +325,41 @@ void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 
 }  // namespace
 
+// Tiles of 256 x 256 read LDS half as often for a product as those of 128 x 128, but
+// small outputs have few of them; rows are split over workgroups where there are few
+// tiles of either kind, at the price of the parts' way through memory.  The least of
+// these estimates, in us, fitted to sweeps over tiles and splits (what they give | what
+// was measured):
+//      rows x out x cols      256 / 1     256 / split     128 / 1     128 / split
+//   8192 x 4096 x  4096     237 | 241    287 | 288 (2)   295 | 288    344 | 330 (2)
+//   4096 x 1280 x  5120     125 | 115     85 |  79 (2)    77 |  77     99 |  95 (2)
+//   8192 x 1280 x  1280     237 | 214     57 |  54 (8)    96 |  89     51 |  52 (4)
+//   2048 x 1280 x  1280      69 |  64     36 |  33 (8)    29 |  27     24 |  23 (2)
+//   1024 x 1280 x  1280      41 |  39     30 |  29 (4)    18 |  17     18 |  18 (2)
+//  16384 x   64 x    64     461 | 408     30 |  30 (32)  186 | 170     17 |  20 (24)
 Act8Split act8_split(int64_t rows, int64_t out, int64_t cols)
 {
-    auto tiles = [&](int64_t b) { return ((out + b - 1) / b) * ((cols + b - 1) / b); };
-    if (tiles(256) >= 160)
-        return {256, 1};
-    const int64_t steps = (rows + kRows - 1) / kRows;
-    const int64_t want = (512 + tiles(128) - 1) / tiles(128);
-    const int64_t s = std::max<int64_t>(1, std::min(want, steps / 4));
-    return {128, (int32_t)s};
+    const int64_t steps = std::max<int64_t>(1, (rows + kRows - 1) / kRows);
+    Act8Split best{128, 1};
+    double least = 1e300;
+    for (int32_t tile : {256, 128}) {
+        const int64_t tiles = ((out + tile - 1) / tile) * ((cols + tile - 1) / tile);
+        for (int64_t s = 1; s <= std::min<int64_t>(steps, 64); ++s) {
+            const int64_t per = (steps + s - 1) / s;
+            if ((steps + per - 1) / per != s)
+                continue;   // the last workgroup would have none
+            // one large tile fits a compute unit, two small ones, which slow each other
+            const int64_t groups = tiles * s;
+            double t = tile == 256 ? (double)((groups + 255) / 256) * (1.75 * (double)per + 13.0)
+                       : groups <= 256 ? 0.7 * (double)per + 6.5
+                                       : (double)((groups + 511) / 512) * (1.1 * (double)per + 6.5);
+            if (s > 1)
+                t += 3.0 + 1e-6 * (double)(s * out * cols);
+            if (t < least)
+                least = t, best = {tile, (int32_t)s};
+        }
+    }
+    return best;
 }
 
 int launch_act8_weight_grad(const Act8GradArgs &a, void *stream)
