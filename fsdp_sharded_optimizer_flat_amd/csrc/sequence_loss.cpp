@@ -20,14 +20,29 @@ zero_status check_sequences(const int64_t *tokens, int64_t n_tokens, const int64
         return ZERO_ERANGE;
     if (n_seqs > 0 && !offsets)
         return ZERO_EINVAL;
-    *s = Sequences{tokens, offsets, n_tokens, n_seqs, mode};
+    *s = Sequences{tokens, offsets, n_tokens, n_seqs, mode, sequence_cut(n_tokens, n_seqs), nullptr};
     return ZERO_OK;
 }
+
+int64_t parts_bytes(const SequenceCut &c) { return c.slots * (int64_t)sizeof(SequencePart); }
 
 // NaN is out of every range.
 bool within(double x, double lo, double hi) { return x >= lo && x <= hi; }
 
 }  // namespace
+
+SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs)
+{
+    if (n_tokens <= kSequenceShort || n_seqs == 0)
+        return {1, 0};
+    // every wave of a sequence adds up all its parts: tiles grow before an even share of
+    // the positions has more than 512 of them
+    int32_t rounds = 1;
+    while (rounds < 64 && n_tokens / n_seqs > (int64_t)rounds * 4 * kWave * 512)
+        rounds *= 4;
+    return {rounds, n_tokens / (rounds * 4 * kWave) + n_seqs};
+}
+
 }  // namespace zero
 
 using namespace zero;
@@ -39,7 +54,7 @@ extern "C" zero_status zero_sequence_loss_workspace_bytes(int64_t n_tokens, int6
         return ZERO_EINVAL;
     if (n_tokens > ZERO_MAX_LOSS_ROWS || n_seqs > ZERO_MAX_SEQUENCES)
         return ZERO_ERANGE;
-    *bytes = 0;
+    *bytes = (size_t)parts_bytes(sequence_cut(n_tokens, n_seqs));
     return ZERO_OK;
 }
 
@@ -61,15 +76,19 @@ extern "C" zero_status zero_policy_loss(const float *logprob, const float *old_l
     if (n_seqs > 0 && ((!advantage && (n_tokens > 0 || !per_token)) || (d_logprob && !d_loss) ||
                        (n_tokens > 0 && (!logprob || !old_logprob || (!loss && !kl && !clipped && !d_logprob)))))
         return ZERO_EINVAL;
+    const int64_t need = parts_bytes(a.seq.cut);
+    if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, need))
+        return s;
     const Span in[] = {vec(logprob, n_tokens, 4), vec(old_logprob, n_tokens, 4),
                        vec(ref_logprob, n_tokens, 4), vec(advantage, per_token ? n_tokens : n_seqs, 4),
                        vec(tokens, n_tokens, 8), vec(offsets, n_seqs + 1, 8), vec(d_loss, n_seqs, 4)};
     const Span out[] = {vec(loss, n_seqs, 4), vec(kl, n_seqs, 4), vec(clipped, n_seqs, 4),
-                        vec(d_logprob, n_tokens, 4)};
-    if (zero_status s = check_spans(in, 7, out, 4))
+                        vec(d_logprob, n_tokens, 4), {need ? workspace : nullptr, need, 16}};
+    if (zero_status s = check_spans(in, 7, out, 5))
         return s;
     if (n_seqs == 0)
         return ZERO_OK;
+    a.seq.parts = static_cast<SequencePart *>(workspace);
     a.logprob = logprob;
     a.old_logprob = old_logprob;
     a.ref_logprob = ref_logprob;
@@ -109,13 +128,18 @@ extern "C" zero_status zero_preference_loss(const float *logprob, const float *r
         return ZERO_EINVAL;
     if (n_pairs > 0 && ((d_logprob && !d_loss) || (n_tokens > 0 && (!logprob || (!loss && !reward && !d_logprob)))))
         return ZERO_EINVAL;
+    const int64_t need = parts_bytes(a.seq.cut);
+    if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, need))
+        return s;
     const Span in[] = {vec(logprob, n_tokens, 4), vec(ref_logprob, n_tokens, 4), vec(tokens, n_tokens, 8),
                        vec(offsets, 2 * n_pairs + 1, 8), vec(d_loss, n_pairs, 4)};
-    const Span out[] = {vec(loss, n_pairs, 4), vec(reward, 2 * n_pairs, 4), vec(d_logprob, n_tokens, 4)};
-    if (zero_status s = check_spans(in, 5, out, 3))
+    const Span out[] = {vec(loss, n_pairs, 4), vec(reward, 2 * n_pairs, 4), vec(d_logprob, n_tokens, 4),
+                        {need ? workspace : nullptr, need, 16}};
+    if (zero_status s = check_spans(in, 5, out, 4))
         return s;
     if (n_pairs == 0)
         return ZERO_OK;
+    a.seq.parts = static_cast<SequencePart *>(workspace);
     a.logprob = logprob;
     a.ref_logprob = ref_logprob;
     a.d_loss = d_loss;

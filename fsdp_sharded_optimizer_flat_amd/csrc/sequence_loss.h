@@ -6,12 +6,32 @@
 
 namespace zero {
 
+// Up to this many positions a call is one launch, a workgroup to a sequence or pair.
+constexpr int64_t kSequenceShort = 16384;
+
+// Longer ones are cut into tiles of the positions (64 lanes, four positions a lane
+// and round); a wave takes a sequence's share of a tile.
+struct SequenceCut {
+    int32_t rounds;
+    int64_t slots;   // shares at most; 0: not cut
+};
+SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs);
+
+// A share's sums.  Policy: of the losses and k, targets beyond the border; preference:
+// of the log ratios.
+struct SequencePart {
+    double a, b;
+    int32_t cut, targets;
+};
+
 // The packed sequences of a call.
 struct Sequences {
     const int64_t *tokens;    // NULL: every position is a target
     const int64_t *offsets;   // n + 1
     int64_t n_tokens, n;
     int32_t mode;
+    SequenceCut cut;
+    SequencePart *parts;      // cut.slots of them
 };
 
 struct PolicyArgs {

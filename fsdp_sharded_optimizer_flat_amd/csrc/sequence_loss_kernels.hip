@@ -5,7 +5,17 @@
 // All terms are binary64: a difference of two binary32 log probabilities is exact
 // there, so whether a ratio is beyond the clipping border is decided on
 // logprob - old against the border's logarithm, exp(x) - 1 - x (about x^2 / 2, x often
-// 10^-3) keeps its digits, and sums over long sequences lose nothing.
+// 10^-3) keeps its digits, and sums over long sequences lose nothing.  MI355X adds and
+// multiplies binary64 as fast as unpacked binary32.
+//
+// Few positions: a workgroup to a sequence or pair, one launch.  Many: the array is
+// cut into tiles and a wave takes what a sequence has of one, so the work is even
+// whatever the lengths.  Share (b, tile) has slot tile + b: the tiles of the sequences
+// before b end at or before the one b begins in, so no two shares meet in a slot, and
+// the slot's b is found by search.  A second launch adds up each sequence's shares, in
+// order, and scales the gradients.
+#include <algorithm>
+
 #include "device_common.h"
 #include "sequence_loss.h"
 
@@ -14,7 +24,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kSeqBlock = 256;
+constexpr int kQuadTokens = 4;   // positions of a lane
 
 struct Range {
     int64_t lo, hi;
@@ -25,33 +35,136 @@ __device__ __forceinline__ Range range_of(const Sequences &s, int64_t b)
     const int64_t lo = min(max(s.offsets[b], int64_t(0)), s.n_tokens);
     return {lo, max(lo, min(s.offsets[b + 1], s.n_tokens))};
 }
-__device__ __forceinline__ bool is_target(const Sequences &s, int64_t t)
-{
-    return !s.tokens || s.tokens[t] >= 0;
-}
 __device__ __forceinline__ double weight_of(const Sequences &s, int64_t targets)
 {
     return s.mode == ZERO_SEQUENCE_SUM || targets == 0 ? 1.0 : 1.0 / (double)targets;
 }
 
-// The sum over the workgroup's threads, in every thread, in a fixed order.
-template <typename T>
-__device__ __forceinline__ T block_sum(T x)
+// Four neighbouring values from position t on, of which those in the range are read.
+__device__ __forceinline__ void load_quad(const float *p, int64_t t, const Range &r, float (&x)[kQuadTokens])
 {
-    __shared__ T sh[kSeqBlock / kWave];
+    typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+    if (t >= r.lo && t + kQuadTokens <= r.hi) {
+        const f32x4 v = *reinterpret_cast<const f32x4_at4 *>(p + t);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k)
+        x[k] = t + k >= r.lo && t + k < r.hi ? p[t + k] : 0.0f;
+}
+__device__ __forceinline__ void store_quad(float *p, int64_t t, const Range &r, const float (&x)[kQuadTokens])
+{
+    typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+    if (t >= r.lo && t + kQuadTokens <= r.hi) {
+        *reinterpret_cast<f32x4_at4 *>(p + t) = f32x4{x[0], x[1], x[2], x[3]};
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k)
+        if (t + k >= r.lo && t + k < r.hi)
+            p[t + k] = x[k];
+}
+// Which of four positions are targets of the range, as bits.
+__device__ __forceinline__ unsigned targets_of(const Sequences &s, int64_t t, const Range &r)
+{
+    typedef long i64x2 __attribute__((ext_vector_type(2)));
+    typedef i64x2 i64x2_at8 __attribute__((aligned(8)));
+    if (s.tokens && t >= r.lo && t + kQuadTokens <= r.hi) {
+        const i64x2 a = *reinterpret_cast<const i64x2_at8 *>(s.tokens + t);
+        const i64x2 b = *reinterpret_cast<const i64x2_at8 *>(s.tokens + t + 2);
+        return (a.x >= 0) | (a.y >= 0) << 1 | (b.x >= 0) << 2 | (b.y >= 0) << 3;
+    }
+    unsigned on = 0;
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k)
+        if (t + k >= r.lo && t + k < r.hi && (!s.tokens || s.tokens[t + k] >= 0))
+            on |= 1u << k;
+    return on;
+}
+
+// -- sums -----------------------------------------------------------------------------
+
+__device__ __forceinline__ void add(SequencePart &p, const SequencePart &q)
+{
+    p.a += q.a;
+    p.b += q.b;
+    p.cut += q.cut;
+    p.targets += q.targets;
+}
+// Over a wave, in every lane, in a fixed order.
+__device__ __forceinline__ SequencePart wave_total(SequencePart p)
+{
 #pragma unroll
     for (int off = kWave / 2; off >= 1; off >>= 1)
-        x += __shfl_xor(x, off, kWave);
-    __syncthreads();
-    if (threadIdx.x % kWave == 0)
-        sh[threadIdx.x / kWave] = x;
-    __syncthreads();
-    x = sh[0];
-#pragma unroll
-    for (int w = 1; w < kSeqBlock / kWave; ++w)
-        x += sh[w];
-    return x;
+        add(p, SequencePart{__shfl_xor(p.a, off, kWave), __shfl_xor(p.b, off, kWave), __shfl_xor(p.cut, off, kWave),
+                            __shfl_xor(p.targets, off, kWave)});
+    return p;
 }
+// Over `waves` waves from wave `first` of a workgroup on, in their threads; `sh`: one
+// per wave of the workgroup.
+__device__ __forceinline__ SequencePart waves_total(SequencePart p, SequencePart *sh, int first, int waves)
+{
+    p = wave_total(p);
+    if (threadIdx.x % kWave == 0)
+        sh[threadIdx.x / kWave] = p;
+    __syncthreads();
+    p = sh[first];
+    for (int w = 1; w < waves; ++w)
+        add(p, sh[first + w]);
+    return p;
+}
+
+// The share that a slot holds: sequence b's positions of a tile.
+struct Share {
+    int64_t b, tile;
+    Range seq, part;
+    bool first;   // of its sequence (of an empty sequence: the only one, empty)
+    bool none;
+};
+// The slot that sequence b's first share has.
+__device__ __forceinline__ int64_t first_slot(const Sequences &s, int64_t b, int64_t span)
+{
+    return min(max(s.offsets[b], int64_t(0)), s.n_tokens) / span + b;
+}
+__device__ __forceinline__ Share share_of(const Sequences &s, int64_t slot)
+{
+    const int64_t span = (int64_t)s.cut.rounds * kQuadTokens * kWave;
+    const int lane = threadIdx.x % kWave;
+    // the last sequence whose first slot is not behind this one: 64 candidates at a time
+    int64_t lo = 0, n = s.n;
+    while (n > 1) {
+        const int64_t step = (n + kWave - 1) / kWave, c = lo + lane * step;
+        const uint64_t not_behind = __ballot(c < lo + n && first_slot(s, c, span) <= slot);
+        const int k = 63 - __builtin_clzll(not_behind | 1);
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    Share h;
+    h.b = lo;
+    h.tile = slot - lo;
+    h.seq = range_of(s, lo);
+    const int64_t begin = h.seq.lo / span;
+    h.first = h.tile == begin;
+    h.part.lo = max(h.seq.lo, h.tile * span);
+    h.part.hi = min(h.seq.hi, (h.tile + 1) * span);
+    h.none = !h.first && (h.tile < begin || h.part.lo >= h.part.hi);
+    return h;
+}
+// The sums of a sequence's shares, in every lane.
+__device__ __forceinline__ SequencePart total_of(const Sequences &s, int64_t b, const Range &r)
+{
+    const int64_t span = (int64_t)s.cut.rounds * kQuadTokens * kWave;
+    SequencePart p{};
+    if (r.hi > r.lo) {
+        const int64_t first = r.lo / span + b, last = (r.hi - 1) / span + b;
+        for (int64_t i = first + threadIdx.x % kWave; i <= last; i += kWave)
+            add(p, s.parts[i]);
+    }
+    return wave_total(p);
+}
+
+// -- policy ---------------------------------------------------------------------------
 
 struct Term {
     double loss, kl, slope;
@@ -78,46 +191,130 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs &a, float lp, float
     return t;
 }
 
-// One workgroup per sequence.
-__global__ __launch_bounds__(kSeqBlock) void policy_kernel(PolicyArgs a)
+// Four positions of sequence b: their sums, their slopes (0 where there is no target).
+__device__ __forceinline__ void policy_quad(const PolicyArgs &a, int64_t b, int64_t t, const Range &r, SequencePart &sum,
+                                            double (&slope)[kQuadTokens])
 {
-    const int64_t b = blockIdx.x;
-    const Range s = range_of(a.seq, b);
-    const float adv = a.per_token ? 0.0f : a.advantage[b];
-    int targets = 0;
-    for (int64_t t = s.lo + threadIdx.x; t < s.hi; t += kSeqBlock)
-        targets += is_target(a.seq, t);
-    targets = block_sum(targets);
-    const double w = weight_of(a.seq, targets);
-    const double up = a.d_logprob ? w * (double)a.d_loss[b] : 0.0;
-    double loss = 0.0, kl = 0.0;
-    int cut = 0;
-    for (int64_t t = s.lo + threadIdx.x; t < s.hi; t += kSeqBlock) {
-        if (!is_target(a.seq, t)) {
-            if (a.d_logprob)
-                a.d_logprob[t] = 0.0f;
-            continue;
+    float lp[kQuadTokens], old[kQuadTokens], ref[kQuadTokens] = {}, adv[kQuadTokens];
+    const unsigned on = targets_of(a.seq, t, r);
+    load_quad(a.logprob, t, r, lp);
+    load_quad(a.old_logprob, t, r, old);
+    if (a.ref_logprob)
+        load_quad(a.ref_logprob, t, r, ref);
+    if (a.per_token)
+        load_quad(a.advantage, t, r, adv);
+    else
+        adv[0] = adv[1] = adv[2] = adv[3] = a.advantage[b];
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k) {
+        slope[k] = 0.0;
+        if (on >> k & 1) {
+            const Term m = policy_term(a, lp[k], old[k], ref[k], adv[k]);
+            add(sum, SequencePart{m.loss, m.kl, m.cut, 1});
+            slope[k] = m.slope;
         }
-        const Term m = policy_term(a, a.logprob[t], a.old_logprob[t], a.ref_logprob ? a.ref_logprob[t] : 0.0f,
-                                   a.per_token ? a.advantage[t] : adv);
-        loss += m.loss;
-        kl += m.kl;
-        cut += m.cut;
-        if (a.d_logprob)
-            a.d_logprob[t] = (float)(up * m.slope);
-    }
-    loss = block_sum(loss);
-    kl = block_sum(kl);
-    cut = block_sum(cut);
-    if (threadIdx.x == 0) {
-        if (a.loss)
-            a.loss[b] = (float)(w * loss);
-        if (a.kl)
-            a.kl[b] = (float)(w * kl);
-        if (a.clipped)
-            a.clipped[b] = cut;
     }
 }
+// A quad's gradients: up times the slopes, zero where there is no target, whatever up is.
+__device__ __forceinline__ void put_slopes(const PolicyArgs &a, int64_t t, const Range &r, double up,
+                                           const double (&slope)[kQuadTokens])
+{
+    const bool plain = __builtin_fabs(up) < __builtin_inf();
+    const unsigned on = plain ? 15u : targets_of(a.seq, t, r);
+    float g[kQuadTokens];
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k)
+        g[k] = on >> k & 1 ? (float)(up * slope[k]) : 0.0f;
+    store_quad(a.d_logprob, t, r, g);
+}
+__device__ __forceinline__ void put_policy(const PolicyArgs &a, int64_t b, const SequencePart &p)
+{
+    const double w = weight_of(a.seq, p.targets);
+    if (a.loss)
+        a.loss[b] = (float)(w * p.a);
+    if (a.kl)
+        a.kl[b] = (float)(w * p.b);
+    if (a.clipped)
+        a.clipped[b] = p.cut;
+}
+
+// A workgroup of NT threads to a sequence; up to 4 NT positions are read once.
+template <int NT>
+__global__ __launch_bounds__(NT) void policy_kernel(PolicyArgs a)
+{
+    __shared__ SequencePart sh[NT / kWave];
+    const int64_t b = blockIdx.x;
+    const Range r = range_of(a.seq, b);
+    const int64_t t0 = r.lo / kQuadTokens * kQuadTokens + threadIdx.x * kQuadTokens;
+    SequencePart sum{};
+    double held[kQuadTokens], slope[kQuadTokens];
+    policy_quad(a, b, t0, r, sum, held);
+    for (int64_t t = t0 + NT * kQuadTokens; t < r.hi; t += NT * kQuadTokens)
+        policy_quad(a, b, t, r, sum, slope);
+    sum = waves_total(sum, sh, 0, NT / kWave);
+    if (threadIdx.x == 0)
+        put_policy(a, b, sum);
+    if (!a.d_logprob)
+        return;
+    const double up = weight_of(a.seq, sum.targets) * (double)a.d_loss[b];
+    put_slopes(a, t0, r, up, held);
+    for (int64_t t = t0 + NT * kQuadTokens; t < r.hi; t += NT * kQuadTokens) {
+        SequencePart again{};
+        policy_quad(a, b, t, r, again, slope);
+        put_slopes(a, t, r, up, slope);
+    }
+}
+
+// A wave to a share: its sums; gradients of sums are finished here, those of means
+// but for the targets' number.
+__global__ __launch_bounds__(kBlock) void policy_share_kernel(PolicyArgs a)
+{
+    const int64_t slot = (int64_t)blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
+    if (slot >= a.seq.cut.slots)
+        return;
+    const Share h = share_of(a.seq, slot);
+    if (h.none || h.part.lo >= h.part.hi)
+        return;
+    const double up = a.d_logprob && a.seq.mode == ZERO_SEQUENCE_SUM ? (double)a.d_loss[h.b] : 1.0;
+    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
+    SequencePart sum{};
+    for (int i = 0; i < a.seq.cut.rounds; ++i) {
+        const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
+        double slope[kQuadTokens];
+        policy_quad(a, h.b, t, h.part, sum, slope);
+        if (a.d_logprob)
+            put_slopes(a, t, h.part, up, slope);
+    }
+    sum = wave_total(sum);
+    if (threadIdx.x % kWave == 0)
+        a.seq.parts[slot] = sum;
+}
+__global__ __launch_bounds__(kBlock) void policy_join_kernel(PolicyArgs a)
+{
+    const int64_t slot = (int64_t)blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
+    if (slot >= a.seq.cut.slots)
+        return;
+    const Share h = share_of(a.seq, slot);
+    const bool scale = a.d_logprob && a.seq.mode == ZERO_SEQUENCE_MEAN && h.part.lo < h.part.hi;
+    if (h.none || !(h.first || scale))
+        return;
+    const SequencePart sum = total_of(a.seq, h.b, h.seq);
+    if (h.first && threadIdx.x % kWave == 0)
+        put_policy(a, h.b, sum);
+    if (!scale)
+        return;
+    const double up = weight_of(a.seq, sum.targets) * (double)a.d_loss[h.b];
+    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
+    for (int i = 0; i < a.seq.cut.rounds; ++i) {
+        const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
+        float g[kQuadTokens];
+        load_quad(a.d_logprob, t, h.part, g);
+        const double slope[kQuadTokens] = {g[0], g[1], g[2], g[3]};
+        put_slopes(a, t, h.part, up, slope);
+    }
+}
+
+// -- preference -----------------------------------------------------------------------
 
 // A pair's loss and its derivative by h.
 __device__ __forceinline__ void preference(const PreferenceArgs &a, double h, double &loss, double &slope)
@@ -140,53 +337,155 @@ __device__ __forceinline__ void preference(const PreferenceArgs &a, double h, do
     }
 }
 
-// One workgroup per pair.
-__global__ __launch_bounds__(kSeqBlock) void preference_kernel(PreferenceArgs a)
+__device__ __forceinline__ unsigned ratio_quad(const PreferenceArgs &a, int64_t t, const Range &r, SequencePart &sum)
 {
-    const int64_t p = blockIdx.x;
-    double reward[2], w[2];
-    for (int i = 0; i < 2; ++i) {
-        const Range s = range_of(a.seq, p + i * a.pairs);
-        double sum = 0.0;
-        int targets = 0;
-        for (int64_t t = s.lo + threadIdx.x; t < s.hi; t += kSeqBlock)
-            if (is_target(a.seq, t)) {
-                sum += a.ref_logprob ? (double)a.logprob[t] - (double)a.ref_logprob[t] : (double)a.logprob[t];
-                ++targets;
-            }
-        w[i] = weight_of(a.seq, block_sum(targets));
-        reward[i] = a.beta * (block_sum(sum) * w[i]);
-        if (a.reward && threadIdx.x == 0)
-            a.reward[p + i * a.pairs] = (float)reward[i];
-    }
+    float lp[kQuadTokens], ref[kQuadTokens] = {};
+    const unsigned on = targets_of(a.seq, t, r);
+    load_quad(a.logprob, t, r, lp);
+    if (a.ref_logprob)
+        load_quad(a.ref_logprob, t, r, ref);
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k)
+        if (on >> k & 1)
+            add(sum, SequencePart{(double)lp[k] - (double)ref[k], 0.0, 0, 1});
+    return on;
+}
+__device__ __forceinline__ void put_constant(const PreferenceArgs &a, int64_t t, const Range &r, unsigned on, float g)
+{
+    float v[kQuadTokens];
+#pragma unroll
+    for (int k = 0; k < kQuadTokens; ++k)
+        v[k] = on >> k & 1 ? g : 0.0f;
+    store_quad(a.d_logprob, t, r, v);
+}
+// Pair p from its sequences' sums: writes its loss and rewards where `put`, returns
+// the gradient of the chosen (of the rejected) sequence's targets.
+__device__ __forceinline__ float pair_gradient(const PreferenceArgs &a, int64_t p, const SequencePart &chosen,
+                                               const SequencePart &rejected, bool put, bool of_rejected)
+{
+    const double wc = weight_of(a.seq, chosen.targets), wr = weight_of(a.seq, rejected.targets);
+    const double rc = a.beta * (chosen.a * wc), rr = a.beta * (rejected.a * wr);
     double loss, slope;
-    preference(a, reward[0] - reward[1] - a.margin, loss, slope);
-    if (a.loss && threadIdx.x == 0)
-        a.loss[p] = (float)loss;
+    preference(a, rc - rr - a.margin, loss, slope);
+    if (put) {
+        if (a.loss)
+            a.loss[p] = (float)loss;
+        if (a.reward)
+            a.reward[p] = (float)rc, a.reward[p + a.pairs] = (float)rr;
+    }
+    if (!a.d_logprob)
+        return 0.0f;
+    const double up = (double)a.d_loss[p] * slope * a.beta;
+    return (float)(of_rejected ? -up * wr : up * wc);
+}
+
+// A workgroup of NT threads to a pair, half of them to each sequence; up to 2 NT
+// positions of a sequence are read once.
+template <int NT>
+__global__ __launch_bounds__(NT) void preference_kernel(PreferenceArgs a)
+{
+    constexpr int Half = NT / 2, Waves = Half / kWave;
+    __shared__ SequencePart sh[2 * Waves], both[2];
+    const int64_t p = blockIdx.x;
+    const int side = threadIdx.x / Half;
+    const Range r = range_of(a.seq, p + side * a.pairs);
+    const int64_t t0 = r.lo / kQuadTokens * kQuadTokens + threadIdx.x % Half * kQuadTokens;
+    SequencePart sum{};
+    const unsigned held = ratio_quad(a, t0, r, sum);
+    for (int64_t t = t0 + Half * kQuadTokens; t < r.hi; t += Half * kQuadTokens)
+        ratio_quad(a, t, r, sum);
+    sum = waves_total(sum, sh, side * Waves, Waves);
+    if (threadIdx.x % Half == 0)
+        both[side] = sum;
+    __syncthreads();
+    const float g = pair_gradient(a, p, both[0], both[1], threadIdx.x == 0, side == 1);
     if (!a.d_logprob)
         return;
-    const double up = (double)a.d_loss[p] * slope * a.beta;
-    for (int i = 0; i < 2; ++i) {
-        const Range s = range_of(a.seq, p + i * a.pairs);
-        const float g = (float)((i ? -up : up) * w[i]);
-        for (int64_t t = s.lo + threadIdx.x; t < s.hi; t += kSeqBlock)
-            a.d_logprob[t] = is_target(a.seq, t) ? g : 0.0f;
+    put_constant(a, t0, r, held, g);
+    for (int64_t t = t0 + Half * kQuadTokens; t < r.hi; t += Half * kQuadTokens)
+        put_constant(a, t, r, targets_of(a.seq, t, r), g);
+}
+
+__global__ __launch_bounds__(kBlock) void preference_share_kernel(PreferenceArgs a)
+{
+    const int64_t slot = (int64_t)blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
+    if (slot >= a.seq.cut.slots)
+        return;
+    const Share h = share_of(a.seq, slot);
+    if (h.none || h.part.lo >= h.part.hi)
+        return;
+    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
+    SequencePart sum{};
+    for (int i = 0; i < a.seq.cut.rounds; ++i)
+        ratio_quad(a, begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens, h.part, sum);
+    sum = wave_total(sum);
+    if (threadIdx.x % kWave == 0)
+        a.seq.parts[slot] = sum;
+}
+__global__ __launch_bounds__(kBlock) void preference_join_kernel(PreferenceArgs a)
+{
+    const int64_t slot = (int64_t)blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
+    if (slot >= a.seq.cut.slots)
+        return;
+    const Share h = share_of(a.seq, slot);
+    const bool rejected = h.b >= a.pairs, put = h.first && !rejected;
+    const bool write = a.d_logprob && h.part.lo < h.part.hi;
+    if (h.none || !(put || write))
+        return;
+    const int64_t p = rejected ? h.b - a.pairs : h.b, o = rejected ? p : p + a.pairs;
+    const SequencePart own = total_of(a.seq, h.b, h.seq), other = total_of(a.seq, o, range_of(a.seq, o));
+    const float g = pair_gradient(a, p, rejected ? other : own, rejected ? own : other,
+                                  put && threadIdx.x % kWave == 0, rejected);
+    if (!write)
+        return;
+    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
+    for (int i = 0; i < a.seq.cut.rounds; ++i) {
+        const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
+        put_constant(a, t, h.part, targets_of(a.seq, t, h.part), g);
     }
+}
+
+// Threads of a workgroup that takes a sequence of `mean` positions on average.
+int threads_for(int64_t mean) { return mean <= 256 ? 64 : mean <= 1024 ? 256 : 1024; }
+
+unsigned share_groups(const Sequences &s)
+{
+    return (unsigned)((s.cut.slots + kBlock / kWave - 1) / (kBlock / kWave));
 }
 
 }  // namespace
 
 int launch_policy_loss(const PolicyArgs &a, void *stream)
 {
-    hipLaunchKernelGGL(policy_kernel, dim3((unsigned)a.seq.n), dim3(kSeqBlock), 0,
-                       reinterpret_cast<hipStream_t>(stream), a);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (a.seq.cut.slots > 0) {
+        hipLaunchKernelGGL(policy_share_kernel, dim3(share_groups(a.seq)), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL(policy_join_kernel, dim3(share_groups(a.seq)), dim3(kBlock), 0, st, a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)a.seq.n);
+    switch (threads_for(a.seq.n_tokens / a.seq.n)) {
+    case 64: hipLaunchKernelGGL((policy_kernel<64>), grid, dim3(64), 0, st, a); break;
+    case 256: hipLaunchKernelGGL((policy_kernel<256>), grid, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((policy_kernel<1024>), grid, dim3(1024), 0, st, a);
+    }
     return hipGetLastError();
 }
 
 int launch_preference_loss(const PreferenceArgs &a, void *stream)
 {
-    hipLaunchKernelGGL(preference_kernel, dim3((unsigned)a.pairs), dim3(kSeqBlock), 0,
-                       reinterpret_cast<hipStream_t>(stream), a);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (a.seq.cut.slots > 0) {
+        hipLaunchKernelGGL(preference_share_kernel, dim3(share_groups(a.seq)), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL(preference_join_kernel, dim3(share_groups(a.seq)), dim3(kBlock), 0, st, a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)a.pairs);
+    switch (threads_for(a.seq.n_tokens / a.seq.n)) {
+    case 64: hipLaunchKernelGGL((preference_kernel<128>), grid, dim3(128), 0, st, a); break;
+    case 256: hipLaunchKernelGGL((preference_kernel<512>), grid, dim3(512), 0, st, a); break;
+    default: hipLaunchKernelGGL((preference_kernel<1024>), grid, dim3(1024), 0, st, a);
+    }
     return hipGetLastError();
 }
 

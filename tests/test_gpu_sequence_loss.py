@@ -110,6 +110,29 @@ def test_policy(name, mode):
         check_policy(d, run_policy(d, **kw), **kw)
 
 
+def crowds():
+    """Many positions: one sequence, thousands of short ones, more than a search of
+    three levels tells apart."""
+    g = np.random.default_rng(3)
+    return {"single": [300001], "thousands": g.integers(0, 17, 5000), "swarm": g.integers(0, 3, 70000),
+            "gaps": [0] * 70 + [20000] + [0] * 4100 + [5] + [0] * 3}
+
+
+@pytest.mark.parametrize("name", crowds())
+def test_policy_of_many_positions(name):
+    d = make(70, crowds()[name], lead=1, tail=2)
+    for kw in (dict(mode="mean"), dict(mode="sum", per_token=False, with_ref=False, shift=1)):
+        check_policy(d, run_policy(d, **kw), **kw)
+
+
+@pytest.mark.parametrize("name", crowds())
+def test_preference_of_many_positions(name):
+    lengths = crowds()[name]
+    d = make(71, list(lengths) + [7] * (len(lengths) % 2), lead=1, tail=2)
+    for kw in (dict(mode="mean", beta=0.5), dict(mode="sum", with_ref=False, shift=1, kind="squared")):
+        check_preference(d, run_preference(d, **kw), **kw)
+
+
 def test_policy_outputs_alone_and_forward_only():
     d = make(5, LENGTHS["uneven"])
     full = run_policy(d)
