@@ -934,15 +934,15 @@ def _on_device(t, dev: int, what: str):
         raise ValueError(f"{what} is on {t.device}, the logits on cuda:{dev}")
 
 
-def _row_values(t, n: int, dev: int, what: str, dtype=None):
+def _row_values(t, n: int, dev: int, what: str, dtype=torch.float32):
     """Address of a contiguous device tensor of exactly n values (None: NULL)."""
     if t is None:
         return None
-    dtype = dtype or _torch().float32
-    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype:
-        raise TypeError(f"{what} must be a {dtype} tensor, got {getattr(t, 'dtype', type(t))}")
-    if t.get_device() == dev and t.numel() == n and t.is_contiguous():
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.numel() == n
+            and t.is_contiguous()):
         return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{what} must be a {dtype} tensor, got {getattr(t, 'dtype', type(t))}")
     _dev_ptr(t, what)
     _on_device(t, dev, what)
     raise ValueError(f"{what} holds {t.numel()} values; the call needs {n}")
@@ -958,9 +958,10 @@ def _d_logits(t, logits):
 def _workspace(t, dev: int):
     if t is None:
         return None, 0
-    ptr = _dev_ptr(t, "workspace")
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), t.nbytes
+    _dev_ptr(t, "workspace")
     _on_device(t, dev, "workspace")
-    return ptr, t.numel() * t.element_size()
 
 
 def _top(index, value, rows: int, dev: int, what):
@@ -972,14 +973,14 @@ def _top(index, value, rows: int, dev: int, what):
     if index.dim() != 2 or index.shape != value.shape or index.shape[0] != rows:
         raise ValueError(f"{what[0]} and {what[1]} must have shape (rows, top_k)")
     k = index.shape[1]
-    return (k, _row_values(index, rows * k, dev, what[0], _torch().int32),
+    return (k, _row_values(index, rows * k, dev, what[0], torch.int32),
             _row_values(value, rows * k, dev, what[1]))
 
 
 def _stream_on(stream, dev: int):
     """_stream, the current stream's handle without an object around it."""
     if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
 
 
@@ -992,7 +993,7 @@ def zero_logprob(logits, tokens=None, *, scale: float = 1.0, logprob=None, entro
     p, dt, n, v, st, dev = _logits(logits)
     k, ip, tp = _top(top_index, top_logprob, n, dev, ("top_index", "top_logprob"))
     wp, wb = _workspace(workspace, dev)
-    _check(_zero_logprob(p, dt, n, v, st, scale, _row_values(tokens, n, dev, "tokens", _torch().int64),
+    _check(_zero_logprob(p, dt, n, v, st, scale, _row_values(tokens, n, dev, "tokens", torch.int64),
                          _row_values(logprob, n, dev, "logprob"),
                          _row_values(entropy, n, dev, "entropy"),
                          _row_values(stats, 2 * n, dev, "stats"), k, ip, tp, wp, wb, _stream_on(stream, dev)),
@@ -1007,7 +1008,7 @@ def zero_logprob_grad(logits, tokens, stats, d_logits, *, scale: float = 1.0, d_
     p, dt, n, v, st, dev = _logits(logits)
     gp, gs = _d_logits(d_logits, logits)
     _check(_zero_logprob_grad(p, dt, n, v, st, scale,
-                              _row_values(tokens, n, dev, "tokens", _torch().int64),
+                              _row_values(tokens, n, dev, "tokens", torch.int64),
                               _row_values(stats, 2 * n, dev, "stats"),
                               _row_values(entropy, n, dev, "entropy"),
                               _row_values(d_logprob, n, dev, "d_logprob"),
@@ -1023,7 +1024,7 @@ def zero_logprob_fused(logits, tokens, d_logits, *, scale: float = 1.0, d_logpro
     gp, gs = _d_logits(d_logits, logits)
     wp, wb = _workspace(workspace, dev)
     _check(_zero_logprob_fused(p, dt, n, v, st, scale,
-                               _row_values(tokens, n, dev, "tokens", _torch().int64),
+                               _row_values(tokens, n, dev, "tokens", torch.int64),
                                _row_values(d_logprob, n, dev, "d_logprob"),
                                _row_values(d_entropy, n, dev, "d_entropy"),
                                _row_values(logprob, n, dev, "logprob"),
@@ -1078,13 +1079,12 @@ def zero_distill_fused(logits, top_index, top_value, mode: int, d_loss, d_logits
 def _on_current_device(t, what: str) -> int:
     """Index of the device of a tensor that names it for the call, which must be
     the current one (the calls run on its streams)."""
-    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch tensor")
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a device tensor (got {t.device})")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{what} is on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return dev
@@ -1105,9 +1105,8 @@ def _sequences(logprob, offsets, tokens):
     n, b = logprob.numel(), offsets.numel() - 1
     if b < 0:
         raise ValueError("offsets must hold the sequences' starts and the last one's end")
-    i64t = _torch().int64
-    return (dev, n, b, _row_values(offsets, b + 1, dev, "offsets", i64t),
-            _row_values(tokens, n, dev, "tokens", i64t))
+    return (dev, n, b, _row_values(offsets, b + 1, dev, "offsets", torch.int64),
+            _row_values(tokens, n, dev, "tokens", torch.int64))
 
 
 def zero_policy_loss(logprob, old_logprob, advantage, offsets, *, tokens=None, ref_logprob=None,
@@ -1131,7 +1130,7 @@ def zero_policy_loss(logprob, old_logprob, advantage, offsets, *, tokens=None, r
                              int(per_token), tok, n, off, b, clip_low, clip_high, kl_coef, mode,
                              _row_values(d_loss, b, dev, "d_loss"), _row_values(loss, b, dev, "loss"),
                              _row_values(kl, b, dev, "kl"),
-                             _row_values(clipped, b, dev, "clipped", _torch().int32),
+                             _row_values(clipped, b, dev, "clipped", torch.int32),
                              _row_values(d_logprob, n, dev, "d_logprob"), wp, wb,
                              _stream_on(stream, dev)), "zero_policy_loss")
 
@@ -1162,12 +1161,12 @@ def zero_preference_loss(logprob, offsets, *, tokens=None, ref_logprob=None,
 def _matrix(t, dev: int, what: str, rows=None, cols=None):
     """(address, dtype, rows, cols, row stride) of a 2-D device tensor, bfloat16
     or float32, whose rows are contiguous; of the given shape where one is given."""
-    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch tensor")
-    dt = ZERO_BF16 if t.dtype is torch.bfloat16 else ZERO_F32 if t.dtype is torch.float32 else None
+    dtype = t.dtype
+    dt = ZERO_BF16 if dtype is torch.bfloat16 else ZERO_F32 if dtype is torch.float32 else None
     if dt is None:
-        raise TypeError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+        raise TypeError(f"{what} must be bfloat16 or float32, got {dtype}")
     ptr, stride = _rows_of(t, what)
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, the call runs on cuda:{dev}")
@@ -1185,7 +1184,7 @@ def zero_embedding(table, tokens, out, *, scale: float = 1.0, stream=None):
     dev = _on_current_device(table, "table")
     tp, tdt, v, h, ts = _matrix(table, dev, "table")
     op, odt, n, _, os_ = _matrix(out, dev, "out", cols=h)
-    _check(_zero_embedding(tp, tdt, v, h, ts, _row_values(tokens, n, dev, "tokens", _torch().int64), n,
+    _check(_zero_embedding(tp, tdt, v, h, ts, _row_values(tokens, n, dev, "tokens", torch.int64), n,
                            scale, op, odt, os_, _stream_on(stream, dev)), "zero_embedding")
 
 
@@ -1207,7 +1206,7 @@ def zero_embedding_grad(d_out, tokens, d_table, *, scale: float = 1.0, accumulat
     gp, gdt, n, h, gs = _matrix(d_out, dev, "d_out")
     tp, tdt, v, _, ts = _matrix(d_table, dev, "d_table", cols=h)
     wp, wb = _workspace(workspace, dev)
-    _check(_zero_embedding_grad(gp, gdt, n, h, gs, _row_values(tokens, n, dev, "tokens", _torch().int64),
+    _check(_zero_embedding_grad(gp, gdt, n, h, gs, _row_values(tokens, n, dev, "tokens", torch.int64),
                                 scale, tp, tdt, v, ts, int(accumulate), wp, wb,
                                 _stream_on(stream, dev)), "zero_embedding_grad")
 
@@ -1216,13 +1215,12 @@ def zero_embedding_grad(d_out, tokens, d_table, *, scale: float = 1.0, accumulat
 
 def _checkpoint(codes, scales, rows: int, cols: int, dev: int):
     """Addresses of a checkpoint's codes and scales."""
-    u8 = _torch().uint8
     blocks = (cols + ZERO_ACT8_BLOCK - 1) // ZERO_ACT8_BLOCK
     for t, n, what in ((codes, cols, "codes"), (scales, blocks, "scales")):
         if t.shape != (rows, n):
             raise ValueError(f"{what} has shape {tuple(t.shape)}; the call needs ({rows}, {n})")
-    return (_row_values(codes, rows * cols, dev, "codes", u8),
-            _row_values(scales, rows * blocks, dev, "scales", u8))
+    return (_row_values(codes, rows * cols, dev, "codes", torch.uint8),
+            _row_values(scales, rows * blocks, dev, "scales", torch.uint8))
 
 
 def zero_act8_pack(x, codes, scales, stream=None):

@@ -21,7 +21,6 @@ using namespace dev;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kRows = 64;   // rows r of a tile

@@ -235,41 +235,61 @@ __device__ __forceinline__ float *part_of(const EmbeddingGradArgs &a, int segmen
     return a.parts + ((int64_t)segment * 2 + tail) * a.columns + c;
 }
 
-// One wave per segment of the sorted list and 512 columns.
+// Rows whose loads are on their way at once.
+constexpr int kBatch = 8;
+
+// One wave per segment of the sorted list and 512 columns.  Lane e has the segment's
+// entry e.
 template <typename T, typename O>
 __global__ __launch_bounds__(kBlock) void segment_sum_kernel(EmbeddingGradArgs a)
 {
     const int lane = threadIdx.x % kWave;
     const int s = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave));
     const int c = (int)(blockIdx.y * kWave + lane) * kOct, n = min(a.hidden - c, kOct);
-    const int lo = s * a.segment;
-    if (s >= a.segments || n <= 0)
+    if (s >= a.segments)
         return;
-    const int hi = min(lo + a.segment, a.rows);
+    const int lo = s * a.segment, entries = min(a.segment, a.rows - lo);
+    // the entries' tokens and rows, the tokens beside the segment (-1: none)
+    const int e = lo + min(lane, entries - 1);
+    const uint32_t key = a.key[e], row = a.row[e];
+    const uint32_t before = lo > 0 ? a.key[lo - 1] : ~0u, after = lo + entries < a.rows ? a.key[lo + entries] : ~0u;
     const T *d_out = static_cast<const T *>(a.d_out) + c;
-    uint32_t run = a.key[lo];
-    const bool before = lo > 0 && a.key[lo - 1] == run;
-    bool first = true;
     float sum[kOct] = {};
-    for (int e = lo; e < hi && run < (uint32_t)a.vocab; ++e) {
-        float x[kOct];
-        load_n(d_out + (int64_t)a.row[e] * a.stride, n, x);
+    uint32_t run = __builtin_amdgcn_readlane(key, 0);
+    bool cut = before == run;
+    for (int e0 = 0; e0 < entries; e0 += kBatch) {
+        float x[kBatch][kOct];
 #pragma unroll
-        for (int k = 0; k < kOct; ++k)
-            sum[k] += x[k];
-        const uint32_t next = e + 1 < a.rows ? a.key[e + 1] : ~0u;
-        if (e + 1 < hi && next == run)
-            continue;
-        const bool cut = first && before, goes_on = next == run;
-        if (cut || goes_on)
-            store8(part_of(a, s, !cut, c), sum);
-        else
-            put<O>(a, run, c, n, sum);
-        first = false;
-        run = next;
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = e0 + i;
+            const uint32_t k = __builtin_amdgcn_readlane(key, j & (kWave - 1));
+            if (j < entries && k < (uint32_t)a.vocab)
+                load_n(d_out + (int64_t)(uint32_t)__builtin_amdgcn_readlane(row, j & (kWave - 1)) * a.stride, n, x[i]);
+        }
 #pragma unroll
-        for (int k = 0; k < kOct; ++k)
-            sum[k] = 0.0f;
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = e0 + i;
+            if (j >= entries || run >= (uint32_t)a.vocab)
+                break;
+#pragma unroll
+            for (int k = 0; k < kOct; ++k)
+                sum[k] += x[i][k];
+            const uint32_t next = j + 1 < entries ? (uint32_t)__builtin_amdgcn_readlane(key, (j + 1) & (kWave - 1)) : after;
+            if (next == run && j + 1 < entries)
+                continue;
+            // the run ends here, or in another segment
+            if (n > 0) {
+                if (cut || next == run)
+                    store8(part_of(a, s, !cut, c), sum);
+                else
+                    put<O>(a, run, c, n, sum);
+            }
+            cut = false;
+            run = next;
+#pragma unroll
+            for (int k = 0; k < kOct; ++k)
+                sum[k] = 0.0f;
+        }
     }
 }
 
@@ -284,16 +304,35 @@ __global__ __launch_bounds__(kBlock) void join_runs_kernel(EmbeddingGradArgs a)
     if (s >= a.segments - 1 || n <= 0)
         return;
     const int lo = s * a.segment, next = lo + a.segment;
-    const uint32_t run = a.key[next - 1];
-    if (run >= (uint32_t)a.vocab || a.key[next] != run || (lo > 0 && a.key[lo - 1] == run))
+    const uint32_t run = a.key[next - 1], begins = a.key[next], before = lo > 0 ? a.key[lo - 1] : ~0u;
+    if (run >= (uint32_t)a.vocab || begins != run || before == run)
         return;
-    float sum[kOct], x[kOct];
+    // the last segment that begins with the run: in steps that double, then halve
+    int last = s + 1, step = 1;
+    auto has = [&](int q) { return q < a.segments && a.key[q * a.segment] == run; };
+    for (; has(last + step); step *= 2)
+        last += step;
+    for (step /= 2; step > 0; step /= 2)
+        if (has(last + step))
+            last += step;
+    float sum[kOct], x[kBatch][kOct];
     load8(part_of(a, s, 1, c), sum);
-    for (int q = s + 1; q < a.segments && a.key[q * a.segment] == run; ++q) {
-        load8(part_of(a, q, 0, c), x);
+    int q = s + 1;
+    for (; q + kBatch <= last + 1; q += kBatch) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            load8(part_of(a, q + i, 0, c), x[i]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int k = 0; k < kOct; ++k)
+                sum[k] += x[i][k];
+    }
+    for (; q <= last; ++q) {
+        load8(part_of(a, q, 0, c), x[0]);
 #pragma unroll
         for (int k = 0; k < kOct; ++k)
-            sum[k] += x[k];
+            sum[k] += x[0][k];
     }
     put<O>(a, run, c, n, sum);
 }
@@ -335,7 +374,11 @@ void embedding_grad_of(const EmbeddingGradArgs &a, hipStream_t st)
 
 }  // namespace
 
-int32_t embedding_segment(int64_t rows, int64_t hidden) { return 32; }
+int32_t embedding_segment(int64_t rows, int64_t hidden)
+{
+    const int64_t slabs = (hidden + kOct * kWave - 1) / (kOct * kWave);
+    return rows > 32 && rows * slabs <= 32768 ? 8 : 32;
+}
 
 int launch_embedding(const EmbeddingArgs &a, void *stream)
 {

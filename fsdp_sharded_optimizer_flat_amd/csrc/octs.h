@@ -7,6 +7,7 @@
 namespace zero {
 namespace dev {
 
+typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 

@@ -166,6 +166,39 @@ __device__ __forceinline__ SequencePart total_of(const Sequences &s, int64_t b, 
 
 // -- policy ---------------------------------------------------------------------------
 
+// e^x, e^x - 1 and e^x - 1 - x: x = n ln 2 + f, |f| <= ln(2) / 2, and the exponential's
+// series in f to its 11th power, whose rest is below 2^-47 (of the results, which are
+// rounded to binary32 in the end: 2^-24).  A third of the library functions' time, which
+// weighed more than the memory's.  Where n = 0 the last two are the series without its
+// first terms, and nothing cancels.
+struct Exponential {
+    double e, less1, rest;
+};
+__device__ __forceinline__ Exponential exponential(double x)
+{
+    constexpr double kLog2E = 1.4426950408889634074;
+    constexpr double kLn2Hi = 0x1.62e42fefa39efp-1, kLn2Lo = 0x1.abc9e3b39803fp-56;
+    const double y = x > 800.0 ? 800.0 : x < -800.0 ? -800.0 : x;   // NaN stays
+    const double n = __builtin_rint(y * kLog2E);
+    const double f = __builtin_fma(-n, kLn2Lo, __builtin_fma(-n, kLn2Hi, y));
+    double q = 1.0 / 39916800.0;
+    q = __builtin_fma(q, f, 1.0 / 3628800.0);
+    q = __builtin_fma(q, f, 1.0 / 362880.0);
+    q = __builtin_fma(q, f, 1.0 / 40320.0);
+    q = __builtin_fma(q, f, 1.0 / 5040.0);
+    q = __builtin_fma(q, f, 1.0 / 720.0);
+    q = __builtin_fma(q, f, 1.0 / 120.0);
+    q = __builtin_fma(q, f, 1.0 / 24.0);
+    q = __builtin_fma(q, f, 1.0 / 6.0);
+    q = __builtin_fma(q, f, 0.5);
+    const double rest = f * f * q;
+    Exponential r;
+    r.e = __builtin_ldexp(1.0 + (f + rest), (int)n);
+    r.less1 = n == 0.0 ? f + rest : r.e - 1.0;
+    r.rest = n == 0.0 ? rest : r.less1 - x;
+    return r;
+}
+
 struct Term {
     double loss, kl, slope;
     int cut;
@@ -173,7 +206,7 @@ struct Term {
 __device__ __forceinline__ Term policy_term(const PolicyArgs &a, float lp, float old, float ref, float adv)
 {
     const double d = (double)lp - (double)old, A = adv;
-    const double r = exp(d);
+    const double r = exponential(d).e;
     const bool above = A > 0.0 && d > a.log_high, below = A < 0.0 && d < a.log_low;
     Term t;
     t.cut = above || below;
@@ -181,11 +214,12 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs &a, float lp, float
     t.slope = t.cut ? 0.0 : -A * r;
     t.kl = 0.0;
     if (a.ref_logprob) {
-        const double x = (double)ref - (double)lp, e = expm1(x);
-        t.kl = x == __builtin_inf() ? x : e - x;
+        const double x = (double)ref - (double)lp;
+        const Exponential e = exponential(x);
+        t.kl = x == __builtin_inf() ? x : e.rest;
         if (a.kl_coef != 0.0) {
             t.loss += a.kl_coef * t.kl;
-            t.slope -= a.kl_coef * e;
+            t.slope -= a.kl_coef * e.less1;
         }
     }
     return t;
@@ -445,8 +479,9 @@ __global__ __launch_bounds__(kBlock) void preference_join_kernel(PreferenceArgs 
     }
 }
 
-// Threads of a workgroup that takes a sequence of `mean` positions on average.
-int threads_for(int64_t mean) { return mean <= 256 ? 64 : mean <= 1024 ? 256 : 1024; }
+// Threads of a workgroup that takes a sequence of `mean` positions on average; some
+// are several times as long.
+int threads_for(int64_t mean) { return mean <= 32 ? 64 : mean <= 512 ? 256 : 1024; }
 
 unsigned share_groups(const Sequences &s)
 {

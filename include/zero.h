@@ -772,7 +772,7 @@ zero_status zero_preference_loss(const float *logprob, const float *ref_logprob,
  * (or added onto) its place in the unit's gradient bucket.
  *
  *     out_r = scale table[token_r]
- *     d_table[v] (+)= scale sum_{r: token_r = v} d_out_r     in ascending order of r
+ *     d_table[v] (+)= scale sum_{r: token_r = v} d_out_r
  *
  * A negative token is a padding row: its out row is zero, its d_out row is not
  * read.  A token >= vocab gives a NaN out row (as in the token losses, so that the
@@ -780,8 +780,8 @@ zero_status zero_preference_loss(const float *logprob, const float *ref_logprob,
  *
  * Tables and activations are ZERO_F32 or ZERO_BF16 each, in rows of `hidden`
  * elements, row r at base + r * stride; elements past a row's hidden stay as they
- * are.  Sums are binary32, in an order that the sizes alone decide (the same call
- * gives the same bits); each output is rounded once.  accumulate = 0 writes the
+ * are.  Sums are binary32, of rows in ascending order, a token's many rows in parts
+ * (the same call gives the same bits); each output is rounded once.  accumulate = 0 writes the
  * whole of d_table, zeros where no token names a row; accumulate = 1 adds to the
  * rows that tokens name (one more rounding) and leaves the others as they are.
  *
