@@ -48,6 +48,40 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[kOct])
     *reinterpret_cast<f32x4_at4 *>(p) = f32x4{x[0], x[1], x[2], x[3]};
     *reinterpret_cast<f32x4_at4 *>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
 }
+// Eight elements as they lie in memory.
+template <typename T>
+struct RawOct;
+template <>
+struct RawOct<uint16_t> {
+    u32x4 a;
+    __device__ __forceinline__ void load(const uint16_t *p) { a = *reinterpret_cast<const u32x4_at2 *>(p); }
+    __device__ __forceinline__ void load(const uint16_t *p, int n)   // the first n
+    {
+#pragma unroll
+        for (int k = 0; k < kOct / 2; ++k)
+            a[k] = (2 * k < n ? p[2 * k] : 0u) | (2 * k + 1 < n ? (unsigned)p[2 * k + 1] << 16 : 0u);
+    }
+    __device__ __forceinline__ float at(int k) const { return k % 2 ? bf_hi(a[k / 2]) : bf_lo(a[k / 2]); }
+};
+template <>
+struct RawOct<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = *reinterpret_cast<const f32x4_at4 *>(p), b = *reinterpret_cast<const f32x4_at4 *>(p + 4);
+    }
+    __device__ __forceinline__ void load(const float *p, int n)
+    {
+#pragma unroll
+        for (int k = 0; k < kOct; ++k)
+            if (k < 4)
+                a[k] = k < n ? p[k] : 0.0f;
+            else
+                b[k - 4] = k < n ? p[k] : 0.0f;
+    }
+    __device__ __forceinline__ float at(int k) const { return k < 4 ? a[k] : b[k - 4]; }
+};
+
 // The first n of them (all eight, or the end of a row).
 template <typename T>
 __device__ __forceinline__ void load_n(const T *p, int n, float (&x)[kOct])
