@@ -3,6 +3,7 @@
 // device work.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "call_check.h"
@@ -12,12 +13,13 @@ namespace zero {
 namespace {
 
 struct Workspace {
-    int64_t chunk_key = 0, chunk_row = 0, key = 0, row = 0, parts = 0, bytes = 0;
-    int32_t segment = 0, segments = 0, columns = 0;
+    int64_t chunk_key = 0, chunk_row = 0, samples = -1, key = 0, row = 0, parts = 0, bytes = 0;
+    int32_t chunk = 0, segment = 0, segments = 0, columns = 0;
 };
-Workspace workspace_layout(int64_t rows, int64_t hidden)
+Workspace workspace_layout(int64_t rows, int64_t hidden, int32_t chunk)
 {
     Workspace w;
+    w.chunk = chunk;
     w.segment = embedding_segment(rows, hidden);
     w.segments = (int32_t)((rows + w.segment - 1) / w.segment);
     w.columns = (int32_t)((hidden + 7) / 8 * 8);
@@ -26,7 +28,8 @@ Workspace workspace_layout(int64_t rows, int64_t hidden)
     w.chunk_key = at, at += list;
     w.chunk_row = at, at += list;
     w.key = w.chunk_key, w.row = w.chunk_row;
-    if (rows > kSortChunk) {
+    if (rows > w.chunk) {
+        w.samples = at, at += (rows + w.chunk - 1) / w.chunk * kSamples * 4;
         w.key = at, at += list;
         w.row = at, at += list;
     }
@@ -91,7 +94,9 @@ extern "C" zero_status zero_embedding_grad_workspace_bytes(int64_t rows, int64_t
         return ZERO_EINVAL;
     if (zero_status s = check_sizes(rows, vocab, hidden, ZERO_MAX_EMBEDDING_ROWS))
         return s;
-    *bytes = (size_t)workspace_layout(rows, hidden).bytes;
+    // the call chooses by more than these sizes
+    *bytes = (size_t)std::max(workspace_layout(rows, hidden, kSortChunk).bytes,
+                              workspace_layout(rows, hidden, kMaxSortChunk).bytes);
     return ZERO_OK;
 }
 
@@ -111,7 +116,8 @@ extern "C" zero_status zero_embedding_grad(const void *d_out, int32_t dtype, int
         return ZERO_EINVAL;
     if (!stride_fits(rows, row_stride) || !stride_fits(vocab, table_stride))
         return ZERO_ERANGE;
-    const Workspace w = workspace_layout(rows, hidden);
+    const int64_t cleared = accumulate ? 0 : vocab * hidden * esize(table_dtype);
+    const Workspace w = workspace_layout(rows, hidden, embedding_chunk(rows, cleared));
     if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, w.bytes))
         return s;
     const Span in[] = {matrix(d_out, rows, hidden, row_stride, esize(dtype)), vec(tokens, rows, 8)};
@@ -138,10 +144,12 @@ extern "C" zero_status zero_embedding_grad(const void *d_out, int32_t dtype, int
     if (rows > 0) {
         a.chunk_key = reinterpret_cast<uint32_t *>(base + w.chunk_key);
         a.chunk_row = reinterpret_cast<uint32_t *>(base + w.chunk_row);
+        a.samples = w.samples < 0 ? nullptr : reinterpret_cast<uint32_t *>(base + w.samples);
         a.key = reinterpret_cast<uint32_t *>(base + w.key);
         a.row = reinterpret_cast<uint32_t *>(base + w.row);
         a.parts = reinterpret_cast<float *>(base + w.parts);
     }
+    a.chunk = w.chunk;
     a.segment = w.segment;
     a.segments = w.segments;
     a.columns = w.columns;

@@ -18,8 +18,18 @@ struct EmbeddingArgs {
 };
 int launch_embedding(const EmbeddingArgs &a, void *stream);
 
-// Tokens one workgroup sorts.
-constexpr int kSortChunk = 8192;
+// Tokens one workgroup sorts: powers of two.  Sorting takes 11 us for chunks of 2048
+// and 26 for 8192, putting chunks together 7 us for up to eight of them and 6 more for
+// eight more, so small chunks serve up to 65536 tokens, unless a gradient of 128 MB or
+// more is cleared meanwhile, which takes longer than either (16384 x 4096 bf16 into
+// 128256 rows 238 us with large chunks, 245 with small ones; added to what is there, 76
+// and 67).
+constexpr int kSortChunk = 2048, kMaxSortChunk = 8192;
+constexpr int kSamples = 128;   // of a sorted chunk's tokens, at even distances
+inline int32_t embedding_chunk(int64_t rows, int64_t cleared_bytes)
+{
+    return rows > 65536 || cleared_bytes >= int64_t(1) << 27 ? kMaxSortChunk : kSortChunk;
+}
 
 struct EmbeddingGradArgs {
     const void *d_out;
@@ -32,9 +42,9 @@ struct EmbeddingGradArgs {
     // Workspace: the tokens in ascending order with their rows (sorted in chunks,
     // then as a whole), and the partial sums of runs that segments cut:
     // segments x 2 x padded columns.
-    uint32_t *chunk_key, *chunk_row, *key, *row;
+    uint32_t *chunk_key, *chunk_row, *samples, *key, *row;
     float *parts;
-    int32_t segment, segments, columns;
+    int32_t chunk, segment, segments, columns;
 };
 int launch_embedding_grad(const EmbeddingGradArgs &a, void *stream);
 

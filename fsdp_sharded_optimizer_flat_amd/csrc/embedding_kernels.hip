@@ -9,6 +9,7 @@
 // are (one token named by every row too), no atomics decide an order, and each
 // row of the gradient is rounded once.
 #include <algorithm>
+#include <type_traits>
 
 #include "embedding.h"
 #include "octs.h"
@@ -47,17 +48,17 @@ __global__ __launch_bounds__(kBlock) void embedding_kernel(EmbeddingArgs a, int6
 
 constexpr int kSortBlock = 1024, kSortWaves = kSortBlock / kWave;
 constexpr int kDigit = 7, kDigits = 1 << kDigit;   // three passes hold ZERO_MAX_VOCAB and one more
-constexpr int kPerThread = kSortChunk / kSortBlock;
+constexpr int kPerThread = kMaxSortChunk / kSortBlock;
 static_assert(ZERO_MAX_VOCAB < 1 << (3 * kDigit), "a token and the mark of no token fit three digits");
 
 struct SortShared {
-    uint32_t key[kSortChunk];
-    uint16_t at[kSortChunk];
+    uint32_t key[kMaxSortChunk];
+    uint16_t at[kMaxSortChunk];
     uint32_t count[kDigits * kSortWaves];   // [digit][wave]
     uint32_t wave_sum[kSortWaves];
 };
 
-// Sorts n <= kSortChunk tokens by value, stable, by digits from the lowest: a
+// Sorts n <= kMaxSortChunk tokens by value, stable, by digits from the lowest: a
 // wave ranks 64 neighbours by a digit with one ballot per bit, a scan over (digit,
 // wave) places them.
 __device__ void sort_chunk(const EmbeddingGradArgs &a, int first, int n, SortShared &sh)
@@ -138,6 +139,10 @@ __device__ void sort_chunk(const EmbeddingGradArgs &a, int first, int n, SortSha
         a.chunk_key[first + p] = sh.key[p];
         a.chunk_row[first + p] = (uint32_t)(first + sh.at[p]);
     }
+    if (a.samples && tid < kSamples) {
+        const int p = (tid + 1) * (a.chunk / kSamples) - 1;
+        a.samples[first / a.chunk * kSamples + tid] = p < n ? sh.key[p] : ~0u;
+    }
 }
 
 // Elements of the gradient that a workgroup clears.
@@ -152,8 +157,8 @@ __global__ __launch_bounds__(kSortBlock) void sort_and_clear_kernel(EmbeddingGra
 {
     __shared__ SortShared sh;
     if ((int)blockIdx.x < chunks) {
-        const int first = blockIdx.x * kSortChunk;
-        sort_chunk(a, first, min(a.rows - first, kSortChunk), sh);
+        const int first = blockIdx.x * a.chunk;
+        sort_chunk(a, first, min(a.rows - first, a.chunk), sh);
         return;
     }
     const int64_t span = (int64_t)(blockIdx.x - chunks) * kClearOcts;
@@ -181,37 +186,55 @@ __global__ __launch_bounds__(kSortBlock) void sort_and_clear_kernel(EmbeddingGra
     }
 }
 
-// Number of keys in k[0..n) below x (or, with EQUAL, not above it).
-template <bool EQUAL>
-__device__ __forceinline__ int keys_below(const uint32_t *k, int n, uint32_t x)
-{
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (EQUAL ? k[mid] <= x : k[mid] < x)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
 // Each sorted chunk's entries to their place in the whole list: what is below them
-// in the other chunks (equal tokens of earlier chunks come first).
+// in the other chunks (equal tokens of earlier chunks come first), first among the
+// chunks' samples, in LDS, then in the stretch between two of them.  Eight chunks are
+// searched at once, so that their loads wait together.
 __global__ __launch_bounds__(kBlock) void merge_chunks_kernel(EmbeddingGradArgs a, int chunks)
 {
+    constexpr int Together = 8;
+    extern __shared__ uint32_t samples[];   // chunks x kSamples
+    for (int i = threadIdx.x; i < chunks * kSamples; i += kBlock)
+        samples[i] = a.samples[i];
+    __syncthreads();
     const int i = blockIdx.x * kBlock + threadIdx.x;
     if (i >= a.rows)
         return;
     const uint32_t x = a.chunk_key[i];
-    const int own = i / kSortChunk;
-    int place = i - own * kSortChunk;
-    for (int c = 0; c < chunks; ++c) {
-        const int first = c * kSortChunk, n = min(a.rows - first, kSortChunk);
-        if (c < own)
-            place += keys_below<true>(a.chunk_key + first, n, x);
-        else if (c > own)
-            place += keys_below<false>(a.chunk_key + first, n, x);
+    const int own = i / a.chunk, stretch = a.chunk / kSamples;   // powers of two
+    int place = i - own * a.chunk;
+    for (int c0 = 0; c0 < chunks; c0 += Together) {
+        int below[Together], size[Together];
+        const uint32_t *keys[Together];
+        bool earlier[Together];
+        auto is_below = [&](int t, uint32_t k) { return earlier[t] ? k <= x : k < x; };
+#pragma unroll
+        for (int t = 0; t < Together; ++t) {
+            const int c = min(c0 + t, chunks - 1);
+            keys[t] = a.chunk_key + c * a.chunk;
+            size[t] = c0 + t < chunks && c != own ? min(a.rows - c * a.chunk, a.chunk) : 0;
+            earlier[t] = c < own;
+            const uint32_t *sample = samples + c * kSamples;
+            int n = 0;
+#pragma unroll
+            for (int step = kSamples / 2; step > 0; step /= 2)
+                n += is_below(t, sample[n + step - 1]) ? step : 0;
+            n += is_below(t, sample[n]);   // all of them, too
+            below[t] = size[t] ? n * stretch : 0;
+        }
+        for (int step = stretch / 2; step > 0; step /= 2) {
+            uint32_t k[Together];
+#pragma unroll
+            for (int t = 0; t < Together; ++t)   // are the chunk's first below + step keys all below?
+                k[t] = keys[t][min(below[t] + step, max(size[t], 1)) - 1];
+#pragma unroll
+            for (int t = 0; t < Together; ++t)
+                if (below[t] + step <= size[t] && is_below(t, k[t]))
+                    below[t] += step;
+        }
+#pragma unroll
+        for (int t = 0; t < Together; ++t)
+            place += below[t];
     }
     a.key[place] = x;
     a.row[place] = a.chunk_row[i];
@@ -219,27 +242,49 @@ __global__ __launch_bounds__(kBlock) void merge_chunks_kernel(EmbeddingGradArgs 
 
 // -- sums over sorted tokens -----------------------------------------------------------------
 
-// A token's finished sum to its row of the gradient, columns from c on: eight, or n of
-// them from element `shift` on.
-template <typename O>
-__device__ __forceinline__ void put(const EmbeddingGradArgs &a, uint32_t token, int c, int shift, int n,
-                                    const float (&sum)[kOct])
+// The columns that a lane works on: eight from `from` on, of which n from element
+// `shift` on are its own (at a row's end the last eight; of a row of fewer than eight,
+// those).  whole: every lane of the wave has eight of its own.
+struct Columns {
+    int from, shift, n;
+    bool whole, narrow;
+    __device__ __forceinline__ Columns(int hidden, int slab)
+    {
+        const int c = (slab * kWave + (int)threadIdx.x % kWave) * kOct;
+        narrow = hidden < kOct;
+        from = narrow ? 0 : min(c, hidden - kOct);
+        shift = narrow && c > 0 ? kOct : c - from;
+        n = min(hidden - c, kOct);
+        whole = (slab + 1) * kWave * kOct <= hidden;
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, RawOct<T> &x) const
+    {
+        if (narrow)
+            x.load(row, n);
+        else
+            x.load(row + from);
+    }
+};
+
+// A token's finished sum to its row of the gradient, added to `was`, what is there,
+// where accumulated.
+template <typename O, bool ACC>
+__device__ __forceinline__ void put(const EmbeddingGradArgs &a, O *row, const Columns &c, const float (&sum)[kOct],
+                                    const RawOct<O> &was)
 {
-    O *p = static_cast<O *>(a.d_table) + (int64_t)token * a.table_stride + c;
-    if (n >= kOct) {
-        float x[kOct];
-        if (a.accumulate)
-            load8(p, x);
+    float x[kOct];
 #pragma unroll
-        for (int k = 0; k < kOct; ++k)
-            x[k] = a.accumulate ? x[k] + a.scale * sum[k] : a.scale * sum[k];
-        store8(p, x);
+    for (int k = 0; k < kOct; ++k)
+        x[k] = ACC ? was.at(k) + a.scale * sum[k] : a.scale * sum[k];
+    if (c.whole) {
+        store8(row + c.from, x);
         return;
     }
 #pragma unroll
     for (int k = 0; k < kOct; ++k)
-        if (k >= shift && k < shift + n)
-            p[k] = narrow<O>(a.accumulate ? widen<O>(p[k]) + a.scale * sum[k] : a.scale * sum[k]);
+        if (k >= c.shift && k < c.shift + c.n)
+            row[c.from + k] = narrow<O>(x[k]);
 }
 
 __device__ __forceinline__ float *part_of(const EmbeddingGradArgs &a, int segment, int tail, int c)
@@ -256,88 +301,92 @@ __device__ __forceinline__ void unit_of(const EmbeddingGradArgs &a, int &segment
     segment = (int)(u / slabs), slab = (int)(u % slabs);
 }
 
-// Rows whose loads are on their way at once.
-constexpr int kBatch = 8;
+// Rows, and parts of a run, whose loads are on their way at once.
+constexpr int kBatch = 8, kJoinBatch = 16;
 
 // One wave per segment of the sorted list and 512 columns.  Lane e has the segment's
-// entry e.  A lane at the end of the columns takes the last eight, of which it stores
-// those that are its own (rows of fewer than eight: element by element).
-template <typename T, typename O>
+// entry e; what decides where sums end is in scalar registers.
+template <typename T, typename O, bool ACC>
 __global__ __launch_bounds__(kBlock) void segment_sum_kernel(EmbeddingGradArgs a)
 {
     const int lane = threadIdx.x % kWave;
     int s, slab;
     unit_of(a, s, slab);
-    const int c = (slab * kWave + lane) * kOct, n = min(a.hidden - c, kOct);
     if (s >= a.segments)
         return;
+    const Columns c(a.hidden, slab);
     const int lo = s * a.segment, entries = min(a.segment, a.rows - lo);
-    // the entries' tokens and rows, the tokens beside the segment (-1: none)
+    // the entries' tokens and rows, the tokens beside them (-1: none)
     const int e = lo + min(lane, entries - 1);
     const uint32_t key = a.key[e], row = a.row[e];
-    const uint32_t before = lo > 0 ? a.key[lo - 1] : ~0u, after = lo + entries < a.rows ? a.key[lo + entries] : ~0u;
-    const bool narrow_rows = a.hidden < kOct;
-    const int from = narrow_rows ? 0 : min(c, a.hidden - kOct), shift = c - from;
-    const T *d_out = static_cast<const T *>(a.d_out) + from;
+    const uint32_t before = lo > 0 ? a.key[lo - 1] : ~0u;
+    const uint32_t after = lo + min(lane, entries - 1) + 1 < a.rows ? a.key[lo + min(lane, entries - 1) + 1] : ~0u;
+    // entries that name a row, the last of each run among them, and whether the first
+    // run began and the last goes on in other segments
+    const uint64_t named = __ballot(lane < entries && key < (uint32_t)a.vocab);
+    const int m = __popcll(named);
+    if (m == 0)
+        return;
+    const uint64_t differ = __ballot(key != after);
+    const uint64_t last = 1ull << (m - 1);
+    const uint64_t ends = (differ & named) | last;
+    const bool begun = __builtin_amdgcn_readfirstlane(before == key), goes_on = !(differ & last);
+    bool first = true;
     float sum[kOct] = {};
-    uint32_t run = __builtin_amdgcn_readlane(key, 0);
-    bool cut = before == run;
-    for (int e0 = 0; e0 < entries; e0 += kBatch) {
+    for (int e0 = 0; e0 < m; e0 += kBatch) {
         RawOct<T> x[kBatch];
-        auto row_at = [&](int i) {
-            return d_out + (int64_t)(uint32_t)__builtin_amdgcn_readlane(row, min(e0 + i, entries - 1)) * a.stride;
+        RawOct<O> was[kBatch];
+        auto d_row = [&](int j) {
+            return static_cast<O *>(a.d_table) + (int64_t)(uint32_t)__builtin_amdgcn_readlane(key, j) * a.table_stride;
         };
-        if (narrow_rows) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                x[i].load(row_at(i), n);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                x[i].load(row_at(i));
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = min(e0 + i, m - 1);
+            c.load(static_cast<const T *>(a.d_out) + (int64_t)(uint32_t)__builtin_amdgcn_readlane(row, j) * a.stride, x[i]);
+            if (ACC && (ends >> j & 1))
+                c.load(d_row(j), was[i]);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int j = e0 + i;
-            if (j >= entries || run >= (uint32_t)a.vocab)
-                break;
+            if (j < m) {
 #pragma unroll
-            for (int k = 0; k < kOct; ++k)
-                sum[k] += x[i].at(k);
-            const uint32_t next = j + 1 < entries ? (uint32_t)__builtin_amdgcn_readlane(key, j + 1) : after;
-            if (next == run && j + 1 < entries)
-                continue;
-            // the run ends here, or in another segment
-            if (n > 0) {
-                if (cut || next == run)
-                    store8(part_of(a, s, !cut, from), sum);
-                else
-                    put<O>(a, run, from, shift, n, sum);
+                for (int k = 0; k < kOct; ++k)
+                    sum[k] += x[i].at(k);
+                if (ends >> j & 1) {
+                    const bool head = first && begun, tail = j == m - 1 && goes_on;
+                    if (head || tail)
+                        store8(part_of(a, s, !head, c.from), sum);
+                    else
+                        put<O, ACC>(a, d_row(j), c, sum, was[i]);
+                    first = false;
+#pragma unroll
+                    for (int k = 0; k < kOct; ++k)
+                        sum[k] = 0.0f;
+                }
             }
-            cut = false;
-            run = next;
-#pragma unroll
-            for (int k = 0; k < kOct; ++k)
-                sum[k] = 0.0f;
         }
     }
 }
 
 // The runs that begin in a segment and go on in the next: one wave per segment and
 // 512 columns.
-template <typename O>
+template <typename O, bool ACC>
 __global__ __launch_bounds__(kBlock) void join_runs_kernel(EmbeddingGradArgs a)
 {
-    const int lane = threadIdx.x % kWave;
     int s, slab;
     unit_of(a, s, slab);
-    const int c = (slab * kWave + lane) * kOct, n = min(a.hidden - c, kOct);
-    if (s >= a.segments - 1 || n <= 0)
+    if (s >= a.segments - 1)
         return;
+    const Columns c(a.hidden, slab);
     const int lo = s * a.segment, next = lo + a.segment;
     const uint32_t run = a.key[next - 1], begins = a.key[next], before = lo > 0 ? a.key[lo - 1] : ~0u;
     if (run >= (uint32_t)a.vocab || begins != run || before == run)
         return;
+    O *row = static_cast<O *>(a.d_table) + (int64_t)run * a.table_stride;
+    RawOct<O> was;
+    if (ACC)
+        c.load(row, was);
     // the last segment that begins with the run: in steps that double, then halve
     int last = s + 1, step = 1;
     auto has = [&](int q) { return q < a.segments && a.key[q * a.segment] == run; };
@@ -346,26 +395,21 @@ __global__ __launch_bounds__(kBlock) void join_runs_kernel(EmbeddingGradArgs a)
     for (step /= 2; step > 0; step /= 2)
         if (has(last + step))
             last += step;
-    float sum[kOct], x[kBatch][kOct];
-    load8(part_of(a, s, 1, c), sum);
-    int q = s + 1;
-    for (; q + kBatch <= last + 1; q += kBatch) {
+    float sum[kOct];
+    load8(part_of(a, s, 1, c.from), sum);
+    for (int q = s + 1; q <= last; q += kJoinBatch) {
+        float x[kJoinBatch][kOct];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            load8(part_of(a, q + i, 0, c), x[i]);
+        for (int i = 0; i < kJoinBatch; ++i)
+            load8(part_of(a, min(q + i, last), 0, c.from), x[i]);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (q + i <= last)
 #pragma unroll
-            for (int k = 0; k < kOct; ++k)
-                sum[k] += x[i][k];
+                for (int k = 0; k < kOct; ++k)
+                    sum[k] += x[i][k];
     }
-    for (; q <= last; ++q) {
-        load8(part_of(a, q, 0, c), x[0]);
-#pragma unroll
-        for (int k = 0; k < kOct; ++k)
-            sum[k] += x[0][k];
-    }
-    put<O>(a, run, c, 0, n, sum);
+    put<O, ACC>(a, row, c, sum, was);
 }
 
 template <typename T, typename O>
@@ -383,7 +427,7 @@ void embedding_rows(const EmbeddingArgs &a, hipStream_t st)
 template <typename T, typename O>
 void embedding_grad_of(const EmbeddingGradArgs &a, hipStream_t st)
 {
-    const int chunks = (a.rows + kSortChunk - 1) / kSortChunk;
+    const int chunks = (a.rows + a.chunk - 1) / a.chunk;
     // octs of all rows, as the rows lie one after another or apart
     const int64_t octs = (int64_t)a.vocab * ((a.hidden + kOct - 1) / kOct);
     const int clear = a.accumulate ? 0 : (int)((octs + kClearOcts - 1) / kClearOcts);
@@ -392,21 +436,40 @@ void embedding_grad_of(const EmbeddingGradArgs &a, hipStream_t st)
     if (a.rows == 0)
         return;
     if (chunks > 1)
-        hipLaunchKernelGGL(merge_chunks_kernel, dim3((a.rows + kBlock - 1) / kBlock), dim3(kBlock), 0, st, a,
-                           chunks);
+        hipLaunchKernelGGL(merge_chunks_kernel, dim3((a.rows + kBlock - 1) / kBlock), dim3(kBlock),
+                           chunks * kSamples * sizeof(uint32_t), st, a, chunks);
     const int64_t units = (int64_t)a.segments * ((a.hidden + kOct * kWave - 1) / (kOct * kWave));
     const dim3 grid((unsigned)((units + kBlock / kWave - 1) / (kBlock / kWave)));
-    hipLaunchKernelGGL((segment_sum_kernel<T, O>), grid, dim3(kBlock), 0, st, a);
-    if (a.segments > 1)
-        hipLaunchKernelGGL((join_runs_kernel<O>), grid, dim3(kBlock), 0, st, a);
+    auto sums = [&](auto acc) {
+        constexpr bool ACC = decltype(acc)::value;
+        hipLaunchKernelGGL((segment_sum_kernel<T, O, ACC>), grid, dim3(kBlock), 0, st, a);
+        if (a.segments > 1)
+            hipLaunchKernelGGL((join_runs_kernel<O, ACC>), grid, dim3(kBlock), 0, st, a);
+    };
+    if (a.accumulate)
+        sums(std::true_type());
+    else
+        sums(std::false_type());
 }
 
 }  // namespace
 
+// Eight rows wait for memory together, so a short segment is summed sooner, but a
+// token of many rows leaves more parts to join.  Added to what is there, us, with
+// segments of
+//      rows x hidden, slabs    8    16    32    64
+//     1024 x 1280     3072    19    23    31    48
+//     1000 x 5000    10000    19    22    31    46
+//    20000 x   64    20000    45    43    48    64
+//     8192 x 1280    24576    38    39    45    64
+//     4096 x 4096    32768    38    38    42    55
+//   100000 x   64   100000   115    91    83    92
+//    16384 x 4096   131072    80    71    67    70
+// Up to 32 rows are one segment, without a join.
 int32_t embedding_segment(int64_t rows, int64_t hidden)
 {
-    const int64_t slabs = (hidden + kOct * kWave - 1) / (kOct * kWave);
-    return rows > 32 && rows * slabs <= 32768 ? 8 : 32;
+    const int64_t work = rows * ((hidden + kOct * kWave - 1) / (kOct * kWave));
+    return rows <= 32 || work > 65536 ? 32 : work > 16384 ? 16 : 8;
 }
 
 int launch_embedding(const EmbeddingArgs &a, void *stream)

@@ -55,6 +55,10 @@ template <>
 struct RawOct<uint16_t> {
     u32x4 a;
     __device__ __forceinline__ void load(const uint16_t *p) { a = *reinterpret_cast<const u32x4_at2 *>(p); }
+    __device__ __forceinline__ void stream(const uint16_t *p)   // not read again soon
+    {
+        a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_at2 *>(p));
+    }
     __device__ __forceinline__ void load(const uint16_t *p, int n)   // the first n
     {
 #pragma unroll
@@ -69,6 +73,11 @@ struct RawOct<float> {
     __device__ __forceinline__ void load(const float *p)
     {
         a = *reinterpret_cast<const f32x4_at4 *>(p), b = *reinterpret_cast<const f32x4_at4 *>(p + 4);
+    }
+    __device__ __forceinline__ void stream(const float *p)
+    {
+        a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_at4 *>(p));
+        b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_at4 *>(p + 4));
     }
     __device__ __forceinline__ void load(const float *p, int n)
     {
