@@ -34,13 +34,13 @@ bool within(double x, double lo, double hi) { return x >= lo && x <= hi; }
 SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs)
 {
     if (n_tokens <= kSequenceShort || n_seqs == 0)
-        return {1, 0};
+        return {kRoundShift, 0};
     // every wave of a sequence adds up all its parts: tiles grow before an even share of
-    // the positions has more than 512 of them
-    int32_t rounds = 1;
-    while (rounds < 64 && n_tokens / n_seqs > (int64_t)rounds * 4 * kWave * 512)
-        rounds *= 4;
-    return {rounds, n_tokens / (rounds * 4 * kWave) + n_seqs};
+    // the positions has more than 1024 of them
+    int32_t shift = kRoundShift;
+    while (n_tokens / n_seqs > (int64_t)1024 << shift)
+        shift += 2;
+    return {shift, (n_tokens >> shift) + n_seqs};
 }
 
 }  // namespace zero

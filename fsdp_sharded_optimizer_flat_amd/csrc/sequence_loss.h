@@ -9,10 +9,11 @@ namespace zero {
 // Up to this many positions a call is one launch, a workgroup to a sequence or pair.
 constexpr int64_t kSequenceShort = 16384;
 
-// Longer ones are cut into tiles of the positions (64 lanes, four positions a lane
-// and round); a wave takes a sequence's share of a tile.
+// Longer ones are cut into tiles of 2^shift positions, whole rounds of a wave (four
+// positions to a lane); a wave takes a sequence's share of a tile.
+constexpr int kRoundShift = 8;
 struct SequenceCut {
-    int32_t rounds;
+    int32_t shift;
     int64_t slots;   // shares at most; 0: not cut
 };
 SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs);

@@ -25,6 +25,7 @@ namespace {
 using namespace dev;
 
 constexpr int kQuadTokens = 4;   // positions of a lane
+static_assert(1 << kRoundShift == kQuadTokens * kWave, "a round of a wave");
 
 struct Range {
     int64_t lo, hi;
@@ -40,22 +41,65 @@ __device__ __forceinline__ double weight_of(const Sequences &s, int64_t targets)
     return s.mode == ZERO_SEQUENCE_SUM || targets == 0 ? 1.0 : 1.0 / (double)targets;
 }
 
-// Four neighbouring values from position t on, of which those in the range are read.
-__device__ __forceinline__ void load_quad(const float *p, int64_t t, const Range &r, float (&x)[kQuadTokens])
-{
-    typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
-    if (t >= r.lo && t + kQuadTokens <= r.hi) {
-        const f32x4 v = *reinterpret_cast<const f32x4_at4 *>(p + t);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        return;
-    }
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+typedef long i64x2 __attribute__((ext_vector_type(2)));
+typedef i64x2 i64x2_at8 __attribute__((aligned(8)));
+
+// N arrays' values at four neighbouring positions, and their tokens.  All loads are
+// issued before any value is used: whole quads where the array has them (neighbours'
+// positions too; what is outside the range is not used).
+template <int N>
+struct Quad {
+    f32x4 x[N];
+    i64x2 token[2];
+    __device__ __forceinline__ Quad(const Sequences &s, const float *const (&p)[N], int64_t t, const Range &r)
+    {
 #pragma unroll
-    for (int k = 0; k < kQuadTokens; ++k)
-        x[k] = t + k >= r.lo && t + k < r.hi ? p[t + k] : 0.0f;
+        for (int i = 0; i < N; ++i)
+            x[i] = f32x4{0, 0, 0, 0};
+        token[0] = token[1] = i64x2{0, 0};
+        if (t >= r.hi || t + kQuadTokens <= r.lo)
+            return;
+        if (t + kQuadTokens <= s.n_tokens) {
+            if (s.tokens) {
+                token[0] = *reinterpret_cast<const i64x2_at8 *>(s.tokens + t);
+                token[1] = *reinterpret_cast<const i64x2_at8 *>(s.tokens + t + 2);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (p[i])
+                    x[i] = *reinterpret_cast<const f32x4_at4 *>(p[i] + t);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kQuadTokens; ++k)
+                if (t + k < s.n_tokens) {
+                    if (s.tokens)
+                        token[k / 2][k % 2] = s.tokens[t + k];
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (p[i])
+                            x[i][k] = p[i][t + k];
+                }
+        }
+    }
+    // Which of the positions are targets of the range, as bits.
+    __device__ __forceinline__ unsigned targets(int64_t t, const Range &r) const
+    {
+        unsigned on = 0;
+#pragma unroll
+        for (int k = 0; k < kQuadTokens; ++k)
+            on |= (unsigned)(t + k >= r.lo && t + k < r.hi && token[k / 2][k % 2] >= 0) << k;
+        return on;
+    }
+};
+__device__ __forceinline__ unsigned targets_of(const Sequences &s, int64_t t, const Range &r)
+{
+    const float *const none[1] = {nullptr};
+    return Quad<1>(s, none, t, r).targets(t, r);
 }
+
 __device__ __forceinline__ void store_quad(float *p, int64_t t, const Range &r, const float (&x)[kQuadTokens])
 {
-    typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
     if (t >= r.lo && t + kQuadTokens <= r.hi) {
         *reinterpret_cast<f32x4_at4 *>(p + t) = f32x4{x[0], x[1], x[2], x[3]};
         return;
@@ -65,22 +109,17 @@ __device__ __forceinline__ void store_quad(float *p, int64_t t, const Range &r, 
         if (t + k >= r.lo && t + k < r.hi)
             p[t + k] = x[k];
 }
-// Which of four positions are targets of the range, as bits.
-__device__ __forceinline__ unsigned targets_of(const Sequences &s, int64_t t, const Range &r)
+// What a quad of the gradient holds, zeros outside the range.
+__device__ __forceinline__ void load_quad(const float *p, int64_t t, const Range &r, float (&x)[kQuadTokens])
 {
-    typedef long i64x2 __attribute__((ext_vector_type(2)));
-    typedef i64x2 i64x2_at8 __attribute__((aligned(8)));
-    if (s.tokens && t >= r.lo && t + kQuadTokens <= r.hi) {
-        const i64x2 a = *reinterpret_cast<const i64x2_at8 *>(s.tokens + t);
-        const i64x2 b = *reinterpret_cast<const i64x2_at8 *>(s.tokens + t + 2);
-        return (a.x >= 0) | (a.y >= 0) << 1 | (b.x >= 0) << 2 | (b.y >= 0) << 3;
+    if (t >= r.lo && t + kQuadTokens <= r.hi) {
+        const f32x4 v = *reinterpret_cast<const f32x4_at4 *>(p + t);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        return;
     }
-    unsigned on = 0;
 #pragma unroll
     for (int k = 0; k < kQuadTokens; ++k)
-        if (t + k >= r.lo && t + k < r.hi && (!s.tokens || s.tokens[t + k] >= 0))
-            on |= 1u << k;
-    return on;
+        x[k] = t + k >= r.lo && t + k < r.hi ? p[t + k] : 0.0f;
 }
 
 // -- sums -----------------------------------------------------------------------------
@@ -122,42 +161,41 @@ struct Share {
     bool first;   // of its sequence (of an empty sequence: the only one, empty)
     bool none;
 };
-// The slot that sequence b's first share has.
-__device__ __forceinline__ int64_t first_slot(const Sequences &s, int64_t b, int64_t span)
-{
-    return min(max(s.offsets[b], int64_t(0)), s.n_tokens) / span + b;
-}
 __device__ __forceinline__ Share share_of(const Sequences &s, int64_t slot)
 {
-    const int64_t span = (int64_t)s.cut.rounds * kQuadTokens * kWave;
-    const int lane = threadIdx.x % kWave;
-    // the last sequence whose first slot is not behind this one: 64 candidates at a time
+    const int shift = s.cut.shift, lane = threadIdx.x % kWave;
+    auto start = [&](int64_t b) { return min(max(s.offsets[b], int64_t(0)), s.n_tokens); };
+    // the last sequence whose first slot is not behind this one: 64 candidates at a
+    // time, at the end neighbours (one less, with the start of the one behind them)
     int64_t lo = 0, n = s.n;
-    while (n > 1) {
+    while (n > kWave - 1) {
         const int64_t step = (n + kWave - 1) / kWave, c = lo + lane * step;
-        const uint64_t not_behind = __ballot(c < lo + n && first_slot(s, c, span) <= slot);
+        const uint64_t not_behind = __ballot(c < lo + n && (start(c) >> shift) + c <= slot);
         const int k = 63 - __builtin_clzll(not_behind | 1);
         n = min(step, n - k * step);
         lo += k * step;
     }
+    const int64_t own = start(min(lo + lane, s.n)), c = lo + lane;
+    const uint64_t not_behind = __ballot(lane < n && (own >> shift) + c <= slot);
+    const int k = 63 - __builtin_clzll(not_behind | 1);
     Share h;
-    h.b = lo;
-    h.tile = slot - lo;
-    h.seq = range_of(s, lo);
-    const int64_t begin = h.seq.lo / span;
+    h.b = lo + k;
+    h.tile = slot - h.b;
+    h.seq.lo = __shfl(own, k, kWave);
+    h.seq.hi = max(h.seq.lo, (int64_t)__shfl(own, k + 1, kWave));
+    const int64_t begin = h.seq.lo >> shift;
     h.first = h.tile == begin;
-    h.part.lo = max(h.seq.lo, h.tile * span);
-    h.part.hi = min(h.seq.hi, (h.tile + 1) * span);
+    h.part.lo = max(h.seq.lo, h.tile << shift);
+    h.part.hi = min(h.seq.hi, (h.tile + 1) << shift);
     h.none = !h.first && (h.tile < begin || h.part.lo >= h.part.hi);
     return h;
 }
 // The sums of a sequence's shares, in every lane.
 __device__ __forceinline__ SequencePart total_of(const Sequences &s, int64_t b, const Range &r)
 {
-    const int64_t span = (int64_t)s.cut.rounds * kQuadTokens * kWave;
     SequencePart p{};
     if (r.hi > r.lo) {
-        const int64_t first = r.lo / span + b, last = (r.hi - 1) / span + b;
+        const int64_t first = (r.lo >> s.cut.shift) + b, last = ((r.hi - 1) >> s.cut.shift) + b;
         for (int64_t i = first + threadIdx.x % kWave; i <= last; i += kWave)
             add(p, s.parts[i]);
     }
@@ -229,21 +267,15 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs &a, float lp, float
 __device__ __forceinline__ void policy_quad(const PolicyArgs &a, int64_t b, int64_t t, const Range &r, SequencePart &sum,
                                             double (&slope)[kQuadTokens])
 {
-    float lp[kQuadTokens], old[kQuadTokens], ref[kQuadTokens] = {}, adv[kQuadTokens];
-    const unsigned on = targets_of(a.seq, t, r);
-    load_quad(a.logprob, t, r, lp);
-    load_quad(a.old_logprob, t, r, old);
-    if (a.ref_logprob)
-        load_quad(a.ref_logprob, t, r, ref);
-    if (a.per_token)
-        load_quad(a.advantage, t, r, adv);
-    else
-        adv[0] = adv[1] = adv[2] = adv[3] = a.advantage[b];
+    const float *const arrays[4] = {a.logprob, a.old_logprob, a.ref_logprob, a.per_token ? a.advantage : nullptr};
+    const Quad<4> q(a.seq, arrays, t, r);
+    const float adv = a.per_token ? 0.0f : a.advantage[b];
+    const unsigned on = q.targets(t, r);
 #pragma unroll
     for (int k = 0; k < kQuadTokens; ++k) {
         slope[k] = 0.0;
         if (on >> k & 1) {
-            const Term m = policy_term(a, lp[k], old[k], ref[k], adv[k]);
+            const Term m = policy_term(a, q.x[0][k], q.x[1][k], q.x[2][k], a.per_token ? q.x[3][k] : adv);
             add(sum, SequencePart{m.loss, m.kl, m.cut, 1});
             slope[k] = m.slope;
         }
@@ -280,21 +312,29 @@ __global__ __launch_bounds__(NT) void policy_kernel(PolicyArgs a)
     const int64_t b = blockIdx.x;
     const Range r = range_of(a.seq, b);
     const int64_t t0 = r.lo / kQuadTokens * kQuadTokens + threadIdx.x * kQuadTokens;
+    const bool mean = a.seq.mode == ZERO_SEQUENCE_MEAN;
+    const double d_loss = a.d_logprob ? a.d_loss[b] : 0.0;
     SequencePart sum{};
     double held[kQuadTokens], slope[kQuadTokens];
     policy_quad(a, b, t0, r, sum, held);
-    for (int64_t t = t0 + NT * kQuadTokens; t < r.hi; t += NT * kQuadTokens)
+    for (int64_t t = t0 + NT * kQuadTokens; t < r.hi; t += NT * kQuadTokens) {
         policy_quad(a, b, t, r, sum, slope);
+        if (a.d_logprob)   // a mean's are scaled below, by the same thread
+            put_slopes(a, t, r, mean ? 1.0 : d_loss, slope);
+    }
     sum = waves_total(sum, sh, 0, NT / kWave);
     if (threadIdx.x == 0)
         put_policy(a, b, sum);
     if (!a.d_logprob)
         return;
-    const double up = weight_of(a.seq, sum.targets) * (double)a.d_loss[b];
+    const double up = weight_of(a.seq, sum.targets) * d_loss;
     put_slopes(a, t0, r, up, held);
-    for (int64_t t = t0 + NT * kQuadTokens; t < r.hi; t += NT * kQuadTokens) {
-        SequencePart again{};
-        policy_quad(a, b, t, r, again, slope);
+    for (int64_t t = t0 + NT * kQuadTokens; mean && t < r.hi; t += NT * kQuadTokens) {
+        float g[kQuadTokens];
+        load_quad(a.d_logprob, t, r, g);
+#pragma unroll
+        for (int k = 0; k < kQuadTokens; ++k)
+            slope[k] = g[k];
         put_slopes(a, t, r, up, slope);
     }
 }
@@ -310,9 +350,10 @@ __global__ __launch_bounds__(kBlock) void policy_share_kernel(PolicyArgs a)
     if (h.none || h.part.lo >= h.part.hi)
         return;
     const double up = a.d_logprob && a.seq.mode == ZERO_SEQUENCE_SUM ? (double)a.d_loss[h.b] : 1.0;
-    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
+    const int64_t begin = h.tile << a.seq.cut.shift;
+    const int rounds = 1 << (a.seq.cut.shift - kRoundShift);
     SequencePart sum{};
-    for (int i = 0; i < a.seq.cut.rounds; ++i) {
+    for (int i = 0; i < rounds; ++i) {
         const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
         double slope[kQuadTokens];
         policy_quad(a, h.b, t, h.part, sum, slope);
@@ -332,17 +373,24 @@ __global__ __launch_bounds__(kBlock) void policy_join_kernel(PolicyArgs a)
     const bool scale = a.d_logprob && a.seq.mode == ZERO_SEQUENCE_MEAN && h.part.lo < h.part.hi;
     if (h.none || !(h.first || scale))
         return;
+    // the first round's slopes are on their way while the parts are added up
+    const int64_t t0 = (h.tile << a.seq.cut.shift) + threadIdx.x % kWave * kQuadTokens;
+    float g[kQuadTokens];
+    if (scale)
+        load_quad(a.d_logprob, t0, h.part, g);
+    const double d_loss = scale ? a.d_loss[h.b] : 0.0;
     const SequencePart sum = total_of(a.seq, h.b, h.seq);
     if (h.first && threadIdx.x % kWave == 0)
         put_policy(a, h.b, sum);
     if (!scale)
         return;
-    const double up = weight_of(a.seq, sum.targets) * (double)a.d_loss[h.b];
-    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
-    for (int i = 0; i < a.seq.cut.rounds; ++i) {
-        const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
-        float g[kQuadTokens];
-        load_quad(a.d_logprob, t, h.part, g);
+    const double up = weight_of(a.seq, sum.targets) * d_loss;
+    const int64_t begin = h.tile << a.seq.cut.shift;
+    const int rounds = 1 << (a.seq.cut.shift - kRoundShift);
+    for (int i = 0; i < rounds; ++i) {
+        const int64_t t = t0 + (int64_t)i * kWave * kQuadTokens;
+        if (i > 0)
+            load_quad(a.d_logprob, t, h.part, g);
         const double slope[kQuadTokens] = {g[0], g[1], g[2], g[3]};
         put_slopes(a, t, h.part, up, slope);
     }
@@ -373,15 +421,13 @@ __device__ __forceinline__ void preference(const PreferenceArgs &a, double h, do
 
 __device__ __forceinline__ unsigned ratio_quad(const PreferenceArgs &a, int64_t t, const Range &r, SequencePart &sum)
 {
-    float lp[kQuadTokens], ref[kQuadTokens] = {};
-    const unsigned on = targets_of(a.seq, t, r);
-    load_quad(a.logprob, t, r, lp);
-    if (a.ref_logprob)
-        load_quad(a.ref_logprob, t, r, ref);
+    const float *const arrays[2] = {a.logprob, a.ref_logprob};
+    const Quad<2> q(a.seq, arrays, t, r);
+    const unsigned on = q.targets(t, r);
 #pragma unroll
     for (int k = 0; k < kQuadTokens; ++k)
         if (on >> k & 1)
-            add(sum, SequencePart{(double)lp[k] - (double)ref[k], 0.0, 0, 1});
+            add(sum, SequencePart{(double)q.x[0][k] - (double)q.x[1][k], 0.0, 0, 1});
     return on;
 }
 __device__ __forceinline__ void put_constant(const PreferenceArgs &a, int64_t t, const Range &r, unsigned on, float g)
@@ -448,9 +494,10 @@ __global__ __launch_bounds__(kBlock) void preference_share_kernel(PreferenceArgs
     const Share h = share_of(a.seq, slot);
     if (h.none || h.part.lo >= h.part.hi)
         return;
-    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
+    const int64_t begin = h.tile << a.seq.cut.shift;
+    const int rounds = 1 << (a.seq.cut.shift - kRoundShift);
     SequencePart sum{};
-    for (int i = 0; i < a.seq.cut.rounds; ++i)
+    for (int i = 0; i < rounds; ++i)
         ratio_quad(a, begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens, h.part, sum);
     sum = wave_total(sum);
     if (threadIdx.x % kWave == 0)
@@ -472,8 +519,9 @@ __global__ __launch_bounds__(kBlock) void preference_join_kernel(PreferenceArgs 
                                   put && threadIdx.x % kWave == 0, rejected);
     if (!write)
         return;
-    const int64_t begin = h.tile * a.seq.cut.rounds * kQuadTokens * kWave;
-    for (int i = 0; i < a.seq.cut.rounds; ++i) {
+    const int64_t begin = h.tile << a.seq.cut.shift;
+    const int rounds = 1 << (a.seq.cut.shift - kRoundShift);
+    for (int i = 0; i < rounds; ++i) {
         const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
         put_constant(a, t, h.part, targets_of(a.seq, t, h.part), g);
     }
