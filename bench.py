@@ -124,17 +124,24 @@ def parse():
                     help="time the per-unit step streamed beside a backward stand-in: each unit's "
                          "gradient buckets written in backward order, the unit stepped serially "
                          "after it or overlapped on a side stream (two recycled bucket slots)")
-    ap.add_argument("--producer", default="gemm", choices=["gemm", "copy"],
+    ap.add_argument("--producer", default="gemm", choices=["gemm", "act8", "copy"],
                     help="backward stand-in for --streamed: the weight-gradient GEMMs "
-                         "dW = dY^T X (MFMA) or a copy of resident gradients (HBM)")
+                         "dW = dY^T X (MFMA), the same from 8-bit checkpoints of X "
+                         "(zero_act8_weight_grad), or a copy of resident gradients (HBM)")
     ap.add_argument("--tokens", type=int, default=1024,
                     help="tokens per simulated rank of the --streamed GEMM producer")
-    ap.add_argument("--loss", default="none", choices=["none", "lm", "distill"],
+    ap.add_argument("--loss", default="none", choices=["none", "lm", "distill", "policy", "preference"],
                     help="with --streamed --workload gpt2l: start each pass with every simulated "
                          "rank's loss over its tokens' logits and take the head's weight gradient "
-                         "from it: the language-model loss (zero_logprob_fused), or the record of "
+                         "from it: the language-model loss (zero_logprob_fused), the record of "
                          "a teacher's top logits and the distillation loss against it "
-                         "(zero_logprob, zero_distill_fused)")
+                         "(zero_logprob, zero_distill_fused), or the clipped policy loss or the "
+                         "preference loss of packed sequences (zero_logprob, zero_policy_loss or "
+                         "zero_preference_loss, zero_logprob_grad)")
+    ap.add_argument("--embedding", action="store_true",
+                    help="with --streamed --workload gpt2l: end each pass with every simulated rank's "
+                         "embedding gradient (zero_embedding_grad), added onto the tied head's in its "
+                         "bucket")
     ap.add_argument("--top-k", type=int, default=64, help="logits of a teacher's record (--loss distill)")
     ap.add_argument("--reshard", default=None, metavar="NAME",
                     help="time a checkpoint reshard (gpt2l_reshard, llama8b_reshard) instead of "
@@ -729,6 +736,9 @@ def setup_step(wl, fused=False, stage_chunk=None, stagger_kib=None, norm_only=No
     return ns
 
 
+SEQUENCE = 128   # tokens of a packed sequence in --loss policy and preference
+
+
 def random_logits(n, tokens, vocab, dev):
     """Normal bf16 logits of deviation 2 for n ranks' tokens."""
     import torch
@@ -754,6 +764,8 @@ def streamed_bench(args):
               gradient work (the vector parameters, 0.05 % of a GPT-2 block,
               keep their values: thousands of tiny launches per pass would
               make the stand-in launch-bound);
+      act8 -- the same from 8-bit checkpoints of X (zero_act8_weight_grad), packed
+              once, as the forward pass leaves them;
       copy -- the unit's buckets copied from resident gradients (HBM-bound).
 
     With --loss the pass starts as backward does, at the loss: each rank's
@@ -762,7 +774,13 @@ def streamed_bench(args):
     d(logits)^T X; `loss_only` times that part.  lm: zero_logprob_fused, the
     mean negative log probability; distill: the teacher's top-k logits
     (zero_logprob) and the renormalised divergence from them
-    (zero_distill_fused), the mean over the rank's tokens.
+    (zero_distill_fused), the mean over the rank's tokens; policy, preference:
+    the tokens' log probabilities (zero_logprob), the loss of packed sequences of
+    SEQUENCE tokens and its gradient (zero_policy_loss with a KL term,
+    zero_preference_loss over neighbouring halves), the backward pass from the
+    forward's statistics (zero_logprob_grad).  With --embedding the pass ends at
+    the embedding: unit 0's bucket gets the gradient of each rank's looked-up
+    rows, added onto what the producer left there (zero_embedding_grad).
 
     Three passes over the whole model, each timed between synchronizations
     (median of `steps` repetitions after `warmup`): the producer alone;
@@ -782,8 +800,12 @@ def streamed_bench(args):
     wl = workload_from_args(args)
     if wl.rank >= 0 or wl.grad_index != "global":
         raise SystemExit("--streamed runs the all-ranks workloads (gpt2l, gpt2l_block)")
-    if args.loss != "none" and (args.workload != "gpt2l" or args.producer != "gemm"):
-        raise SystemExit("--loss needs --workload gpt2l (a head) and --producer gemm")
+    if args.loss != "none" and (args.workload != "gpt2l" or args.producer == "copy"):
+        raise SystemExit("--loss needs --workload gpt2l (a head) and --producer gemm or act8")
+    if args.embedding and (args.workload != "gpt2l" or args.producer == "copy"):
+        raise SystemExit("--embedding needs --workload gpt2l (an embedding) and --producer gemm or act8")
+    if args.loss == "preference" and args.tokens < 2:
+        raise SystemExit("--loss preference needs --tokens 2 or more (a pair)")
     if args.loss == "distill" and not 1 <= args.top_k <= z.ZERO_MAX_TOP:
         raise SystemExit(f"--top-k must be between 1 and {z.ZERO_MAX_TOP}")
     n, h = wl.n_ranks, wl.hyper
@@ -803,7 +825,7 @@ def streamed_bench(args):
     slots = torch.empty(2, n, cap, dtype=torch.bfloat16, device=dev)
     main, side = torch.cuda.current_stream(), torch.cuda.Stream()
     tok = args.tokens
-    if args.producer == "gemm":
+    if args.producer != "copy":
         # one contiguous activation matrix per input width, one dY^T per
         # output height (row slices of the tallest are contiguous)
         X = {k: (torch.randn(tok, k, device=dev) * 0.5).to(torch.bfloat16)
@@ -811,6 +833,17 @@ def streamed_bench(args):
         max_out = max(s[0] for u in shapes for s in u if len(s) == 2)
         dYT = (torch.randn(max_out, tok, device=dev) * 1e-3).to(torch.bfloat16)
         flops = 2.0 * tok * n * sum(s[0] * s[1] for u in shapes for s in u if len(s) == 2)
+        if args.producer == "act8":
+            dY = dYT.t().contiguous()
+            kept = {}
+            for k, x in X.items():
+                codes = torch.empty(tok, k, dtype=torch.uint8, device=dev)
+                scales = torch.empty(tok, -(-k // z.ZERO_ACT8_BLOCK), dtype=torch.uint8, device=dev)
+                z.zero_act8_pack(x, codes, scales)
+                kept[k] = (codes, scales)
+            wg_ws = torch.empty(max([1] + [z.zero_act8_weight_grad_workspace_bytes(tok, *s)
+                                           for u in shapes for s in u if len(s) == 2]),
+                                dtype=torch.uint8, device=dev)
     else:
         src = torch.empty(n, P, dtype=torch.bfloat16, device=dev)
         for r in range(n):
@@ -833,6 +866,42 @@ def streamed_bench(args):
             top_i = torch.empty(tok, args.top_k, dtype=torch.int32, device=dev)
             top_v = torch.empty(tok, args.top_k, device=dev)
             loss_bytes += teacher.nbytes
+        elif args.loss in ("policy", "preference"):
+            loss_bytes += logits.nbytes   # the backward pass reads them again
+            n_seqs = -(-tok // SEQUENCE)
+            if args.loss == "preference":
+                n_seqs = max(2, n_seqs // 2 * 2)
+            offsets = torch.linspace(0, tok, n_seqs + 1, device=dev).long()
+            logprob, row_stats = torch.empty(n, tok, device=dev), torch.empty(n, tok, 2, device=dev)
+            d_logprob = torch.empty(n, tok, device=dev)
+            for r in range(n):   # the sampler's and the reference's, a little away
+                z.zero_logprob(logits[r], targets[r], logprob=logprob[r], workspace=loss_ws)
+            older = logprob + 0.1 * torch.randn_like(logprob)
+            reference = logprob + 0.1 * torch.randn_like(logprob)
+            advantage = torch.randn(n, n_seqs, device=dev)
+            n_losses = n_seqs if args.loss == "policy" else n_seqs // 2
+            seq_loss = torch.empty(n, n_losses, device=dev)
+            seq_weight = torch.full((n_losses,), 1.0 / n_losses, device=dev)
+            seq_ws = torch.empty(max(z.zero_sequence_loss_workspace_bytes(tok, n_seqs), 1),
+                                 dtype=torch.uint8, device=dev)
+    if args.embedding:
+        ids = torch.randint(0, workloads.VOCAB_GPT2L, (n, tok), device=dev)
+        d_rows = (torch.randn(n, tok, workloads.HIDDEN_GPT2L, device=dev) * 1e-3).to(torch.bfloat16)
+        emb_ws = torch.empty(z.zero_embedding_grad_workspace_bytes(tok, workloads.VOCAB_GPT2L,
+                                                                   workloads.HIDDEN_GPT2L),
+                             dtype=torch.uint8, device=dev)
+
+    def sequence_loss(r):
+        z.zero_logprob(logits[r], targets[r], logprob=logprob[r], stats=row_stats[r], workspace=loss_ws)
+        if args.loss == "policy":
+            z.zero_policy_loss(logprob[r], older[r], advantage[r], offsets, tokens=targets[r],
+                               ref_logprob=reference[r], kl_coef=0.05, d_loss=seq_weight, loss=seq_loss[r],
+                               d_logprob=d_logprob[r], workspace=seq_ws)
+        else:
+            z.zero_preference_loss(logprob[r], offsets, tokens=targets[r], ref_logprob=reference[r],
+                                   d_loss=seq_weight, loss=seq_loss[r], d_logprob=d_logprob[r],
+                                   workspace=seq_ws)
+        z.zero_logprob_grad(logits[r], targets[r], row_stats[r], d_logits[r], d_logprob=d_logprob[r])
 
     def loss():
         for r in range(n):
@@ -843,6 +912,14 @@ def streamed_bench(args):
                 z.zero_logprob(teacher[r], top_index=top_i, top_logprob=top_v, workspace=loss_ws)
                 z.zero_distill_fused(logits[r], top_i, top_v, z.ZERO_DISTILL_RENORM, weight, d_logits[r],
                                      loss=row_loss[r], workspace=loss_ws)
+            elif args.loss != "none":
+                sequence_loss(r)
+
+    def weight_gradient(d_y_t, shape, d_w):
+        if args.producer == "act8":
+            z.zero_act8_weight_grad(d_y_t.t(), *kept[shape[1]], d_w, workspace=wg_ws)
+        else:
+            torch.matmul(d_y_t, X[shape[1]], out=d_w)
 
     def produce(u, slot):
         pad = int(T[u, 1])
@@ -854,10 +931,15 @@ def streamed_bench(args):
             at = 0
             for s in shapes[u]:
                 k = workloads.numel_of(s)
-                if args.loss != "none" and u == 0 and at == 0:   # the token embedding, the tied head
-                    torch.matmul(d_logits[r].t(), X[s[1]], out=slots[slot, r, :k].view(s[0], s[1]))
-                elif len(s) == 2:   # dW [out, in] = dY^T [out, T] @ X [T, in]
-                    torch.matmul(dYT[:s[0]], X[s[1]], out=slots[slot, r, at:at + k].view(s[0], s[1]))
+                if len(s) == 2:   # dW [out, in] = dY^T [out, T] @ X [T, in]
+                    d_w = slots[slot, r, at:at + k].view(s[0], s[1])
+                    head = u == 0 and at == 0   # the token embedding, the tied head
+                    if head and args.loss != "none":
+                        weight_gradient(d_logits[r].t(), s, d_w)
+                    else:
+                        weight_gradient(dY[:, :s[0]].t() if args.producer == "act8" else dYT[:s[0]], s, d_w)
+                    if head and args.embedding:
+                        z.zero_embedding_grad(d_rows[r], ids[r], d_w, accumulate=True, workspace=emb_ws)
                 at += k
 
     sc_t = [0]
@@ -963,7 +1045,7 @@ def streamed_bench(args):
         "dtype": "f32",
         "data": "synthetic",
         "config": {"workload": wl.name, "simulated_ranks": n, "units": U, "elements": int(elements),
-                   "producer": args.producer, "tokens_per_rank": tok if args.producer == "gemm" else None,
+                   "producer": args.producer, "tokens_per_rank": tok if args.producer != "copy" else None,
                    "producer_tflop_per_pass": flops / 1e12 if flops else None,
                    "bucket_slots_bytes": 2 * n * cap * 2,
                    "full_gradients_bytes": n * P * 2},
@@ -981,7 +1063,10 @@ def streamed_bench(args):
         # a rate of HBM where the ranks' logits together exceed the memory-side cache (256 MB)
         result["loss_bytes"] = loss_bytes
         result["loss_hbm_GBps"] = loss_bytes / (res["loss_only"][0] / 1e3) / 1e9
-        result["mean_loss"] = float(row_loss.mean()) * (-1.0 if args.loss == "lm" else 1.0)
+        result["mean_loss"] = (float(row_loss.mean()) * (-1.0 if args.loss == "lm" else 1.0)
+                               if args.loss in ("lm", "distill") else float(seq_loss.mean()))
+    if args.embedding:
+        result["config"]["embedding_gradient"] = True
     print(json.dumps(result))
 
 
