@@ -72,23 +72,29 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         int xend, send, yend;                // bytes from there to the arrays' ends, 2^31 - 1 at most
         __amdgpu_buffer_rsrc_t xw, sw, yw;
     };
-    auto source = [&](int t) {
+    // The tile that is read next; behind the last, the last again, which is not used.
+    int ahead_of = first;
+    const int64_t r0 = (int64_t)min(first, tiles - 1) * kRows, left = a.rows - r0;
+    const uint8_t *xp = a.codes + r0 * a.cols + c0, *sp = a.scales + r0 * a.blocks + c0 / kActBlock;
+    const uint8_t *yp = reinterpret_cast<const uint8_t *>(a.d_y + r0 * a.dy_stride + o0);
+    int64_t xleft = left * a.cols - c0, sleft = left * a.blocks - c0 / kActBlock;
+    int64_t yleft = ((left - 1) * a.dy_stride + a.out - o0) * 2;
+    auto next_source = [&]() {
+        // by scalar arithmetic of few steps: nothing else runs while it does
+        auto bound = [](int64_t bytes) { return (uint64_t)bytes >> 31 ? 0x7fffffff : (int)bytes; };
         Source f;
-        // a tile behind the last is read, as the last, but not used
-        const int64_t r0 = (int64_t)min(first + t, tiles - 1) * kRows, left = a.rows - r0;
-        auto bound = [](int64_t bytes) { return (int)min(bytes, int64_t(0x7fffffff)); };
-        f.x = a.codes + r0 * a.cols + c0;
-        f.s = a.scales + r0 * a.blocks + c0 / kActBlock;
-        f.y = reinterpret_cast<const uint8_t *>(a.d_y + r0 * a.dy_stride + o0);
-        f.xend = bound(left * a.cols - c0);
-        f.send = bound(left * a.blocks - c0 / kActBlock);
-        f.yend = bound(((left - 1) * a.dy_stride + a.out - o0) * 2);
+        f.x = xp, f.s = sp, f.y = yp;
+        f.xend = bound(xleft), f.send = bound(sleft), f.yend = bound(yleft);
         if constexpr (FAST) {
             auto window = [](const uint8_t *p, int n) {
                 return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, n, kRawBufferWord3);
             };
             f.xw = window(f.x, f.xend), f.sw = window(f.s, f.send), f.yw = window(f.y, f.yend);
         }
+        const int go = ++ahead_of < tiles ? kRows : 0;
+        const int64_t dx = (int64_t)go * a.cols, ds = (int64_t)go * a.blocks, dy = (int64_t)go * (int)a.dy_stride * 2;
+        xp += dx, sp += ds, yp += dy;
+        xleft -= dx, sleft -= ds, yleft -= dy;
         return f;
     };
     // Chunk i of a thread: XRows i (YRows i) rows below its first.
@@ -142,16 +148,20 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                 yr[d][i] = shift_down(yr[d][i], over);
         }
     };
-    auto store_x = [&](int d, int i) {
+    // Words w0 .. w1 - 1 of chunk i's eight of values, to LDS by fours.
+    unsigned wide[8];
+    auto store_x = [&](int d, int i, int w0, int w1) {
         const float s = __uint_as_float(sr[d][i] << 23);
         const unsigned w[4] = {xr[d][i].x, xr[d][i].y, xr[d][i].z, xr[d][i].w};
-        unsigned v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = widen_pair(w[j / 2], s, j % 2);
+            if (j >= w0 && j < w1)
+                wide[j] = widen_pair(w[j / 2], s, j % 2);
         u32x4 *q = reinterpret_cast<u32x4 *>(sh + xto + i * XRows * RowBytes);
-        q[0] = u32x4{v[0], v[1], v[2], v[3]};
-        q[1] = u32x4{v[4], v[5], v[6], v[7]};
+        if (w0 < 4 && w1 >= 4)
+            q[0] = u32x4{wide[0], wide[1], wide[2], wide[3]};
+        if (w1 == 8)
+            q[1] = u32x4{wide[4], wide[5], wide[6], wide[7]};
     };
     auto store_y = [&](int d, int i) {
         *reinterpret_cast<u32x4 *>(sh + yto + i * YRows * RowBytes) = yr[d][i];
@@ -175,8 +185,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     f32x4 acc[N][N] = {};   // [columns][out]
     if (n > 0) {
         Source held[kDepth];   // of the chunks in registers
-        auto fetch = [&](int d, int t) {
-            held[d] = source(t);
+        auto fetch = [&](int d) {
+            held[d] = next_source();
 #pragma unroll
             for (int i = 0; i < XPer; ++i)
                 load_x(held[d], d, i);
@@ -186,16 +196,16 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         };
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
-            fetch(d, d);
+            fetch(d);
         if constexpr (!FAST)
             settle(held[0], 0);
 #pragma unroll
         for (int i = 0; i < XPer; ++i)
-            store_x(0, i);
+            store_x(0, i, 0, 8);
 #pragma unroll
         for (int i = 0; i < YPer; ++i)
             store_y(0, i);
-        fetch(0, kDepth);
+        fetch(0);
         xto ^= Bytes, yto ^= Bytes;
         __syncthreads();
 #pragma unroll
@@ -207,7 +217,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         auto step = [&](int d, int t) {   // tile t; d: where tile t + 1 is held
             if constexpr (!FAST)
                 settle(held[d], d);
-            const Source f = source(t + 1 + kDepth);   // chunk by chunk in the places of held[d]'s
+            const Source f = next_source();   // chunk by chunk in the places of held[d]'s
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 if (g == kGroups - kAhead) {
@@ -228,9 +238,10 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                         store_y(d, g);
                         load_y(f, d, g);
                     }
-                    if (g % 3 == 1 && g / 3 < XPer && j == N - 2) {
-                        store_x(d, g / 3);
-                        load_x(f, d, g / 3);
+                    if (g % 3 == 1 && g / 3 < XPer) {
+                        store_x(d, g / 3, j * 8 / N, (j + 1) * 8 / N);
+                        if (j == N - 1)
+                            load_x(f, d, g / 3);
                     }
                 };
 #pragma unroll
