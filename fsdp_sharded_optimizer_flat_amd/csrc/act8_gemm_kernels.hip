@@ -41,6 +41,20 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int n)
     return u32x4{(unsigned)l, (unsigned)(l >> 32), (unsigned)h, (unsigned)(h >> 32)};
 }
 
+// The tile and share of the rows that a workgroup takes.  Workgroups go to the eight
+// dies in turn; each die takes neighbours among the tiles, so that a factor's tiles
+// stay in the L2 of few dies.
+constexpr unsigned kDies = 8;
+__device__ __forceinline__ void place_of(const Act8GradArgs &a, int tile, int &ct, int &ot, int &split)
+{
+    const unsigned all = gridDim.x, die = blockIdx.x % kDies, q = all / kDies, r = all % kDies;
+    const unsigned i = die * q + min(die, r) + blockIdx.x / kDies;
+    const unsigned cts = (unsigned)(a.cols + tile - 1) / tile, ots = (unsigned)(a.out + tile - 1) / tile;
+    ct = (int)(i % cts);
+    ot = (int)(i / cts % ots);
+    split = (int)(i / cts / ots);
+}
+
 // A workgroup of four waves per B x B tile of d_w, a wave per quarter.  FAST: rows
 // of both factors are whole 16-byte chunks at 16-byte addresses.
 template <int B, bool FAST, typename O>
@@ -55,10 +69,12 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     constexpr int kDepth = B == 256 ? 1 : 3;
     __shared__ __attribute__((aligned(16))) char sh[4 * Bytes];   // x', d_y; two tiles each
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int c0 = blockIdx.x * B, o0 = blockIdx.y * B;
+    int ct, ot, split;
+    place_of(a, B, ct, ot, split);
+    const int c0 = ct * B, o0 = ot * B;
     const int tiles = (int)((a.rows + kRows - 1) / kRows);
     const int per = (tiles + a.splits - 1) / a.splits;
-    const int first = blockIdx.z * per, n = min(per, tiles - first);
+    const int first = split * per, n = min(per, tiles - first);
 
     // A tile on its way: chunk i of x' and of d_y in registers.  Rows behind the last
     // are zeros; columns past a row's end may hold the next row's, which reach no
@@ -277,7 +293,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
             const int m = min(a.cols - c, 4);
             float v[4] = {acc[i][j].x, acc[i][j].y, acc[i][j].z, acc[i][j].w};
             if (a.splits > 1) {
-                float *p = a.parts + ((int64_t)blockIdx.z * a.out + o) * a.columns + c;
+                float *p = a.parts + ((int64_t)split * a.out + o) * a.columns + c;
                 *reinterpret_cast<f32x4 *>(p) = acc[i][j];
                 continue;
             }
@@ -321,7 +337,7 @@ __global__ __launch_bounds__(kBlock) void join_splits_kernel(Act8GradArgs a)
 template <int B, typename O>
 void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 {
-    const dim3 grid((a.cols + B - 1) / B, (a.out + B - 1) / B, a.splits);
+    const dim3 grid((unsigned)((a.cols + B - 1) / B) * (unsigned)((a.out + B - 1) / B) * (unsigned)a.splits);
     const bool fast = a.out % 8 == 0 && a.dy_stride % 8 == 0 && a.cols % 16 == 0 &&
                       (reinterpret_cast<uintptr_t>(a.d_y) | reinterpret_cast<uintptr_t>(a.codes)) % 16 == 0;
     if (fast)
