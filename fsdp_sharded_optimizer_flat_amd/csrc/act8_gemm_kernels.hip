@@ -357,12 +357,12 @@ void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 // these estimates, in us, fitted to sweeps over tiles and splits (what they give | what
 // was measured):
 //      rows x out x cols      256 / 1     256 / split     128 / 1     128 / split
-//   8192 x 4096 x  4096     237 | 241    287 | 288 (2)   295 | 288    344 | 330 (2)
-//   4096 x 1280 x  5120     125 | 115     85 |  79 (2)    77 |  77     99 |  95 (2)
-//   8192 x 1280 x  1280     237 | 214     57 |  54 (8)    96 |  89     51 |  52 (4)
-//   2048 x 1280 x  1280      69 |  64     36 |  33 (8)    29 |  27     24 |  23 (2)
-//   1024 x 1280 x  1280      41 |  39     30 |  29 (4)    18 |  17     18 |  18 (2)
-//  16384 x   64 x    64     461 | 408     30 |  30 (32)  186 | 170     17 |  20 (24)
+//   8192 x 4096 x  4096      223 | 225    272 | 255 (2)    282 | 279    332 | 326 (2)
+//   4096 x 1280 x  5120      118 | 107     81 |  72 (2)     74 |  75     97 |  93 (2)
+//   8192 x 1280 x  1280      223 | 194     56 |  50 (8)     83 |  83     50 |  48 (4)
+//   2048 x 1280 x  1280       65 |  58     36 |  33 (8)     26 |  26     23 |  25 (2)
+//   1024 x 1280 x  1280       38 |  35     29 |  30 (4)     16 |  16     18 |  20 (2)
+//  16384 x   64 x    64      434 | 369     35 |  29 (32)   160 | 157     21 |  20 (24)
 Act8Split act8_split(int64_t rows, int64_t out, int64_t cols)
 {
     const int64_t steps = std::max<int64_t>(1, (rows + kRows - 1) / kRows);
@@ -376,11 +376,11 @@ Act8Split act8_split(int64_t rows, int64_t out, int64_t cols)
                 continue;   // the last workgroup would have none
             // one large tile fits a compute unit, two small ones, which slow each other
             const int64_t groups = tiles * s;
-            double t = tile == 256 ? (double)((groups + 255) / 256) * (1.75 * (double)per + 13.0)
-                       : groups <= 256 ? 0.7 * (double)per + 6.5
-                                       : (double)((groups + 511) / 512) * (1.1 * (double)per + 6.5);
+            double t = tile == 256 ? (double)((groups + 255) / 256) * (1.65 * (double)per + 12.0)
+                       : groups <= 256 ? 0.6 * (double)per + 6.5
+                                       : (double)((groups + 511) / 512) * (1.05 * (double)per + 6.5);
             if (s > 1)
-                t += 3.0 + 1e-6 * (double)(s * out * cols);
+                t += 3.0 + 0.2 * (double)s + 1e-6 * (double)(s * out * cols);
             if (t < least)
                 least = t, best = {tile, (int32_t)s};
         }
