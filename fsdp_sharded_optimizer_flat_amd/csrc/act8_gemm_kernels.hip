@@ -88,7 +88,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         int xend, send, yend;                // bytes from there to the arrays' ends, 2^31 - 1 at most
         __amdgpu_buffer_rsrc_t xw, sw, yw;
     };
-    // The tile that is read next; behind the last, the last again, which is not used.
+    // The tile that is read next; behind the array's last, the last again, which is not
+    // used (FAST: behind the workgroup's last, nothing).
     int ahead_of = first;
     const int64_t r0 = (int64_t)min(first, tiles - 1) * kRows, left = a.rows - r0;
     const uint8_t *xp = a.codes + r0 * a.cols + c0, *sp = a.scales + r0 * a.blocks + c0 / kActBlock;
@@ -102,6 +103,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
         f.x = xp, f.s = sp, f.y = yp;
         f.xend = bound(xleft), f.send = bound(sleft), f.yend = bound(yleft);
         if constexpr (FAST) {
+            if (ahead_of >= first + n)
+                f.xend = f.send = f.yend = 0;
             auto window = [](const uint8_t *p, int n) {
                 return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, n, kRawBufferWord3);
             };
