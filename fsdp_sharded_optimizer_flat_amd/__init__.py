@@ -1102,6 +1102,8 @@ def zero_sequence_loss_workspace_bytes(n_tokens: int, n_seqs: int) -> int:
 def _sequences(logprob, offsets, tokens):
     """(device index, n_tokens, n_seqs, offsets address, tokens address)"""
     dev = _on_current_device(logprob, "logprob")
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a torch tensor")
     n, b = logprob.numel(), offsets.numel() - 1
     if b < 0:
         raise ValueError("offsets must hold the sequences' starts and the last one's end")
@@ -1217,6 +1219,8 @@ def _checkpoint(codes, scales, rows: int, cols: int, dev: int):
     """Addresses of a checkpoint's codes and scales."""
     blocks = (cols + ZERO_ACT8_BLOCK - 1) // ZERO_ACT8_BLOCK
     for t, n, what in ((codes, cols, "codes"), (scales, blocks, "scales")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch tensor")
         if t.shape != (rows, n):
             raise ValueError(f"{what} has shape {tuple(t.shape)}; the call needs ({rows}, {n})")
     return (_row_values(codes, rows * cols, dev, "codes", torch.uint8),

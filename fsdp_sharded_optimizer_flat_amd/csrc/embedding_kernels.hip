@@ -243,25 +243,26 @@ __global__ __launch_bounds__(kBlock) void merge_chunks_kernel(EmbeddingGradArgs 
 // -- sums over sorted tokens -----------------------------------------------------------------
 
 // The columns that a lane works on: eight from `from` on, of which n from element
-// `shift` on are its own (at a row's end the last eight; of a row of fewer than eight,
-// those).  whole: every lane of the wave has eight of its own.
+// `shift` on are its own (at a row's end the last eight, behind it none of them; of a row
+// of fewer than eight every lane works on all, the first lane has them).  Lanes that
+// work on the same columns have the same sums, so where they store the same parts they
+// store the same values.  whole: every lane of the wave has eight of its own.
 struct Columns {
-    int from, shift, n;
-    bool whole, narrow;
-    __device__ __forceinline__ Columns(int hidden, int slab)
+    int from, shift, n, hidden;
+    bool whole;
+    __device__ __forceinline__ Columns(int hidden_, int slab) : hidden(hidden_)
     {
         const int c = (slab * kWave + (int)threadIdx.x % kWave) * kOct;
-        narrow = hidden < kOct;
-        from = narrow ? 0 : min(c, hidden - kOct);
-        shift = narrow && c > 0 ? kOct : c - from;
+        from = max(min(c, hidden - kOct), 0);
+        shift = c - from;
         n = min(hidden - c, kOct);
         whole = (slab + 1) * kWave * kOct <= hidden;
     }
     template <typename T>
     __device__ __forceinline__ void load(const T *row, RawOct<T> &x) const
     {
-        if (narrow)
-            x.load(row, n);
+        if (hidden < kOct)
+            x.load(row, hidden);
         else
             x.load(row + from);
     }

@@ -259,3 +259,37 @@ def test_offsets_past_32_bits():
     d_w = torch.empty(1, cols, device=DEV)
     z.zero_act8_weight_grad(d_y, codes, scales, d_w, workspace=workspace(rows, 1, cols))
     assert torch.equal(d_w[0], 2 * x[-1].float())
+
+
+def test_more_rows_than_a_launch_holds():
+    """Rows of one element take four threads each: more than 2^31 in all."""
+    rows = 600_000_011
+    x = torch.zeros(rows, 1, dtype=torch.bfloat16, device=DEV)
+    at = [0, 1, (1 << 29) - 1, 1 << 29, rows - 2, rows - 1]
+    x[at] = torch.tensor([3.0, -5.0, 7.0, 11.0, -13.0, 0.5], dtype=torch.bfloat16, device=DEV)[:, None]
+    codes = torch.empty(rows, 1, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(rows, 1, dtype=torch.uint8, device=DEV)
+    z.zero_act8_pack(x, codes, scales)
+    y = torch.ones_like(x)
+    z.zero_act8_unpack(codes, scales, y)
+    assert torch.equal(y, x)
+
+
+@pytest.mark.parametrize("rows,out,cols", [(65, 300, 5), (130, 8, 600), (64, 257, 16), (1, 1, 40), (15, 9, 1), (16, 2, 1),
+                                           (7, 1, 40), (8, 1, 40), (1, 7, 40), (1, 8, 40), (200, 600, 17)])
+def test_weight_grad_at_the_arrays_ends(rows, out, cols):
+    """Few columns, so that a tile's chunks reach past many rows and the arrays' ends,
+    in arrays that begin anywhere and end with their allocation."""
+    g = torch.Generator(device=DEV).manual_seed(rows + cols)
+    for shift in (0, 1, 2, 5):
+        d_y, codes, scales = whole_numbers(g, rows, out, cols)
+        a = torch.full((shift + d_y.numel(),), float("nan"), dtype=torch.bfloat16, device=DEV)
+        b = torch.full((shift + codes.numel(),), 0x7f, dtype=torch.uint8, device=DEV)
+        c = torch.full((shift + scales.numel(),), 255, dtype=torch.uint8, device=DEV)
+        views = [t[shift:].view(s.shape) for t, s in ((a, d_y), (b, codes), (c, scales))]
+        for v, s in zip(views, (d_y, codes, scales)):
+            v.copy_(s)
+        want = d_y.double().T @ act8_ref.unpack_values(codes, scales).to(DEV)
+        d_w = torch.empty(out, cols, device=DEV)
+        z.zero_act8_weight_grad(*views, d_w, workspace=workspace(rows, out, cols))
+        same(d_w, want.float().cpu())

@@ -135,6 +135,53 @@ def test_grad_of_many_tokens(rows, hidden, vocab):
         assert torch.equal(d_table.double().cpu(), want), name
 
 
+@pytest.mark.parametrize("hidden", [1, 3, 7, 8, 9, 15, 511, 512, 513, 520, 1025])
+@pytest.mark.parametrize("dst", TYPES)
+def test_grad_of_runs_over_many_segments(dst, hidden):
+    """Runs that many segments share, in rows of fewer than eight columns and around a
+    wave's 512; whole numbers, so every element has to be equal."""
+    g = torch.Generator(device=DEV).manual_seed(hidden)
+    rows, vocab = 700, 4
+    for accumulate in (False, True):
+        tokens = torch.randint(-1, vocab - 1, (rows,), generator=g, device=DEV)
+        d_out = torch.randint(-2, 3, (rows, hidden), generator=g, device=DEV).to(torch.bfloat16)
+        buf, d_table = rows_of(vocab, hidden, TYPES[dst], hidden + 1, 1)
+        d_table.copy_(torch.randint(-8, 9, (vocab, hidden), generator=g, device=DEV))
+        want = d_table.double().cpu() if accumulate else torch.zeros(vocab, hidden, dtype=torch.float64)
+        ok = tokens >= 0
+        want.index_add_(0, tokens[ok].cpu(), d_out[ok].double().cpu())
+        z.zero_embedding_grad(d_out, tokens, d_table, accumulate=accumulate, workspace=workspace(rows, vocab, hidden))
+        # sums of at most 700 * 2 + 8 < 2^11: bf16 rounds those beyond 2^8
+        assert torch.equal(d_table.cpu(), want.to(TYPES[dst]))
+        assert bool((outside(buf, d_table) == KEPT).all())
+
+
+def test_grad_of_the_most_rows():
+    """ZERO_MAX_EMBEDDING_ROWS rows: the most sorted chunks that are put together."""
+    rows, vocab, hidden = z.ZERO_MAX_EMBEDDING_ROWS, 5003, 2
+    g = torch.Generator(device=DEV).manual_seed(6)
+    d_out = torch.randint(-2, 3, (rows, hidden), generator=g, device=DEV).to(torch.bfloat16)
+    for name in ("text", "mixed", "one"):
+        tokens = token_sets(g, rows, vocab)[name]
+        d_table = torch.empty(vocab, hidden, device=DEV)
+        z.zero_embedding_grad(d_out, tokens, d_table, workspace=workspace(rows, vocab, hidden))
+        ok = (tokens >= 0) & (tokens < vocab)
+        want = torch.zeros(vocab, hidden, dtype=torch.float64).index_add_(0, tokens[ok].cpu(), d_out[ok].double().cpu())
+        assert torch.equal(d_table.double().cpu(), want), name
+
+
+def test_lookup_of_more_rows_than_a_launch_holds():
+    rows, hidden = (1 << 30) + 5, 9      # two threads a row
+    table = torch.arange(3 * hidden, device=DEV).view(3, hidden).to(torch.bfloat16)
+    tokens = torch.zeros(rows, dtype=torch.int64, device=DEV)
+    ends = [0, 1, (1 << 30) - 1, 1 << 30, rows - 1]
+    tokens[ends] = torch.tensor([1, 2, 1, 2, 1], device=DEV)
+    out = torch.empty(rows, hidden, dtype=torch.bfloat16, device=DEV)
+    z.zero_embedding(table, tokens, out)
+    assert torch.equal(out[ends], table[tokens[ends]])
+    assert torch.equal(out[12345::1 << 20], table[:1].expand(len(range(12345, rows, 1 << 20)), hidden))
+
+
 def test_grad_orders_equal_tokens_by_row():
     """A token's rows are added from the first to the last: 2^24 + 1 rounds to 2^24
     (ties to even), while 1 - 2^24 is a binary32 number."""
