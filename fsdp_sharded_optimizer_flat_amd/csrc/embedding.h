@@ -19,7 +19,7 @@ struct EmbeddingArgs {
 int launch_embedding(const EmbeddingArgs &a, void *stream);
 
 // Tokens one workgroup sorts: powers of two.  Sorting takes 11 us for chunks of 2048
-// and 26 for 8192, putting chunks together 7 us for up to eight of them and 6 more for
+// and 26 for 8192, putting chunks together 7 us for up to eight of them and 5 more for
 // eight more, so small chunks serve up to 65536 tokens, unless a gradient of 128 MB or
 // more is cleared meanwhile, which takes longer than either (16384 x 4096 bf16 into
 // 128256 rows 238 us with large chunks, 245 with small ones; added to what is there, 76

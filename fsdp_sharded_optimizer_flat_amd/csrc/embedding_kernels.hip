@@ -204,24 +204,32 @@ __global__ __launch_bounds__(kBlock) void merge_chunks_kernel(EmbeddingGradArgs 
     const int own = i / a.chunk, stretch = a.chunk / kSamples;   // powers of two
     int place = i - own * a.chunk;
     for (int c0 = 0; c0 < chunks; c0 += Together) {
-        int below[Together], size[Together];
-        const uint32_t *keys[Together];
+        int below[Together] = {}, size[Together];
+        const uint32_t *keys[Together], *sample[Together];
         bool earlier[Together];
         auto is_below = [&](int t, uint32_t k) { return earlier[t] ? k <= x : k < x; };
 #pragma unroll
         for (int t = 0; t < Together; ++t) {
             const int c = min(c0 + t, chunks - 1);
             keys[t] = a.chunk_key + c * a.chunk;
+            sample[t] = samples + c * kSamples;
             size[t] = c0 + t < chunks && c != own ? min(a.rows - c * a.chunk, a.chunk) : 0;
             earlier[t] = c < own;
-            const uint32_t *sample = samples + c * kSamples;
-            int n = 0;
-#pragma unroll
-            for (int step = kSamples / 2; step > 0; step /= 2)
-                n += is_below(t, sample[n + step - 1]) ? step : 0;
-            n += is_below(t, sample[n]);   // all of them, too
-            below[t] = size[t] ? n * stretch : 0;
         }
+        // samples below: by halves of them, and the last one
+#pragma unroll
+        for (int step = kSamples / 2; step >= 0; step = step > 0 ? step / 2 : -1) {
+            uint32_t k[Together];
+#pragma unroll
+            for (int t = 0; t < Together; ++t)
+                k[t] = sample[t][below[t] + max(step, 1) - 1];
+#pragma unroll
+            for (int t = 0; t < Together; ++t)
+                below[t] += is_below(t, k[t]) ? max(step, 1) : 0;
+        }
+#pragma unroll
+        for (int t = 0; t < Together; ++t)
+            below[t] = size[t] ? below[t] * stretch : 0;
         for (int step = stretch / 2; step > 0; step /= 2) {
             uint32_t k[Together];
 #pragma unroll
@@ -370,23 +378,24 @@ __global__ __launch_bounds__(kBlock) void segment_sum_kernel(EmbeddingGradArgs a
     }
 }
 
-// The runs that begin in a segment and go on in the next: one wave per segment and
-// 512 columns.
+// The runs that begin in a segment and go on in the next: a workgroup per segment and
+// 512 columns, whose waves take a quarter each of the run's parts.
 template <typename O, bool ACC>
 __global__ __launch_bounds__(kBlock) void join_runs_kernel(EmbeddingGradArgs a)
 {
-    int s, slab;
-    unit_of(a, s, slab);
-    if (s >= a.segments - 1)
-        return;
-    const Columns c(a.hidden, slab);
+    constexpr int Waves = kBlock / kWave;
+    __shared__ f32x4 sh[Waves - 1][kWave][2];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t slabs = (uint32_t)(a.hidden + kOct * kWave - 1) / (kOct * kWave);
+    const int s = (int)(blockIdx.x / slabs);
+    const Columns c(a.hidden, (int)(blockIdx.x % slabs));
     const int lo = s * a.segment, next = lo + a.segment;
     const uint32_t run = a.key[next - 1], begins = a.key[next], before = lo > 0 ? a.key[lo - 1] : ~0u;
     if (run >= (uint32_t)a.vocab || begins != run || before == run)
         return;
     O *row = static_cast<O *>(a.d_table) + (int64_t)run * a.table_stride;
     RawOct<O> was;
-    if (ACC)
+    if (ACC && wave == 0)
         c.load(row, was);
     // the last segment that begins with the run: in steps that double, then halve
     int last = s + 1, step = 1;
@@ -396,20 +405,33 @@ __global__ __launch_bounds__(kBlock) void join_runs_kernel(EmbeddingGradArgs a)
     for (step /= 2; step > 0; step /= 2)
         if (has(last + step))
             last += step;
-    float sum[kOct];
-    load8(part_of(a, s, 1, c.from), sum);
-    for (int q = s + 1; q <= last; q += kJoinBatch) {
+    const int share = (last - s + 1 + Waves - 1) / Waves;   // parts s .. last, the first its segment's tail
+    const int from = s + wave * share, to = min(from + share, last + 1);
+    float sum[kOct] = {};
+    for (int q = from; q < to; q += kJoinBatch) {
         float x[kJoinBatch][kOct];
 #pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i)
-            load8(part_of(a, min(q + i, last), 0, c.from), x[i]);
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const int p = min(q + i, to - 1);
+            load8(part_of(a, p, p == s, c.from), x[i]);
+        }
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i)
-            if (q + i <= last)
+            if (q + i < to)
 #pragma unroll
                 for (int k = 0; k < kOct; ++k)
                     sum[k] += x[i][k];
     }
+    if (wave > 0)
+        sh[wave - 1][lane][0] = f32x4{sum[0], sum[1], sum[2], sum[3]}, sh[wave - 1][lane][1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+    __syncthreads();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int w = 0; w < Waves - 1; ++w)
+#pragma unroll
+        for (int k = 0; k < kOct; ++k)
+            sum[k] += sh[w][lane][k / 4][k % 4];
     put<O, ACC>(a, row, c, sum, was);
 }
 
@@ -436,16 +458,18 @@ void embedding_grad_of(const EmbeddingGradArgs &a, hipStream_t st)
         hipLaunchKernelGGL((sort_and_clear_kernel<O>), dim3(chunks + clear), dim3(kSortBlock), 0, st, a, chunks);
     if (a.rows == 0)
         return;
+    const dim3 entries((a.rows + kBlock - 1) / kBlock);
+    const size_t samples = chunks * kSamples * sizeof(uint32_t);
     if (chunks > 1)
-        hipLaunchKernelGGL(merge_chunks_kernel, dim3((a.rows + kBlock - 1) / kBlock), dim3(kBlock),
-                           chunks * kSamples * sizeof(uint32_t), st, a, chunks);
+        hipLaunchKernelGGL(merge_chunks_kernel, entries, dim3(kBlock), samples, st, a, chunks);
     const int64_t units = (int64_t)a.segments * ((a.hidden + kOct * kWave - 1) / (kOct * kWave));
     const dim3 grid((unsigned)((units + kBlock / kWave - 1) / (kBlock / kWave)));
     auto sums = [&](auto acc) {
         constexpr bool ACC = decltype(acc)::value;
         hipLaunchKernelGGL((segment_sum_kernel<T, O, ACC>), grid, dim3(kBlock), 0, st, a);
-        if (a.segments > 1)
-            hipLaunchKernelGGL((join_runs_kernel<O, ACC>), grid, dim3(kBlock), 0, st, a);
+        if (a.segments > 1)   // the last segment's run goes on nowhere
+            hipLaunchKernelGGL((join_runs_kernel<O, ACC>), dim3((unsigned)(units - units / a.segments)), dim3(kBlock), 0,
+                               st, a);
     };
     if (a.accumulate)
         sums(std::true_type());
