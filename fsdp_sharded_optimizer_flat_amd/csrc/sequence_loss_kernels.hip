@@ -85,10 +85,12 @@ struct Quad {
     // Which of the positions are targets of the range, as bits.
     __device__ __forceinline__ unsigned targets(int64_t t, const Range &r) const
     {
+        const int from = (int)min(max(r.lo - t, int64_t(0)), int64_t(kQuadTokens));
+        const int to = (int)min(max(r.hi - t, int64_t(0)), int64_t(kQuadTokens));
         unsigned on = 0;
 #pragma unroll
         for (int k = 0; k < kQuadTokens; ++k)
-            on |= (unsigned)(t + k >= r.lo && t + k < r.hi && token[k / 2][k % 2] >= 0) << k;
+            on |= (unsigned)(k >= from && k < to && token[k / 2][k % 2] >= 0) << k;
         return on;
     }
 };
@@ -190,8 +192,8 @@ __device__ __forceinline__ Share share_of(const Sequences &s, int64_t slot)
     h.none = !h.first && (h.tile < begin || h.part.lo >= h.part.hi);
     return h;
 }
-// The sums of a sequence's shares, in every lane.
-__device__ __forceinline__ SequencePart total_of(const Sequences &s, int64_t b, const Range &r)
+// A lane's part of the sums of a sequence's shares.
+__device__ __forceinline__ SequencePart parts_of(const Sequences &s, int64_t b, const Range &r)
 {
     SequencePart p{};
     if (r.hi > r.lo) {
@@ -199,7 +201,7 @@ __device__ __forceinline__ SequencePart total_of(const Sequences &s, int64_t b, 
         for (int64_t i = first + threadIdx.x % kWave; i <= last; i += kWave)
             add(p, s.parts[i]);
     }
-    return wave_total(p);
+    return p;
 }
 
 // -- policy ---------------------------------------------------------------------------
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(kBlock) void policy_join_kernel(PolicyArgs a)
     if (scale)
         load_quad(a.d_logprob, t0, h.part, g);
     const double d_loss = scale ? a.d_loss[h.b] : 0.0;
-    const SequencePart sum = total_of(a.seq, h.b, h.seq);
+    const SequencePart sum = wave_total(parts_of(a.seq, h.b, h.seq));
     if (h.first && threadIdx.x % kWave == 0)
         put_policy(a, h.b, sum);
     if (!scale)
@@ -399,24 +401,30 @@ __global__ __launch_bounds__(kBlock) void policy_join_kernel(PolicyArgs a)
 // -- preference -----------------------------------------------------------------------
 
 // A pair's loss and its derivative by h.
-__device__ __forceinline__ void preference(const PreferenceArgs &a, double h, double &loss, double &slope)
+__device__ __forceinline__ double preference_loss(const PreferenceArgs &a, double h)
 {
     if (a.kind == ZERO_PREFER_SIGMOID) {
         // ln(1 + e^v) = max(v, 0) + ln(1 + e^-|v|); of an infinite h too
         const double near = log1p(exp(-fabs(h))), eps = a.smoothing;
         const double up = fmax(h, 0.0) + near, down = fmax(-h, 0.0) + near;
-        loss = eps == 0.0 ? down : eps == 1.0 ? up : (1.0 - eps) * down + eps * up;
-        slope = eps / (1.0 + exp(-h)) - (1.0 - eps) / (1.0 + exp(h));
-        if (h != h)
-            loss = h;
-    } else if (a.kind == ZERO_PREFER_HINGE) {
-        loss = h >= 1.0 ? 0.0 : 1.0 - h;
-        slope = h >= 1.0 ? 0.0 : h != h ? h : -1.0;
-    } else {
-        const double u = (h - 0.5) / a.beta;
-        loss = u * u;
-        slope = 2.0 * u / a.beta;
+        return h != h ? h : eps == 0.0 ? down : eps == 1.0 ? up : (1.0 - eps) * down + eps * up;
     }
+    if (a.kind == ZERO_PREFER_HINGE)
+        return h >= 1.0 ? 0.0 : 1.0 - h;
+    const double u = (h - 0.5) / a.beta;
+    return u * u;
+}
+__device__ __forceinline__ double preference_slope(const PreferenceArgs &a, double h)
+{
+    if (a.kind == ZERO_PREFER_SIGMOID) {
+        // 1 / (1 + e^h) = e^-h / (1 + e^-h): of the smaller exponential, which is finite
+        const double e = exponential(-fabs(h)).e, less = e / (1.0 + e), more = 1.0 / (1.0 + e);
+        return h >= 0.0 ? a.smoothing * more - (1.0 - a.smoothing) * less
+                        : a.smoothing * less - (1.0 - a.smoothing) * more;
+    }
+    if (a.kind == ZERO_PREFER_HINGE)
+        return h >= 1.0 ? 0.0 : h != h ? h : -1.0;
+    return 2.0 * (h - 0.5) / (a.beta * a.beta);
 }
 
 __device__ __forceinline__ unsigned ratio_quad(const PreferenceArgs &a, int64_t t, const Range &r, SequencePart &sum)
@@ -438,24 +446,28 @@ __device__ __forceinline__ void put_constant(const PreferenceArgs &a, int64_t t,
         v[k] = on >> k & 1 ? g : 0.0f;
     store_quad(a.d_logprob, t, r, v);
 }
-// Pair p from its sequences' sums: writes its loss and rewards where `put`, returns
-// the gradient of the chosen (of the rejected) sequence's targets.
-__device__ __forceinline__ float pair_gradient(const PreferenceArgs &a, int64_t p, const SequencePart &chosen,
-                                               const SequencePart &rejected, bool put, bool of_rejected)
+// Pair p from its sequences' sums, as log ratios and targets: lane `put` writes its loss
+// and rewards, every lane gets the gradient of the chosen (of the rejected) sequence's
+// targets.  `writes`: the same in every lane, whether one of them puts.
+__device__ __forceinline__ float pair_gradient(const PreferenceArgs &a, int64_t p, double chosen, int chosen_targets,
+                                               double rejected, int rejected_targets, bool writes, bool put,
+                                               bool of_rejected)
 {
-    const double wc = weight_of(a.seq, chosen.targets), wr = weight_of(a.seq, rejected.targets);
-    const double rc = a.beta * (chosen.a * wc), rr = a.beta * (rejected.a * wr);
-    double loss, slope;
-    preference(a, rc - rr - a.margin, loss, slope);
-    if (put) {
-        if (a.loss)
-            a.loss[p] = (float)loss;
-        if (a.reward)
-            a.reward[p] = (float)rc, a.reward[p + a.pairs] = (float)rr;
+    const double wc = weight_of(a.seq, chosen_targets), wr = weight_of(a.seq, rejected_targets);
+    const double rc = a.beta * (chosen * wc), rr = a.beta * (rejected * wr);
+    const double h = rc - rr - a.margin;
+    if (writes) {
+        const double loss = preference_loss(a, h);
+        if (put) {
+            if (a.loss)
+                a.loss[p] = (float)loss;
+            if (a.reward)
+                a.reward[p] = (float)rc, a.reward[p + a.pairs] = (float)rr;
+        }
     }
     if (!a.d_logprob)
         return 0.0f;
-    const double up = (double)a.d_loss[p] * slope * a.beta;
+    const double up = (double)a.d_loss[p] * preference_slope(a, h) * a.beta;
     return (float)(of_rejected ? -up * wr : up * wc);
 }
 
@@ -478,7 +490,8 @@ __global__ __launch_bounds__(NT) void preference_kernel(PreferenceArgs a)
     if (threadIdx.x % Half == 0)
         both[side] = sum;
     __syncthreads();
-    const float g = pair_gradient(a, p, both[0], both[1], threadIdx.x == 0, side == 1);
+    const float g = pair_gradient(a, p, both[0].a, both[0].targets, both[1].a, both[1].targets, threadIdx.x < kWave,
+                                  threadIdx.x == 0, side == 1);
     if (!a.d_logprob)
         return;
     put_constant(a, t0, r, held, g);
@@ -514,16 +527,23 @@ __global__ __launch_bounds__(kBlock) void preference_join_kernel(PreferenceArgs 
     if (h.none || !(put || write))
         return;
     const int64_t p = rejected ? h.b - a.pairs : h.b, o = rejected ? p : p + a.pairs;
-    const SequencePart own = total_of(a.seq, h.b, h.seq), other = total_of(a.seq, o, range_of(a.seq, o));
-    const float g = pair_gradient(a, p, rejected ? other : own, rejected ? own : other,
-                                  put && threadIdx.x % kWave == 0, rejected);
+    // the first round's targets are on their way while the parts are added up
+    const int64_t t0 = (h.tile << a.seq.cut.shift) + threadIdx.x % kWave * kQuadTokens;
+    const float *const none[1] = {nullptr};
+    const Quad<1> ahead(a.seq, none, t0, h.part);
+    // both sequences' sums at once: log ratios in a and b, targets in cut and targets
+    const SequencePart own = parts_of(a.seq, h.b, h.seq), other = parts_of(a.seq, o, range_of(a.seq, o));
+    const SequencePart both = wave_total(SequencePart{own.a, other.a, own.targets, other.targets});
+    const float g = rejected ? pair_gradient(a, p, both.b, both.targets, both.a, both.cut, put,
+                                             put && threadIdx.x % kWave == 0, true)
+                             : pair_gradient(a, p, both.a, both.cut, both.b, both.targets, put,
+                                             put && threadIdx.x % kWave == 0, false);
     if (!write)
         return;
-    const int64_t begin = h.tile << a.seq.cut.shift;
     const int rounds = 1 << (a.seq.cut.shift - kRoundShift);
     for (int i = 0; i < rounds; ++i) {
-        const int64_t t = begin + (int64_t)(i * kWave + threadIdx.x % kWave) * kQuadTokens;
-        put_constant(a, t, h.part, targets_of(a.seq, t, h.part), g);
+        const int64_t t = t0 + (int64_t)i * kWave * kQuadTokens;
+        put_constant(a, t, h.part, i == 0 ? ahead.targets(t, h.part) : targets_of(a.seq, t, h.part), g);
     }
 }
 
