@@ -12,7 +12,7 @@ namespace zero {
 namespace {
 
 zero_status check_sequences(const int64_t *tokens, int64_t n_tokens, const int64_t *offsets,
-                            int64_t n_seqs, int32_t mode, Sequences *s)
+                            int64_t n_seqs, int32_t mode, int64_t mean, Sequences *s)
 {
     if (n_tokens < 0 || n_seqs < 0 || (mode != ZERO_SEQUENCE_MEAN && mode != ZERO_SEQUENCE_SUM))
         return ZERO_EINVAL;
@@ -20,7 +20,7 @@ zero_status check_sequences(const int64_t *tokens, int64_t n_tokens, const int64
         return ZERO_ERANGE;
     if (n_seqs > 0 && !offsets)
         return ZERO_EINVAL;
-    *s = Sequences{tokens, offsets, n_tokens, n_seqs, mode, sequence_cut(n_tokens, n_seqs), nullptr};
+    *s = Sequences{tokens, offsets, n_tokens, n_seqs, mode, sequence_cut(n_tokens, n_seqs, mean), nullptr};
     return ZERO_OK;
 }
 
@@ -31,9 +31,9 @@ bool within(double x, double lo, double hi) { return x >= lo && x <= hi; }
 
 }  // namespace
 
-SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs)
+SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs, int64_t mean)
 {
-    if (n_tokens <= kSequenceShort || n_seqs == 0)
+    if (n_seqs == 0 || (n_tokens <= kSequenceShort && n_tokens / n_seqs <= mean))
         return {kRoundShift, 0};
     // every wave of a sequence adds up all its parts: tiles grow before an even share of
     // the positions has more than 1024 of them
@@ -54,7 +54,7 @@ extern "C" zero_status zero_sequence_loss_workspace_bytes(int64_t n_tokens, int6
         return ZERO_EINVAL;
     if (n_tokens > ZERO_MAX_LOSS_ROWS || n_seqs > ZERO_MAX_SEQUENCES)
         return ZERO_ERANGE;
-    *bytes = (size_t)parts_bytes(sequence_cut(n_tokens, n_seqs));
+    *bytes = (size_t)parts_bytes(sequence_cut(n_tokens, n_seqs, kPolicyShort));
     return ZERO_OK;
 }
 
@@ -68,7 +68,7 @@ extern "C" zero_status zero_policy_loss(const float *logprob, const float *old_l
                                         size_t workspace_bytes, void *stream)
 {
     PolicyArgs a{};
-    if (zero_status s = check_sequences(tokens, n_tokens, offsets, n_seqs, mode, &a.seq))
+    if (zero_status s = check_sequences(tokens, n_tokens, offsets, n_seqs, mode, kPolicyShort, &a.seq))
         return s;
     if (!within(clip_low, 0.0, 1.0) || !within(clip_high, 0.0, INFINITY) ||
         !within(kl_coef, 0.0, 1.7e308) || (!ref_logprob && (kl || (kl_coef != 0.0 && n_tokens > 0))))
@@ -120,7 +120,7 @@ extern "C" zero_status zero_preference_loss(const float *logprob, const float *r
         return ZERO_EINVAL;
     if (n_pairs > ZERO_MAX_SEQUENCES / 2)
         return ZERO_ERANGE;
-    if (zero_status s = check_sequences(tokens, n_tokens, offsets, 2 * n_pairs, mode, &a.seq))
+    if (zero_status s = check_sequences(tokens, n_tokens, offsets, 2 * n_pairs, mode, kSequenceShort, &a.seq))
         return s;
     if ((kind != ZERO_PREFER_SIGMOID && kind != ZERO_PREFER_HINGE && kind != ZERO_PREFER_SQUARED) ||
         !std::isfinite(beta) || !(beta > 0.0) || !std::isfinite(margin) || !within(smoothing, 0.0, 1.0) ||

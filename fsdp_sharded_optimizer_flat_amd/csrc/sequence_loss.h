@@ -6,8 +6,10 @@
 
 namespace zero {
 
-// Up to this many positions a call is one launch, a workgroup to a sequence or pair.
-constexpr int64_t kSequenceShort = 16384;
+// Up to this many positions a call is one launch, a workgroup to a sequence or pair;
+// the policy loss only if its sequences have at most kPolicyShort positions on average,
+// which a workgroup of 512 reads once.
+constexpr int64_t kSequenceShort = 16384, kPolicyShort = 2048;
 
 // Longer ones are cut into tiles of 2^shift positions, whole rounds of a wave (four
 // positions to a lane); a wave takes a sequence's share of a tile.
@@ -16,7 +18,7 @@ struct SequenceCut {
     int32_t shift;
     int64_t slots;   // shares at most; 0: not cut
 };
-SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs);
+SequenceCut sequence_cut(int64_t n_tokens, int64_t n_seqs, int64_t mean);   // whole up to `mean` each
 
 // A share's sums.  Policy: of the losses and k, targets beyond the border; preference:
 // of the log ratios.

@@ -549,7 +549,7 @@ __global__ __launch_bounds__(kBlock) void preference_join_kernel(PreferenceArgs 
 
 // Threads of a workgroup that takes a sequence of `mean` positions on average; some
 // are several times as long.
-int threads_for(int64_t mean) { return mean <= 32 ? 64 : mean <= 512 ? 256 : 1024; }
+int threads_for(int64_t mean) { return mean <= 32 ? 64 : mean <= 512 ? 256 : 512; }
 
 unsigned share_groups(const Sequences &s)
 {
@@ -570,7 +570,7 @@ int launch_policy_loss(const PolicyArgs &a, void *stream)
     switch (threads_for(a.seq.n_tokens / a.seq.n)) {
     case 64: hipLaunchKernelGGL((policy_kernel<64>), grid, dim3(64), 0, st, a); break;
     case 256: hipLaunchKernelGGL((policy_kernel<256>), grid, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((policy_kernel<1024>), grid, dim3(1024), 0, st, a);
+    default: hipLaunchKernelGGL((policy_kernel<512>), grid, dim3(512), 0, st, a);
     }
     return hipGetLastError();
 }
