@@ -8,6 +8,13 @@
 // 10^-3) keeps its digits, and sums over long sequences lose nothing.  MI355X adds and
 // multiplies binary64 as fast as unpacked binary32.
 //
+// Short calls are bound by their way to the device: 1 sequence of 1024 positions is 5 us
+// of kernel and 8.5 us from call to call.  Long ones by a wave's chain of search, loads,
+// terms and sums: 300 sequences of 3400 with a KL term take 10.4 us for the terms, two
+// exponentials a target in some 90 binary64 instructions, and 6.0 to scale the
+// gradients, where the memory's traffic is 4.3 us; 128 pairs of sequences of 4000, a
+// subtraction a target, 5.1 and 6.8 of 3.1.
+//
 // Few positions: a workgroup to a sequence or pair, one launch.  Many: the array is
 // cut into tiles and a wave takes what a sequence has of one, so the work is even
 // whatever the lengths.  Share (b, tile) has slot tile + b: the tiles of the sequences
@@ -548,8 +555,14 @@ __global__ __launch_bounds__(kBlock) void preference_join_kernel(PreferenceArgs 
 }
 
 // Threads of a workgroup that takes a sequence of `mean` positions on average; some
-// are several times as long.
-int threads_for(int64_t mean) { return mean <= 32 ? 64 : mean <= 512 ? 256 : 512; }
+// are several times as long.  16384 positions of the policy (of the preference) loss, us,
+// most of them the call's way to the device, with
+//   sequences of     64 threads      256          512
+//       8            9.3 ( 8.2)    9.1 (10.0)  15.9 (18.0)
+//      16            9.2 ( 8.2)    8.9 ( 8.0)  10.0 (10.3)
+//     256           12.3 (10.8)    8.9 ( 8.1)   9.2 ( 8.1)
+//     819           22.7 ( 7.9)    9.5 ( 8.0)   9.0 ( 8.2)
+int threads_for(int64_t mean) { return mean <= 8 ? 64 : mean <= 512 ? 256 : 512; }
 
 unsigned share_groups(const Sequences &s)
 {
