@@ -279,7 +279,8 @@ def _run_own(st):
                 SQUARED: z.ZERO_PREFER_SQUARED}[case["kind"]]
         z.zero_preference_loss(st["logprob"], st["offsets"], tokens=st["tokens"],
                                ref_logprob=st["ref"], kind=kind, beta=case["beta"],
-                               margin=case["margin"], smoothing=case["smoothing"], mode=mode,
+                               margin=case["margin"], mode=mode,
+                               smoothing=case["smoothing"] if case["kind"] == SIGMOID else 0.0,
                                d_loss=d_loss, loss=o["loss"], reward=o["reward"],
                                d_logprob=o.get("d_logprob"), workspace=st["workspace"])
     elif op == "embed":
