@@ -403,7 +403,8 @@ int launch_act8_weight_grad(const Act8GradArgs &a, void *stream)
 {
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     by_types(ZERO_F32, a.w_dtype, [&](auto, auto o) {
-        if (a.rows * a.cols < 16 || (a.rows - 1) * a.dy_stride + a.out < 8)
+        // (no rows: the tiled kernel writes zeros, of any size)
+        if (a.rows > 0 && (a.rows * a.cols < 16 || (a.rows - 1) * a.dy_stride + a.out < 8))
             hipLaunchKernelGGL((weight_grad_of_few_kernel<decltype(o)>),
                                dim3((unsigned)(((int64_t)a.out * a.cols + kBlock - 1) / kBlock)), dim3(kBlock), 0, st, a);
         else if (a.tile == 256)

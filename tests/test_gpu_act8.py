@@ -293,3 +293,12 @@ def test_weight_grad_at_the_arrays_ends(rows, out, cols):
         d_w = torch.empty(out, cols, device=DEV)
         z.zero_act8_weight_grad(*views, d_w, workspace=workspace(rows, out, cols))
         same(d_w, want.float().cpu())
+
+
+def test_weight_grad_no_rows_of_many_elements():
+    """More than 2^32 elements of zeros."""
+    n = 65600
+    d_w = torch.ones(n, n, dtype=torch.bfloat16, device=DEV)
+    empty = lambda cols, dtype: torch.empty(0, cols, dtype=dtype, device=DEV)
+    z.zero_act8_weight_grad(empty(n, torch.bfloat16), empty(n, torch.uint8), empty(n // 32, torch.uint8), d_w)
+    assert not any(bool(rows.any()) for rows in d_w.split(4096))
