@@ -75,10 +75,9 @@ zero_status check_grad_sizes(int64_t rows, int64_t out_features, int64_t cols)
         return ZERO_EINVAL;
     return out_features > ZERO_MAX_HIDDEN ? ZERO_ERANGE : ZERO_OK;
 }
-int64_t whole_quads(int64_t cols) { return (cols + 3) / 4 * 4; }
 int64_t parts_bytes(const Act8Split &s, int64_t out, int64_t cols)
 {
-    return s.splits > 1 ? s.splits * out * whole_quads(cols) * 4 : 0;
+    return s.splits * s.shared(out, cols) * s.tile * s.tile * 4;
 }
 }  // namespace
 
@@ -136,7 +135,7 @@ extern "C" zero_status zero_act8_weight_grad(const uint16_t *d_y, int64_t rows,
     a.accumulate = accumulate;
     a.tile = split.tile;
     a.splits = split.splits;
-    a.columns = (int32_t)whole_quads(cols);
+    a.whole = split.whole;
     a.parts = static_cast<float *>(workspace);
     return done(launch_act8_weight_grad(a, stream), "zero_act8_weight_grad");
 }

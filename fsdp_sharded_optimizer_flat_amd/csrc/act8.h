@@ -24,12 +24,17 @@ struct Act8GradArgs {
     void *d_w;
     int64_t rows, dy_stride, w_stride;
     int32_t out, cols, blocks, w_dtype, accumulate;
-    int32_t tile, splits;     // d_w's tiles; workgroups that share a tile's rows
-    int32_t columns;          // of the parts: cols rounded up to whole quads
-    float *parts;             // splits x out x columns, where splits > 1
+    int32_t tile;             // d_w's tiles: tile x tile
+    int32_t splits;           // workgroups that share a tile's rows, but for
+    int32_t whole;            // the first tiles, which a workgroup each takes whole
+    float *parts;             // splits x the other tiles x tile x tile
 };
 struct Act8Split {
-    int32_t tile, splits;
+    int32_t tile, splits, whole;
+    int64_t shared(int64_t out, int64_t cols) const   // tiles that are not whole
+    {
+        return ((out + tile - 1) / tile) * ((cols + tile - 1) / tile) - whole;
+    }
 };
 Act8Split act8_split(int64_t rows, int64_t out, int64_t cols);
 int launch_act8_weight_grad(const Act8GradArgs &a, void *stream);

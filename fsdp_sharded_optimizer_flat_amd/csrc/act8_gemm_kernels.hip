@@ -11,8 +11,8 @@
 // same for both factors and otherwise free: lanes 16 g .. 16 g + 15 hold rows 4 g ..
 // 4 g + 3 and 16 more.
 //
-// Bound by the matrix cores' feeding: 8192 x 14336 x 4096 into bf16 takes 820 to 910 us,
-// 1.06 to 1.18 PFLOP/s, where the library's product of two bf16 matrices takes 1010 to
+// Bound by the matrix cores' feeding: 8192 x 14336 x 4096 into bf16 takes 815 to 860 us,
+// 1.12 to 1.18 PFLOP/s, as the clock goes, where the library's product of two bf16 matrices takes 1010 to
 // 1040; 8192 x 4096 x 4096 225 (230), with products under way in 51 % of the cycles and
 // LDS busy in 32 %.  Small outputs have too few tiles for the device and are bound by a
 // tile's latency: 1023 x 1280 x 1280 takes 15.7 us on 100 compute units (library: 20).
@@ -47,24 +47,33 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int n)
     return u32x4{(unsigned)l, (unsigned)(l >> 32), (unsigned)h, (unsigned)(h >> 32)};
 }
 
-// The tile and share of the rows that a workgroup takes.  Workgroups go to the eight
-// dies in turn; each die takes neighbours among the tiles, so that a factor's tiles
-// stay in the L2 of few dies.
+// The tile and share of the rows that a workgroup takes, and its part (none: -1).
+// Workgroups go to the eight dies in turn; each die takes neighbours among the tiles, so
+// that a factor's tiles stay in the L2 of few dies.
 constexpr unsigned kDies = 8;
-__device__ __forceinline__ void place_of(const Act8GradArgs &a, int tile, int &ct, int &ot, int &split)
+__device__ __forceinline__ void place_of(const Act8GradArgs &a, int tile, int &ct, int &ot, int &split, int &part)
 {
-    const unsigned all = gridDim.x, die = blockIdx.x % kDies, q = all / kDies, r = all % kDies;
-    const unsigned i = die * q + min(die, r) + blockIdx.x / kDies;
-    const unsigned cts = (unsigned)(a.cols + tile - 1) / tile, ots = (unsigned)(a.out + tile - 1) / tile;
+    const unsigned whole = (unsigned)a.whole;
+    const bool shared = blockIdx.x >= whole;
+    const unsigned b = shared ? blockIdx.x - whole : blockIdx.x, all = shared ? gridDim.x - whole : whole;
+    const unsigned die = b % kDies, q = all / kDies, r = all % kDies;
+    unsigned i = die * q + min(die, r) + b / kDies;
+    const unsigned cts = (unsigned)(a.cols + tile - 1) / tile;
+    split = 0, part = -1;
+    if (shared) {
+        const unsigned tiles = all / (unsigned)a.splits;
+        part = (int)i;
+        split = (int)(i / tiles);
+        i = whole + i % tiles;
+    }
     ct = (int)(i % cts);
-    ot = (int)(i / cts % ots);
-    split = (int)(i / cts / ots);
+    ot = (int)(i / cts);
 }
 
 // A workgroup of four waves per B x B tile of d_w, a wave per quarter.  FAST: rows
 // of both factors are whole 16-byte chunks at 16-byte addresses, read through buffer
-// descriptors, whose bounds replace the general path's (8192 x 14336 x 4096: 825 us, by
-// the general path 866).
+// descriptors, whose bounds replace the general path's (8192 x 14336 x 4096 with whole
+// tiles: 825 us, by the general path 866).
 template <int B, bool FAST, typename O>
 __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
 {
@@ -77,11 +86,11 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     constexpr int kDepth = B == 256 ? 1 : 3;
     __shared__ __attribute__((aligned(16))) char sh[4 * Bytes];   // x', d_y; two tiles each
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    int ct, ot, split;
-    place_of(a, B, ct, ot, split);
+    int ct, ot, split, part;
+    place_of(a, B, ct, ot, split, part);
     const int c0 = ct * B, o0 = ot * B;
     const int tiles = (int)((a.rows + kRows - 1) / kRows);
-    const int per = (tiles + a.splits - 1) / a.splits;
+    const int per = part < 0 ? tiles : (tiles + a.splits - 1) / a.splits;
     const int first = split * per, n = min(per, tiles - first);
 
     // A tile on its way: chunk i of x' and of d_y in registers.  Rows behind the last
@@ -303,8 +312,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
                 continue;
             const int m = min(a.cols - c, 4);
             float v[4] = {acc[i][j].x, acc[i][j].y, acc[i][j].z, acc[i][j].w};
-            if (a.splits > 1) {
-                float *p = a.parts + ((int64_t)split * a.out + o) * a.columns + c;
+            if (part >= 0) {
+                float *p = a.parts + (int64_t)part * (B * B) + (o - o0) * B + c - c0;
                 *reinterpret_cast<f32x4 *>(p) = acc[i][j];
                 continue;
             }
@@ -329,18 +338,20 @@ __global__ __launch_bounds__(kBlock) void weight_grad_of_few_kernel(Act8GradArgs
     put4(static_cast<O *>(a.d_w) + (int64_t)o * a.w_stride + c, 1, sum, a.accumulate);
 }
 
-// The parts of each element added in order; four columns to a thread.
-template <typename O>
+// The parts of each element of the shared tiles added in order; four columns to a
+// thread, a workgroup per kBlock of them within a tile.
+template <int B, typename O>
 __global__ __launch_bounds__(kBlock) void join_splits_kernel(Act8GradArgs a)
 {
-    const int quads = a.columns / 4;
-    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-    if (i >= (int64_t)quads * a.out)
+    constexpr unsigned Groups = B * B / 4 / kBlock;   // of a tile
+    const unsigned t = blockIdx.x / Groups, quad = blockIdx.x % Groups * kBlock + threadIdx.x;
+    const unsigned tiles = gridDim.x / Groups, cts = (unsigned)(a.cols + B - 1) / B, tile = (unsigned)a.whole + t;
+    const int o = (int)(tile / cts * B + quad / (B / 4)), c = (int)(tile % cts * B + quad % (B / 4) * 4);
+    if (o >= a.out || c >= a.cols)
         return;
-    const int o = (int)(i / quads), c = (int)(i - (int64_t)o * quads) * 4;
     f32x4 sum = {};
     for (int s = 0; s < a.splits; ++s)
-        sum += *reinterpret_cast<const f32x4 *>(a.parts + ((int64_t)s * a.out + o) * a.columns + c);
+        sum += *reinterpret_cast<const f32x4 *>(a.parts + ((int64_t)s * tiles + t) * (B * B) + quad * 4);
     const float v[4] = {sum.x, sum.y, sum.z, sum.w};
     put4(static_cast<O *>(a.d_w) + (int64_t)o * a.w_stride + c, min(a.cols - c, 4), v, a.accumulate);
 }
@@ -348,24 +359,25 @@ __global__ __launch_bounds__(kBlock) void join_splits_kernel(Act8GradArgs a)
 template <int B, typename O>
 void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.cols + B - 1) / B) * (unsigned)((a.out + B - 1) / B) * (unsigned)a.splits);
+    const unsigned shared = (unsigned)Act8Split{B, a.splits, a.whole}.shared(a.out, a.cols);
+    const dim3 grid((unsigned)a.whole + shared * (unsigned)a.splits);
     const bool fast = a.out % 8 == 0 && a.dy_stride % 8 == 0 && a.cols % 16 == 0 &&
                       (reinterpret_cast<uintptr_t>(a.d_y) | reinterpret_cast<uintptr_t>(a.codes)) % 16 == 0;
     if (fast)
         hipLaunchKernelGGL((weight_grad_kernel<B, true, O>), grid, dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL((weight_grad_kernel<B, false, O>), grid, dim3(256), 0, st, a);
-    if (a.splits > 1)
-        hipLaunchKernelGGL((join_splits_kernel<O>), dim3((unsigned)(((int64_t)a.columns / 4 * a.out + kBlock - 1) / kBlock)),
-                           dim3(kBlock), 0, st, a);
+    if (shared > 0)
+        hipLaunchKernelGGL((join_splits_kernel<B, O>), dim3(shared * (B * B / 4 / kBlock)), dim3(kBlock), 0, st, a);
 }
 
 }  // namespace
 
 // Tiles of 256 x 256 read LDS half as often for a product as those of 128 x 128, but
 // small outputs have few of them; rows are split over workgroups where there are few
-// tiles of either kind, at the price of the parts' way through memory.  The least of
-// these estimates, in us, fitted to sweeps over tiles and splits (what they give | what
+// tiles of either kind, at the price of the parts' way through memory; or only those of
+// the last tiles that do not fill the device (8192 x 14336 x 4096, 128 of 896: 850 : 815
+// us; 8192 x 4095 x 4097, 16 of 272: 400 : 276).  The least of these estimates, in us, fitted to sweeps over tiles and splits (what they give | what
 // was measured):
 //      rows x out x cols      256 / 1     256 / split     128 / 1     128 / split
 //   8192 x 4096 x  4096      223 | 225    272 | 255 (2)    282 | 279    332 | 326 (2)
@@ -377,23 +389,33 @@ void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 Act8Split act8_split(int64_t rows, int64_t out, int64_t cols)
 {
     const int64_t steps = std::max<int64_t>(1, (rows + kRows - 1) / kRows);
-    Act8Split best{128, 1};
+    Act8Split best{128, 1, 0};
     double least = 1e300;
     for (int32_t tile : {256, 128}) {
         const int64_t tiles = ((out + tile - 1) / tile) * ((cols + tile - 1) / tile);
+        // one large tile fits a compute unit, two small ones, which slow each other
+        const int64_t round = tile == 256 ? 256 : 512;
+        auto time = [&](int64_t groups, int64_t per) {
+            return tile == 256    ? (double)((groups + 255) / 256) * (1.65 * (double)per + 12.0)
+                   : groups <= 256 ? 0.6 * (double)per + 6.5
+                                   : (double)((groups + 511) / 512) * (1.05 * (double)per + 6.5);
+        };
         for (int64_t s = 1; s <= std::min<int64_t>(steps, 64); ++s) {
             const int64_t per = (steps + s - 1) / s;
             if ((steps + per - 1) / per != s)
                 continue;   // the last workgroup would have none
-            // one large tile fits a compute unit, two small ones, which slow each other
-            const int64_t groups = tiles * s;
-            double t = tile == 256 ? (double)((groups + 255) / 256) * (1.65 * (double)per + 12.0)
-                       : groups <= 256 ? 0.6 * (double)per + 6.5
-                                       : (double)((groups + 511) / 512) * (1.05 * (double)per + 6.5);
-            if (s > 1)
-                t += 3.0 + 0.2 * (double)s + 1e-6 * (double)(s * out * cols);
-            if (t < least)
-                least = t, best = {tile, (int32_t)s};
+            // all tiles shared, or those of the last round
+            for (int64_t whole : {s == 1 ? tiles : 0, tiles / round * round}) {
+                const int64_t rest = tiles - whole;
+                if (rest > 0 && s == 1)
+                    continue;
+                double t = rest < tiles ? time(whole, steps) : 0.0;
+                if (rest > 0)
+                    t += time(rest * s, per) + 3.0 + 0.2 * (double)s +
+                         1e-6 * (double)(s * std::min(rest * tile * tile, out * cols));
+                if (t < least)
+                    least = t, best = {tile, (int32_t)s, (int32_t)whole};
+            }
         }
     }
     return best;
