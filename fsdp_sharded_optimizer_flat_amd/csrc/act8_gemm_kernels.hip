@@ -376,9 +376,11 @@ void weight_grad_of(const Act8GradArgs &a, hipStream_t st)
 // Tiles of 256 x 256 read LDS half as often for a product as those of 128 x 128, but
 // small outputs have few of them; rows are split over workgroups where there are few
 // tiles of either kind, at the price of the parts' way through memory; or only those of
-// the last tiles that do not fill the device (8192 x 14336 x 4096, 128 of 896: 850 : 815
-// us; 8192 x 4095 x 4097, 16 of 272: 400 : 276).  The least of these estimates, in us, fitted to sweeps over tiles and splits (what they give | what
-// was measured):
+// the last tiles that do not fill the device (8192 x 14336 x 4096, 128 of 896: 850 us
+// without, 815 with it; 8192 x 4095 x 4097, 16 of 272: 400 and 276; 36 random sizes where
+// this is chosen, 0.99 to 1.42 times as fast, 1.2 in the middle).  The least of these
+// estimates, in us, fitted to sweeps over tiles and splits (what they give | what was
+// measured):
 //      rows x out x cols      256 / 1     256 / split     128 / 1     128 / split
 //   8192 x 4096 x  4096      223 | 225    272 | 255 (2)    282 | 279    332 | 326 (2)
 //   4096 x 1280 x  5120      118 | 107     81 |  72 (2)     74 |  75     97 |  93 (2)

@@ -302,3 +302,24 @@ def test_weight_grad_no_rows_of_many_elements():
     empty = lambda cols, dtype: torch.empty(0, cols, dtype=dtype, device=DEV)
     z.zero_act8_weight_grad(empty(n, torch.bfloat16), empty(n, torch.uint8), empty(n // 32, torch.uint8), d_w)
     assert not any(bool(rows.any()) for rows in d_w.split(4096))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,out,cols", [(425, 4795, 6872), (355, 3561, 4716), (2050, 4100, 4200)])
+def test_weight_grad_whole_and_shared_tiles(dtype, rows, out, cols):
+    """Outputs of a little more than whole rounds of tiles: the last tiles' rows are
+    shared by several workgroups, the others' are not."""
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    for accumulate in (False, True):
+        d_y, codes, scales = whole_numbers(g, rows, out, cols)
+        want = d_y.double().T @ act8_ref.unpack_values(codes, scales).to(DEV)
+        buf, d_w = rows_of(out, cols, TYPES[dtype], cols + 3 if accumulate else None, 0)
+        if accumulate:
+            base = torch.randint(-9, 10, (out, cols), generator=g, device=DEV)
+            d_w.copy_(base)
+            want = want + base
+        ws = workspace(rows, out, cols)
+        assert 0 < ws.numel() < 4 * out * cols   # the parts of some tiles only
+        z.zero_act8_weight_grad(d_y, codes, scales, d_w, accumulate=accumulate, workspace=ws)
+        same(d_w, want.to(TYPES[dtype]).cpu())
+        assert bool((outside(buf, d_w) == KEPT).all())
