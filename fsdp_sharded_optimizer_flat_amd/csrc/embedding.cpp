@@ -16,10 +16,10 @@ struct Workspace {
     int64_t chunk_key = 0, chunk_row = 0, samples = -1, key = 0, row = 0, parts = 0, bytes = 0;
     int32_t chunk = 0, segment = 0, segments = 0, columns = 0;
 };
-Workspace workspace_layout(int64_t rows, int64_t hidden, int32_t chunk)
+Workspace workspace_layout(int64_t rows, int64_t hidden)
 {
     Workspace w;
-    w.chunk = chunk;
+    w.chunk = embedding_chunk(rows);
     w.segment = embedding_segment(rows, hidden);
     w.segments = (int32_t)((rows + w.segment - 1) / w.segment);
     w.columns = (int32_t)((hidden + 7) / 8 * 8);
@@ -29,7 +29,8 @@ Workspace workspace_layout(int64_t rows, int64_t hidden, int32_t chunk)
     w.chunk_row = at, at += list;
     w.key = w.chunk_key, w.row = w.chunk_row;
     if (rows > w.chunk) {
-        w.samples = at, at += (rows + w.chunk - 1) / w.chunk * kSamples * 4;
+        // (of small chunks: more rows never need less)
+        w.samples = at, at += (rows + kSortChunk - 1) / kSortChunk * kSamples * 4;
         w.key = at, at += list;
         w.row = at, at += list;
     }
@@ -94,9 +95,11 @@ extern "C" zero_status zero_embedding_grad_workspace_bytes(int64_t rows, int64_t
         return ZERO_EINVAL;
     if (zero_status s = check_sizes(rows, vocab, hidden, ZERO_MAX_EMBEDDING_ROWS))
         return s;
-    // the call chooses by more than these sizes
-    *bytes = (size_t)std::max(workspace_layout(rows, hidden, kSortChunk).bytes,
-                              workspace_layout(rows, hidden, kMaxSortChunk).bytes);
+    // longer segments have fewer parts: what serves these rows serves fewer of them too
+    int64_t need = workspace_layout(rows, hidden).bytes;
+    for (const int64_t work : kSegmentWork)
+        need = std::max(need, workspace_layout(std::min(rows, work / embedding_slabs(hidden)), hidden).bytes);
+    *bytes = (size_t)need;
     return ZERO_OK;
 }
 
@@ -116,8 +119,7 @@ extern "C" zero_status zero_embedding_grad(const void *d_out, int32_t dtype, int
         return ZERO_EINVAL;
     if (!stride_fits(rows, row_stride) || !stride_fits(vocab, table_stride))
         return ZERO_ERANGE;
-    const int64_t cleared = accumulate ? 0 : vocab * hidden * esize(table_dtype);
-    const Workspace w = workspace_layout(rows, hidden, embedding_chunk(rows, cleared));
+    const Workspace w = workspace_layout(rows, hidden);
     if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, w.bytes))
         return s;
     const Span in[] = {matrix(d_out, rows, hidden, row_stride, esize(dtype)), vec(tokens, rows, 8)};

@@ -20,16 +20,12 @@ int launch_embedding(const EmbeddingArgs &a, void *stream);
 
 // Tokens one workgroup sorts: powers of two.  Sorting takes 11 us for chunks of 2048
 // and 26 for 8192, putting chunks together 7 us for up to eight of them and 5 more for
-// eight more, so small chunks serve up to 65536 tokens, unless a gradient of 128 MB or
-// more is cleared meanwhile, which takes longer than either (16384 x 4096 bf16 into
-// 128256 rows 238 us with large chunks, 245 with small ones; added to what is there, 76
-// and 67).
+// eight more, so small chunks serve up to 65536 tokens.  Small and large ones, us, tables
+// cleared meanwhile: 8192 x 1280 into 50304 rows of bf16 43 and 50, 32768 x 2048 103 and
+// 118, 16384 x 4096 into 128256 242 and 240; added to what is there 67 and 76.
 constexpr int kSortChunk = 2048, kMaxSortChunk = 8192;
 constexpr int kSamples = 128;   // of a sorted chunk's tokens, at even distances
-inline int32_t embedding_chunk(int64_t rows, int64_t cleared_bytes)
-{
-    return rows > 65536 || cleared_bytes >= int64_t(1) << 27 ? kMaxSortChunk : kSortChunk;
-}
+inline int32_t embedding_chunk(int64_t rows) { return rows > 65536 ? kMaxSortChunk : kSortChunk; }
 
 struct EmbeddingGradArgs {
     const void *d_out;
@@ -48,7 +44,10 @@ struct EmbeddingGradArgs {
 };
 int launch_embedding_grad(const EmbeddingGradArgs &a, void *stream);
 
-// Sorted tokens that one wave adds up.
+// Sorted tokens that one wave adds up: more where rows times slabs of 512 columns exceed
+// each of these.
+constexpr int64_t kSegmentWork[] = {16384, 65536};
+inline int64_t embedding_slabs(int64_t hidden) { return (hidden + 511) / 512; }
 int32_t embedding_segment(int64_t rows, int64_t hidden);
 
 }  // namespace zero

@@ -12,7 +12,7 @@
 // The lookup is bound by memory (20001 rows of 1280, binary32 to bf16: 154 MB in 17.7
 // us of kernel).  So is the gradient of a whole table, by its clearing: 16384 rows of 4096 into
 // 128256 of bf16 take 155 us to clear 1.05 GB (6.8 TB/s, with the sorting behind it),
-// 8.5 to put the sorted chunks together, 68 for the sums (which wait for the cleared
+// 9.3 to put the sorted chunks together, 68 for the sums (which wait for the cleared
 // lines to be written back: the whole call takes 67 where the gradient is added to what
 // is there) and 10 for the runs of several segments.  Small ones are bound by their
 // launches' latencies: 1024 rows of 1280 into 50304 take 18 us to clear, 6.6 and 4.1.
@@ -501,8 +501,9 @@ void embedding_grad_of(const EmbeddingGradArgs &a, hipStream_t st)
 // Up to 32 rows are one segment, without a join.
 int32_t embedding_segment(int64_t rows, int64_t hidden)
 {
-    const int64_t work = rows * ((hidden + kOct * kWave - 1) / (kOct * kWave));
-    return rows <= 32 || work > 65536 ? 32 : work > 16384 ? 16 : 8;
+    static_assert(kOct * kWave == 512, "a slab");
+    const int64_t work = rows * embedding_slabs(hidden);
+    return rows <= 32 || work > kSegmentWork[1] ? 32 : work > kSegmentWork[0] ? 16 : 8;
 }
 
 int launch_embedding(const EmbeddingArgs &a, void *stream)

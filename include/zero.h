@@ -799,8 +799,8 @@ zero_status zero_embedding(const void *table, int32_t dtype, int64_t vocab, int6
                            int64_t row_stride, const int64_t *tokens, int64_t rows, float scale,
                            void *out, int32_t out_dtype, int64_t out_stride, void *stream);
 
-/* Workspace bytes that are enough for the gradient call of these sizes (16-byte
- * aligned device memory). */
+/* Workspace bytes that are enough for the gradient call of these sizes and for fewer
+ * rows (16-byte aligned device memory). */
 zero_status zero_embedding_grad_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden,
                                                 size_t *bytes);
 

@@ -83,3 +83,13 @@ def test_binding_refuses_host_tensors():
         z.zero_embedding_grad(f, t, f)
     with pytest.raises(TypeError):
         z.zero_embedding([[0.0]], t, f)
+
+
+def test_a_workspace_serves_fewer_rows():
+    """Around every change of the sorting and the sums."""
+    for hidden in (5, 512, 1280, 8200):
+        last = 0
+        for rows in (1, 32, 33, 2047, 2048, 2049, 4096, 8191, 8192, 8193, 65535, 65536, 65537, 70000, (1 << 20) - 1, 1 << 20):
+            now = z.zero_embedding_grad_workspace_bytes(rows, 1000, hidden)
+            assert now >= last, (hidden, rows)
+            last = now

@@ -291,3 +291,35 @@ def test_offsets_past_32_bits():
     out = torch.empty(4, hidden, dtype=torch.bfloat16, device=DEV)
     z.zero_embedding(table, tokens, out)
     assert torch.equal(out, table[tokens])
+
+
+@pytest.mark.parametrize("dst", TYPES)
+@pytest.mark.parametrize("rows,hidden,vocab,gap", [(1, 1280, 128001, 0), (3000, 701, 120011, 3), (2049, 8200, 23000, 0),
+                                                   (20000, 64, 1 << 20, 5), (2500, 5, 1 << 20, 500), (700, 2, 1 << 20, 150)])
+def test_grad_of_a_large_table(dst, rows, hidden, vocab, gap):
+    """Tables of which a part is cleared before the sums and the rest, but for the rows
+    that tokens name, beside them: whole numbers, so that every sum is exact, tokens at
+    both ends of the table, in neighbouring rows and many times."""
+    g = torch.Generator(device=DEV).manual_seed(rows + hidden)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    tokens[rows // 2:] = vocab - 1 - torch.arange(rows - rows // 2, device=DEV) // 2
+    if rows > 100:
+        tokens[:40] = vocab - 700
+        tokens[40:44] = torch.tensor([0, -1, vocab, vocab + 9], device=DEV)
+    x = torch.randint(-3, 4, (rows, hidden), generator=g, device=DEV).to(torch.bfloat16)
+    buf, d_table = rows_of(vocab, hidden, TYPES[dst], hidden + gap, 1 if gap else 0)
+    d_table.fill_(float("nan"))
+    ok = (tokens >= 0) & (tokens < vocab)
+    named, which = tokens[ok].unique(return_inverse=True)
+    want = torch.zeros(named.numel(), hidden, device=DEV).index_add_(0, which, x[ok].float())
+    ws = workspace(rows, vocab, hidden)
+    for _ in range(2):
+        z.zero_embedding_grad(x, tokens, d_table, workspace=ws)
+        assert torch.equal(d_table[named], want.to(TYPES[dst]))
+        others = torch.ones(vocab, dtype=torch.bool, device=DEV)
+        others[named] = False
+        for part, on in zip(d_table.split(1 << 15), others.split(1 << 15)):
+            assert bool((part[on] == 0).all())
+        if gap:
+            assert bool((outside(buf, d_table) == KEPT).all())
+        d_table[:, :].fill_(float("nan"))
