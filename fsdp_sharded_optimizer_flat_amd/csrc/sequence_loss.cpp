@@ -71,7 +71,7 @@ extern "C" zero_status zero_policy_loss(const float *logprob, const float *old_l
     if (zero_status s = check_sequences(tokens, n_tokens, offsets, n_seqs, mode, kPolicyShort, &a.seq))
         return s;
     if (!within(clip_low, 0.0, 1.0) || !within(clip_high, 0.0, INFINITY) ||
-        !within(kl_coef, 0.0, 1.7e308) || (!ref_logprob && (kl || (kl_coef != 0.0 && n_tokens > 0))))
+        !within(kl_coef, 0.0, 1.7e308) || (!ref_logprob && n_tokens > 0 && (kl || kl_coef != 0.0)))
         return ZERO_EINVAL;
     if (n_seqs > 0 && ((!advantage && (n_tokens > 0 || !per_token)) || (d_logprob && !d_loss) ||
                        (n_tokens > 0 && (!logprob || !old_logprob || (!loss && !kl && !clipped && !d_logprob)))))

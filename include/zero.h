@@ -744,7 +744,8 @@ zero_status zero_distill_fused(const void *logits, int32_t dtype, int64_t rows, 
 zero_status zero_sequence_loss_workspace_bytes(int64_t n_tokens, int64_t n_seqs, size_t *bytes);
 
 /* advantage: one value per position (per_token nonzero, [n_tokens]) or per
- * sequence ([n_seqs]).  ref_logprob may be NULL (then kl is NULL and kl_coef 0).
+ * sequence ([n_seqs]).  ref_logprob may be NULL (then kl is NULL and kl_coef 0, but
+ * where n_tokens is 0).
  * loss, kl, clipped [n_seqs] and d_logprob [n_tokens] may be NULL, not all of
  * them; d_logprob needs d_loss [n_seqs].  0 <= clip_low <= 1, 0 <= clip_high,
  * which may be infinite, 0 <= kl_coef. */

@@ -384,3 +384,23 @@ def test_same_bits_on_another_stream_and_in_graphs():
             assert torch.equal(outs[k], want[k]), (turn, k)
         for k in pouts:
             assert torch.equal(pouts[k], pwant[k]), (turn, k)
+
+
+@pytest.mark.parametrize("b", [2, 300])
+def test_no_positions(b):
+    """Sequences that are all empty, with every output: torch's tensors of no elements
+    have no address."""
+    e, off = torch.empty(0, device=DEV), torch.zeros(b + 1, dtype=torch.int64, device=DEV)
+    tok, up = torch.empty(0, dtype=torch.int64, device=DEV), torch.ones(b, device=DEV)
+    f = lambda n: torch.full((n,), KEPT, device=DEV)
+    for per_token in (True, False):
+        for mode in MODE.values():
+            o = dict(loss=f(b), kl=f(b), clipped=torch.full((b,), 3, dtype=torch.int32, device=DEV))
+            z.zero_policy_loss(e, e, e if per_token else up, off, tokens=tok, ref_logprob=e, per_token=per_token,
+                               kl_coef=0.1, mode=mode, d_loss=up, d_logprob=e, workspace=workspace(0, b), **o)
+            assert all(bool((v == 0).all()) for v in o.values())
+    loss, reward = f(b // 2), f(b)
+    z.zero_preference_loss(e, off, tokens=tok, ref_logprob=e, d_loss=up[:b // 2], loss=loss, reward=reward,
+                           d_logprob=e, workspace=workspace(0, b))
+    close(loss, np.full(b // 2, np.log(2.0)))
+    assert bool((reward == 0).all())

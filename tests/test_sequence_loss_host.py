@@ -103,3 +103,9 @@ def test_binding_refuses_host_tensors():
         z.zero_preference_loss(f, t, loss=f)
     with pytest.raises(TypeError):
         z.zero_policy_loss([0.0], f, f, t, loss=f)
+
+
+def test_a_reference_of_no_positions_may_be_null():
+    assert call("zero_policy_loss", b=0, n=0, ref=None) == z.ZERO_OK
+    assert call("zero_policy_loss", b=0, n=0, ref=None, kl=None) == z.ZERO_OK
+    assert call("zero_policy_loss", n=1, ref=None, coef=0.0) == EINVAL
