@@ -429,7 +429,7 @@ __global__ __launch_bounds__(kBlock) void policy_join_kernel(PolicyArgs a)
 
 // -- preference -----------------------------------------------------------------------
 
-// A pair's loss and its derivative by h.
+// A pair's loss, and `up` times beta times its derivative by h.
 __device__ __forceinline__ double preference_loss(const PreferenceArgs &a, double h)
 {
     if (a.kind == ZERO_PREFER_SIGMOID) {
@@ -443,17 +443,20 @@ __device__ __forceinline__ double preference_loss(const PreferenceArgs &a, doubl
     const double u = (h - 0.5) / a.beta;
     return u * u;
 }
-__device__ __forceinline__ double preference_slope(const PreferenceArgs &a, double h)
+__device__ __forceinline__ double preference_slope(const PreferenceArgs &a, double h, double up)
 {
-    if (a.kind == ZERO_PREFER_SIGMOID) {
+    if (a.kind == ZERO_PREFER_SQUARED)   // beta's square may have no binary64 value
+        return up * (2.0 * (h - 0.5) / a.beta);
+    double slope;
+    if (a.kind == ZERO_PREFER_HINGE) {
+        slope = h >= 1.0 ? 0.0 : h != h ? h : -1.0;
+    } else {
         // 1 / (1 + e^h) = e^-h / (1 + e^-h): of the smaller exponential, which is finite
         const double e = exponential(-fabs(h)).e, less = e / (1.0 + e), more = 1.0 / (1.0 + e);
-        return h >= 0.0 ? a.smoothing * more - (1.0 - a.smoothing) * less
-                        : a.smoothing * less - (1.0 - a.smoothing) * more;
+        slope = h >= 0.0 ? a.smoothing * more - (1.0 - a.smoothing) * less
+                         : a.smoothing * less - (1.0 - a.smoothing) * more;
     }
-    if (a.kind == ZERO_PREFER_HINGE)
-        return h >= 1.0 ? 0.0 : h != h ? h : -1.0;
-    return 2.0 * (h - 0.5) / (a.beta * a.beta);
+    return up * slope * a.beta;
 }
 
 __device__ __forceinline__ unsigned ratio_quad(const PreferenceArgs &a, int64_t t, const Range &r, SequencePart &sum)
@@ -496,7 +499,7 @@ __device__ __forceinline__ float pair_gradient(const PreferenceArgs &a, int64_t 
     }
     if (!a.d_logprob)
         return 0.0f;
-    const double up = (double)a.d_loss[p] * preference_slope(a, h) * a.beta;
+    const double up = preference_slope(a, h, a.d_loss[p]);
     return (float)(of_rejected ? -up * wr : up * wc);
 }
 

@@ -404,3 +404,27 @@ def test_no_positions(b):
                            d_logprob=e, workspace=workspace(0, b))
     close(loss, np.full(b // 2, np.log(2.0)))
     assert bool((reward == 0).all())
+
+
+@pytest.mark.parametrize("lengths", [[30, 20, 25, 10], PAIRS["cut"]])
+def test_preference_squared_of_extreme_beta(lengths):
+    """The derivative is 2 (h - 1/2) / beta, whatever beta's square is: with a beta of
+    10^-170 zero for an upstream of zero, with one of 10^170 twice the difference of the
+    log ratios, (h - 1/2) / beta."""
+    d = make(34, lengths, prompts=0.2)
+    p = len(lengths) // 2
+    d["d_loss"][:] = 0.0
+    o = run_preference(d, kind="squared", beta=1e-170)
+    assert bool((o["d_logprob"] == 0).all()) and bool((o["reward"] == 0).all())
+    d["d_loss"][:] = 1.0
+    o = run_preference(d, kind="squared", beta=1e170)
+    s = [sum(float(d["lp"][t]) - float(d["ref"][t]) for t in q)
+         for q in ref64.targets_of(d["off"], d["tokens"], d["n"])]
+    size = float(np.abs(d["lp"]).sum())
+    want = np.zeros(d["n"])
+    for i in range(p):
+        for b, sign in ((i, 1.0), (i + p, -1.0)):
+            q = ref64.targets_of(d["off"], d["tokens"], d["n"])[b]
+            want[q] = sign * 2.0 * (s[i] - s[i + p])
+    close(o["loss"], (np.array(s[:p]) - np.array(s[p:])) ** 2, 1, size * size, "loss")
+    close(o["d_logprob"], want, 1, size, "d_logprob")
