@@ -96,7 +96,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_kernel(Act8GradArgs a)
     // A tile on its way: chunk i of x' and of d_y in registers.  Rows behind the last
     // are zeros; columns past a row's end may hold the next row's, which reach no
     // output.  FAST: windows that end where the arrays do (what lies past them reads as
-    // zero).  Else a chunk that would reach past its array is read from the array's last
+    // zero, also where the scalar offset alone is past it: tests/test_gpu_act8_windows.py
+    // has NaN there).  Else a chunk that would reach past its array is read from the array's last
     // 16 bytes and shifted to its place before it is stored (settle).
     u32x4 xr[kDepth][XPer], yr[kDepth][YPer];
     unsigned sr[kDepth][XPer];

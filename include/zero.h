@@ -830,8 +830,8 @@ zero_status zero_embedding_grad(const void *d_out, int32_t dtype, int64_t rows, 
  *   zero_act8_unpack        x' = code * scale, rounded to the output's type
  *   zero_act8_weight_grad   d_w[o][c] (+)= sum_r d_y[r][o] x'[r][c]
  *
- * The weight gradient's factors d_y (bf16) and x' (exact in bf16, but for elements
- * below its normal range) are multiplied on the matrix cores, sums are binary32 in an
+ * The weight gradient's factors d_y (bf16) and x' (rounded to bf16: exact but for
+ * elements below its normal range) are multiplied on the matrix cores, sums are binary32 in an
  * order that the sizes alone decide; each element of d_w [out_features][cols] is
  * rounded once to its type, or, with accumulate = 1, added to what is there (one
  * more rounding).
