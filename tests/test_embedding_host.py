@@ -93,3 +93,18 @@ def test_a_workspace_serves_fewer_rows():
             now = z.zero_embedding_grad_workspace_bytes(rows, 1000, hidden)
             assert now >= last, (hidden, rows)
             last = now
+
+
+@pytest.mark.parametrize("hidden", [1, 5, 512, 513, 1280, 4096, 8200, 1 << 20])
+def test_a_workspace_serves_fewer_rows_around_each_change_of_the_segments(hidden):
+    """Segments grow where rows times slabs of 512 columns pass 2^14 and 2^16; longer ones
+    need fewer parts, which must not show in what the query says."""
+    slabs = (hidden + 511) // 512
+    around = {w // slabs + d for w in (1 << 14, 1 << 16) for d in (-1, 0, 1, 2)}
+    around |= {r for w in (1 << 14, 1 << 16) for r in (w // slabs * 2, w // slabs * 2 + 1)}
+    around |= {1, 31, 32, 33, 2048, 2049, 65536, 65537, 1 << 20}
+    last = 0
+    for rows in sorted(r for r in around if 1 <= r <= z.ZERO_MAX_EMBEDDING_ROWS):
+        now = z.zero_embedding_grad_workspace_bytes(rows, 1000, hidden)
+        assert now >= last, (hidden, rows)
+        last = now
