@@ -11,8 +11,8 @@
 // same for both factors and otherwise free: lanes 16 g .. 16 g + 15 hold rows 4 g ..
 // 4 g + 3 and 16 more.
 //
-// Bound by the matrix cores' feeding: 8192 x 14336 x 4096 into bf16 takes 787 to 860 us,
-// 1.12 to 1.22 PFLOP/s, as the clock goes, where the library's product of two bf16 matrices takes 1010 to
+// Bound by the matrix cores' feeding: 8192 x 14336 x 4096 into bf16 takes 774 to 860 us,
+// 1.12 to 1.24 PFLOP/s, as the clock goes, where the library's product of two bf16 matrices takes 950 to
 // 1040; 8192 x 4096 x 4096 225 (230), with products under way in 51 % of the cycles and
 // LDS busy in 32 %.  Small outputs have too few tiles for the device and are bound by a
 // tile's latency: 1023 x 1280 x 1280 takes 15.7 us on 100 compute units (library: 20).

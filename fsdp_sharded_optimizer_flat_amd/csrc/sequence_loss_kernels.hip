@@ -214,10 +214,10 @@ __device__ __forceinline__ SequencePart parts_of(const Sequences &s, int64_t b, 
 // -- policy ---------------------------------------------------------------------------
 
 // e^x, e^x - 1 and e^x - 1 - x: x = n ln 2 + f, |f| <= ln(2) / 2, and the exponential's
-// series in f to its 11th power, whose rest is below 2^-47 (of the results, which are
-// rounded to binary32 in the end: 2^-24).  A third of the library functions' time, which
-// weighed more than the memory's.  Where n = 0 the last two are the series without its
-// first terms, and nothing cancels.
+// series in f to its 11th power.  The rest is below 2^-46 of e^x, 2^-44 of e^x - 1 and
+// 2^-42 of e^x - 1 - x, which are rounded to binary32 in the end (2^-24).  A third of the
+// library functions' time, which weighed more than the memory's.  Where n = 0 the last two
+// are the series without its first terms, and nothing cancels.
 struct Exponential {
     double e, less1, rest;
 };

@@ -782,9 +782,10 @@ zero_status zero_preference_loss(const float *logprob, const float *ref_logprob,
  * Tables and activations are ZERO_F32 or ZERO_BF16 each, in rows of `hidden`
  * elements, row r at base + r * stride; elements past a row's hidden stay as they
  * are.  Sums are binary32, of rows in ascending order, a token's many rows in parts
- * (the same call gives the same bits); each output is rounded once.  accumulate = 0 writes the
- * whole of d_table, zeros where no token names a row; accumulate = 1 adds to the
- * rows that tokens name (one more rounding) and leaves the others as they are.
+ * (the same call gives the same bits).  So is the product with scale, which is rounded to
+ * binary32 (not where scale is a power of two) and then to the output's type.  accumulate
+ * = 0 writes the whole of d_table, zeros where no token names a row; accumulate = 1 adds to
+ * the rows that tokens name (in binary32, one more rounding) and leaves the others as they are.
  *
  * Device pointers, aligned to their elements; outputs must not overlap inputs.
  * Async on `stream`, no allocation, capturable; a workspace serves one call at a

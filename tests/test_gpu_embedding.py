@@ -297,9 +297,9 @@ def test_offsets_past_32_bits():
 @pytest.mark.parametrize("rows,hidden,vocab,gap", [(1, 1280, 128001, 0), (3000, 701, 120011, 3), (2049, 8200, 23000, 0),
                                                    (20000, 64, 1 << 20, 5), (2500, 5, 1 << 20, 500), (700, 2, 1 << 20, 150)])
 def test_grad_of_a_large_table(dst, rows, hidden, vocab, gap):
-    """Tables of which a part is cleared before the sums and the rest, but for the rows
-    that tokens name, beside them: whole numbers, so that every sum is exact, tokens at
-    both ends of the table, in neighbouring rows and many times."""
+    """Tables cleared by many workgroups, as one run of elements or row by row (gaps), that
+    begin at and off 16 bytes and hold NaN before: whole numbers, so that every sum is exact,
+    tokens at both ends of the table, in neighbouring rows and many times."""
     g = torch.Generator(device=DEV).manual_seed(rows + hidden)
     tokens = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
     tokens[rows // 2:] = vocab - 1 - torch.arange(rows - rows // 2, device=DEV) // 2
