@@ -1092,7 +1092,8 @@ def _on_current_device(t, what: str) -> int:
 
 def zero_sequence_loss_workspace_bytes(n_tokens: int, n_seqs: int) -> int:
     """Bytes of a workspace (a device tensor) that is enough for either sequence
-    loss on ``n_tokens`` positions of ``n_seqs`` sequences (pairs count twice)."""
+    loss on ``n_tokens`` positions of ``n_seqs`` sequences (pairs count twice), and
+    on fewer of both."""
     b = sz()
     _check(_zero_sequence_loss_workspace_bytes(n_tokens, n_seqs, C.byref(b)),
            "zero_sequence_loss_workspace_bytes")

@@ -3,6 +3,7 @@
 // device work.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "call_check.h"
@@ -24,7 +25,26 @@ zero_status check_sequences(const int64_t *tokens, int64_t n_tokens, const int64
     return ZERO_OK;
 }
 
-int64_t parts_bytes(const SequenceCut &c) { return c.slots * (int64_t)sizeof(SequencePart); }
+int64_t parts_bytes(int64_t slots) { return slots * (int64_t)sizeof(SequencePart); }
+
+// The most slots of a call with up to n_tokens positions of up to n_seqs sequences.
+int64_t most_slots(int64_t n_tokens, int64_t n_seqs)
+{
+    if (n_tokens <= kSequenceShort) {
+        // a policy loss is cut if its sequences have more than kPolicyShort positions
+        const int64_t n = std::min(n_seqs, n_tokens / (kPolicyShort + 1));
+        return n > 0 ? (n_tokens >> kRoundShift) + n : 0;
+    }
+    // tiles of 2^shift are for as many positions as an average of 1024 tiles allows
+    int64_t most = 0;
+    for (int32_t shift = kRoundShift; n_seqs > 0; shift += 2) {
+        const int64_t n = std::min(n_tokens, (((int64_t)1024 << shift) + 1) * n_seqs - 1);
+        most = std::max(most, (n >> shift) + n_seqs);
+        if (n == n_tokens)
+            break;
+    }
+    return most;
+}
 
 // NaN is out of every range.
 bool within(double x, double lo, double hi) { return x >= lo && x <= hi; }
@@ -54,7 +74,7 @@ extern "C" zero_status zero_sequence_loss_workspace_bytes(int64_t n_tokens, int6
         return ZERO_EINVAL;
     if (n_tokens > ZERO_MAX_LOSS_ROWS || n_seqs > ZERO_MAX_SEQUENCES)
         return ZERO_ERANGE;
-    *bytes = (size_t)parts_bytes(sequence_cut(n_tokens, n_seqs, kPolicyShort));
+    *bytes = (size_t)parts_bytes(most_slots(n_tokens, n_seqs));
     return ZERO_OK;
 }
 
@@ -76,7 +96,7 @@ extern "C" zero_status zero_policy_loss(const float *logprob, const float *old_l
     if (n_seqs > 0 && ((!advantage && (n_tokens > 0 || !per_token)) || (d_logprob && !d_loss) ||
                        (n_tokens > 0 && (!logprob || !old_logprob || (!loss && !kl && !clipped && !d_logprob)))))
         return ZERO_EINVAL;
-    const int64_t need = parts_bytes(a.seq.cut);
+    const int64_t need = parts_bytes(a.seq.cut.slots);
     if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, need))
         return s;
     const Span in[] = {vec(logprob, n_tokens, 4), vec(old_logprob, n_tokens, 4),
@@ -128,7 +148,7 @@ extern "C" zero_status zero_preference_loss(const float *logprob, const float *r
         return ZERO_EINVAL;
     if (n_pairs > 0 && ((d_logprob && !d_loss) || (n_tokens > 0 && (!logprob || (!loss && !reward && !d_logprob)))))
         return ZERO_EINVAL;
-    const int64_t need = parts_bytes(a.seq.cut);
+    const int64_t need = parts_bytes(a.seq.cut.slots);
     if (zero_status s = check_workspace_bytes(workspace, workspace_bytes, need))
         return s;
     const Span in[] = {vec(logprob, n_tokens, 4), vec(ref_logprob, n_tokens, 4), vec(tokens, n_tokens, 8),

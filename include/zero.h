@@ -739,8 +739,8 @@ zero_status zero_distill_fused(const void *logits, int32_t dtype, int64_t rows, 
 #define ZERO_PREFER_SQUARED 2
 
 /* Workspace bytes that are enough for either call below on n_tokens positions
- * of n_seqs sequences (16-byte aligned device memory; where this is 0 a NULL
- * workspace). */
+ * of n_seqs sequences and on fewer of both (16-byte aligned device memory; where
+ * this is 0 a NULL workspace). */
 zero_status zero_sequence_loss_workspace_bytes(int64_t n_tokens, int64_t n_seqs, size_t *bytes);
 
 /* advantage: one value per position (per_token nonzero, [n_tokens]) or per

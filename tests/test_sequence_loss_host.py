@@ -109,3 +109,42 @@ def test_a_reference_of_no_positions_may_be_null():
     assert call("zero_policy_loss", b=0, n=0, ref=None) == z.ZERO_OK
     assert call("zero_policy_loss", b=0, n=0, ref=None, kl=None) == z.ZERO_OK
     assert call("zero_policy_loss", n=1, ref=None, coef=0.0) == EINVAL
+
+
+def test_a_workspace_serves_fewer_positions_and_sequences():
+    """Around each change of the tiles (at 1024 tiles a sequence of 2^8, 2^10 ... positions)
+    and of the single launch's sizes."""
+    most = z.ZERO_MAX_LOSS_ROWS
+    for b in (1, 2, 3, 300, 4097, 1 << 20):
+        around = {min(most, max(0, n * b + d)) for n in (2048, 1 << 18, 1 << 20, 1 << 22, 1 << 24, 1 << 26, 1 << 28)
+                  for d in (-1, 0, 1, b - 1, b, b + 1)} | {0, 1, 16384, 16385, 100000, most}
+        last = 0
+        for n in sorted(around):
+            now = z.zero_sequence_loss_workspace_bytes(n, b)
+            assert now >= last, (n, b)
+            last = now
+    for n in (1000, 5000, 16384, 16385, 1 << 20, 300_000_001, most):
+        around = {max(1, min(1 << 20, (n >> k) + d)) for k in (11, 18, 20, 22, 24, 26, 28) for d in (-1, 0, 1)}
+        last = 0
+        for b in sorted(around | {1, 2, 3, 1 << 20}):
+            now = z.zero_sequence_loss_workspace_bytes(n, b)
+            assert now >= last, (n, b)
+            last = now
+
+
+@pytest.mark.parametrize("entry", BOTH)
+def test_a_workspace_is_enough(entry):
+    """A call with what the query says for its sizes or more is not refused for it, but
+    for the overlap that it has besides; one with less is."""
+    far = {k: BASE + i * (1 << 40) for i, k in enumerate(A)}
+    sizes = [(n, b) for n in (0, 1, 2048, 2049, 4098, 4099, 9000, 16383, 16384, 16385, 300000, 524288, 524291, 1 << 21,
+                              40_000_000, (1 << 31) - 1) for b in (2, 4, 6, 8, 64, 300, 1 << 20)]
+    cut = 0
+    for n, b in sizes:
+        clash = far | dict(n=n, b=b, kl=far["loss"], reward=far["loss"])
+        for most in sizes:
+            if most[0] >= n and most[1] >= b:
+                wb = z.zero_sequence_loss_workspace_bytes(*most)
+                assert call(entry, **clash, wb=wb) == EINVAL, (n, b, most)
+        cut += call(entry, **clash, wb=23) == ENOSPC
+    assert cut > 20
