@@ -1193,7 +1193,7 @@ def zero_embedding(table, tokens, out, *, scale: float = 1.0, stream=None):
 
 def zero_embedding_grad_workspace_bytes(rows: int, vocab: int, hidden: int) -> int:
     """Bytes of a workspace (a device tensor) that is enough for
-    zero_embedding_grad of these sizes."""
+    zero_embedding_grad of these sizes and of fewer rows."""
     b = sz()
     _check(_zero_embedding_grad_workspace_bytes(rows, vocab, hidden, C.byref(b)),
            "zero_embedding_grad_workspace_bytes")
@@ -1248,7 +1248,7 @@ def zero_act8_unpack(codes, scales, x, stream=None):
 
 def zero_act8_weight_grad_workspace_bytes(rows: int, out_features: int, cols: int) -> int:
     """Bytes of a workspace (a device tensor) that is enough for
-    zero_act8_weight_grad of these sizes."""
+    zero_act8_weight_grad of these sizes (fewer rows may need more)."""
     b = sz()
     _check(_zero_act8_weight_grad_workspace_bytes(rows, out_features, cols, C.byref(b)),
            "zero_act8_weight_grad_workspace_bytes")

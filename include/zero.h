@@ -854,7 +854,8 @@ zero_status zero_act8_unpack(const uint8_t *codes, const uint8_t *scales, int64_
                              void *stream);
 
 /* Workspace bytes that are enough for the weight gradient of these sizes
- * (16-byte aligned device memory; where this is 0 a NULL workspace). */
+ * (16-byte aligned device memory; where this is 0 a NULL workspace).  Fewer rows may
+ * need more, because they are split differently: ask for each number of rows. */
 zero_status zero_act8_weight_grad_workspace_bytes(int64_t rows, int64_t out_features,
                                                   int64_t cols, size_t *bytes);
 
