@@ -11,7 +11,7 @@
 // Short calls are bound by their way to the device: 1 sequence of 1024 positions is 3.6
 // us of kernel and 8.2 us from call to call.  Long ones by a wave's chain of search, loads,
 // terms and sums: 300 sequences of 3400 with a KL term take 10.4 us for the terms, two
-// exponentials a target in some 90 binary64 instructions, and 5.9 to scale the
+// exponentials a target in some 90 binary64 instructions, and 5.6 to scale the
 // gradients, where the memory's traffic is 4.3 us; 128 pairs of sequences of 4000, a
 // subtraction a target, 4.7 and 7.1 of 3.1.
 //
